@@ -15,7 +15,10 @@
  *     assembled: y = sum over elements of rho_e K0 applied to the element's
  *     24 dofs (spmv_plan_create_fem).
  * x is fp32 for fp32 values and fp16 otherwise; y is always fp32 and every
- * product is accumulated in fp32.
+ * product is accumulated in fp32. Around the products of pruned language
+ * models it also has the layer norm (with its gradient), the low-rank
+ * adapters of many requests and the logits' penalties, biases and grammar
+ * masks ("Operators around a pruned layer", at the end).
  *
  * Sources (web pages, by title and section):
  *   [CSR]   "CUDA CSR SpMV optimisation" (codechina.net), section 2.1: the CSR
@@ -76,7 +79,9 @@ typedef enum spmv_status {
                                     device status word (bounded wait expired) */
 } spmv_status;
 
-typedef enum spmv_dtype { SPMV_F32 = 0, SPMV_F16 = 1 } spmv_dtype;
+/* SPMV_BF16 is taken by the operators around a pruned layer (below) only;
+ * matrices and their vectors are fp32 or fp16. */
+typedef enum spmv_dtype { SPMV_F32 = 0, SPMV_F16 = 1, SPMV_BF16 = 2 } spmv_dtype;
 
 typedef enum spmv_format {
   SPMV_FORMAT_CSR = 0,     /* [CSR] section 2.1                               */
@@ -504,6 +509,151 @@ spmv_status spmv_noalloc_check(void);
  * the cudaFree counterpart of [CSR] 2.2's one-time upload. NULL is
  * accepted. */
 void spmv_plan_destroy(spmv_plan* plan);
+
+/* ------------------------------------------------------------------------
+ * Operators around a pruned layer.
+ *
+ * What a language model with pruned weights computes at the two ends of a
+ * product y = A x and beside it: the layer norm that turns the fp32 residual
+ * stream into the fp16 x of the next product (with its gradient, for the
+ * recovery training of the norms after pruning), the low-rank adapters of
+ * many requests beside a shared projection, and the penalties, biases and
+ * grammar masks on the logits that an output head's product gives. The pages
+ * have no counterpart: each call states its formula.
+ *
+ * Conventions, besides those above:
+ *   - Every data pointer is CUDA device memory of the current device; calls
+ *     are asynchronous on `stream`, allocate nothing, keep nothing between
+ *     calls and may be captured into a CUDA graph. Calls on different
+ *     streams are independent as long as they share no output or workspace.
+ *   - Matrices are row-major with a row stride in ELEMENTS (columns are
+ *     contiguous). An input's stride may be 0 (one row used for all); an
+ *     output's is at least its number of columns. Pointers are aligned to
+ *     their element size; 16-byte aligned rows are the fastest.
+ *   - Inputs and outputs do not overlap unless a call says so.
+ *   - Sums, statistics and products are held in fp32, and each output is
+ *     rounded to its type once. Runs are deterministic: the same inputs give
+ *     the same bits.
+ * ------------------------------------------------------------------------ */
+
+/* Layer norm of each row: with mean = sum_j x_j / n_cols and
+ * rstd = 1 / sqrt(sum_j (x_j - mean)^2 / n_cols + eps),
+ *   y_j = (x_j - mean) * rstd * weight_j + bias_j.
+ * x: n_rows x n_cols of x_dtype; y: of y_dtype, which is x_dtype, or any type
+ * when x is fp32. weight, bias: n_cols of param_dtype (any type), either may
+ * be NULL (1 and 0). mean_out, rstd_out: n_rows fp32 each, or NULL. y may be
+ * x itself (same pointer, type and stride). Errors: INVALID_ARG (sizes,
+ * n_cols < 1, null or misaligned pointers, strides, overlaps, eps negative or
+ * not finite), UNSUPPORTED (x_dtype / y_dtype pair), TOO_LARGE (n_cols above
+ * 2^31 - 4097 or rows past 63 bits), CUDA. */
+spmv_status spmv_layernorm(int64_t n_rows, int32_t n_cols, const void* x, spmv_dtype x_dtype,
+                           int64_t x_stride, const void* weight, const void* bias,
+                           spmv_dtype param_dtype, float eps, void* y, spmv_dtype y_dtype,
+                           int64_t y_stride, float* mean_out, float* rstd_out, void* stream);
+
+/* Bytes of workspace that spmv_layernorm_backward needs for these sizes (0
+ * for sizes it refuses, and where neither dweight nor dbias is wanted). */
+int64_t spmv_layernorm_backward_workspace(int64_t n_rows, int32_t n_cols, int32_t want_params);
+
+/* Gradient of spmv_layernorm. With xhat = (x - mean) * rstd and
+ * g = dy * weight, per row
+ *   dx = rstd * (g - sum(g) / n_cols - xhat * sum(g * xhat) / n_cols),
+ * and over the rows dweight = sum(dy * xhat), dbias = sum(dy).
+ * dy: the gradient of y, of the forward call's y_dtype; mean, rstd: the
+ * forward call's. dx: of x_dtype; dweight, dbias: n_cols of param_dtype,
+ * overwritten (zeros when n_rows is 0). Each of dx, dweight and dbias may be
+ * NULL (not wanted); weight may be NULL (1). dx may be dy itself (same
+ * pointer, type and stride). workspace: 16-byte aligned device memory of at
+ * least spmv_layernorm_backward_workspace bytes (NULL when that is 0); its
+ * contents need no initialisation and mean nothing afterwards.
+ * Errors: as spmv_layernorm, and INVALID_ARG for a workspace that is too
+ * small. */
+spmv_status spmv_layernorm_backward(int64_t n_rows, int32_t n_cols, const void* dy,
+                                    spmv_dtype dy_dtype, int64_t dy_stride, const void* x,
+                                    spmv_dtype x_dtype, int64_t x_stride, const void* weight,
+                                    spmv_dtype param_dtype, const float* mean, const float* rstd,
+                                    void* dx, int64_t dx_stride, void* dweight, void* dbias,
+                                    void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Largest rank and number of slots of spmv_adapters_run. */
+#define SPMV_ADAPTER_MAX_RANK 256
+#define SPMV_ADAPTER_MAX_SLOTS 16384
+
+/* Bytes of workspace that spmv_adapters_run needs for these sizes (may be 0;
+ * 0 for sizes it refuses). */
+int64_t spmv_adapters_workspace(int32_t n_tokens, int32_t n_slots, int32_t rank);
+
+/* Low-rank adapters of many requests beside a shared projection. Token t of
+ * slot s = slot_ids[t] gets
+ *   y_t = base_t + scales[s] * B_s (A_s x_t),
+ * and a token whose slot id is outside [0, n_slots) gets y_t = base_t.
+ * x: n_tokens x n_in of `dtype` (fp16 or bf16). a: n_slots x rank x n_in and
+ * b: n_slots x n_out x rank, both contiguous and of `dtype`. ranks: n_slots
+ * int32 or NULL: slot s uses the first ranks[s] rows of A_s and columns of
+ * B_s (clamped to [0, rank]; the others are not read); NULL: all. scales:
+ * n_slots fp32 or NULL (1). base: n_tokens x n_out of y_dtype, the shared
+ * projection's output (spmv_run's y of each token), or NULL (0); y: of
+ * y_dtype, which is fp32 or `dtype`. y may be base itself (same pointer and
+ * stride). A_s x_t and the product with B_s are held in fp32. workspace:
+ * 16-byte aligned device memory of at least spmv_adapters_workspace bytes
+ * (NULL when that is 0); no initialisation, no meaning afterwards.
+ * Errors: INVALID_ARG (sizes, null or misaligned pointers, strides,
+ * overlaps, workspace too small), UNSUPPORTED (types), TOO_LARGE (rank or
+ * n_slots above the limits), CUDA. */
+spmv_status spmv_adapters_run(int32_t n_tokens, int32_t n_in, int32_t n_out, int32_t n_slots,
+                              int32_t rank, spmv_dtype dtype, const void* x, int64_t x_stride,
+                              const void* a, const void* b, const int32_t* slot_ids,
+                              const int32_t* ranks, const float* scales, const void* base,
+                              int64_t base_stride, void* y, spmv_dtype y_dtype, int64_t y_stride,
+                              void* workspace, int64_t workspace_bytes, void* stream);
+
+/* What spmv_logits_process does to each request's logits (device pointers
+ * except for the struct itself, which is read during the call only; zeroed
+ * fields switch their step off). Lists of a request i are
+ * list[offsets[i] .. offsets[i + 1]), offsets being n_requests + 1
+ * non-decreasing int64 on the device. */
+typedef struct spmv_logits {
+  int32_t n_requests;
+  int32_t vocab;
+  const void* logits;          /* n_requests x vocab of `dtype`              */
+  int64_t stride;
+  void* out;                   /* n_requests x vocab of `out_dtype`          */
+  int64_t out_stride;
+  spmv_dtype dtype;            /* any type                                   */
+  spmv_dtype out_dtype;        /* fp32, or dtype                             */
+  const int32_t* prompt_tokens;   /* tokens of each request's prompt         */
+  const int64_t* prompt_offsets;
+  const int32_t* output_tokens;   /* tokens generated so far                 */
+  const int64_t* output_offsets;
+  const float* repetition;     /* per request; NULL: 1                       */
+  const float* frequency;      /* per request; NULL: 0                       */
+  const float* presence;       /* per request; NULL: 0                       */
+  const int32_t* bias_tokens;  /* lists of (token, bias)                     */
+  const float* bias_values;
+  const int64_t* bias_offsets;
+  const uint32_t* mask;        /* n_masks rows of allowed-token bits: bit    */
+  int64_t mask_stride;         /*   v % 32 of word v / 32; stride in words   */
+  const int32_t* mask_rows;    /* mask row of each request, outside          */
+  int32_t n_masks;             /*   [0, n_masks): none; NULL: row i          */
+  int32_t reserved;
+} spmv_logits;
+
+/* Penalties, biases and grammar masks on logits. For request i and token v,
+ * with l the logit, n the number of times v stands among the request's
+ * output tokens, and seen true when v stands among its prompt or output
+ * tokens, in this order and in fp32:
+ *   seen:  l = l > 0 ? l / repetition[i] : l * repetition[i];
+ *   n > 0: l = l - frequency[i] * n - presence[i];
+ *   v listed among the biases: l = l + (the sum of v's biases in list order);
+ *   v not allowed by the request's mask: l = -inf (whatever it was, NaN
+ *   included).
+ * A request whose mask allows nothing gets -inf everywhere. Tokens of the
+ * lists outside [0, vocab) are ignored, so lists may be padded with -1.
+ * out may be logits itself (same pointer, type and stride). Errors:
+ * INVALID_ARG (sizes, null or misaligned pointers, a list without its
+ * offsets, strides, overlaps), UNSUPPORTED (types), TOO_LARGE (more than
+ * 2^31 - 1 blocks of work), CUDA. */
+spmv_status spmv_logits_process(const spmv_logits* args, void* stream);
 
 #ifdef __cplusplus
 }

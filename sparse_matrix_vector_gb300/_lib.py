@@ -14,11 +14,12 @@ c_i32 = ctypes.c_int32
 c_i64 = ctypes.c_int64
 c_p = ctypes.c_void_p
 
-SPMV_F32, SPMV_F16 = 0, 1
+SPMV_F32, SPMV_F16, SPMV_BF16 = 0, 1, 2
 SPMV_FORMAT_CSR, SPMV_FORMAT_DELTA4, SPMV_FORMAT_DELTA2, SPMV_FORMAT_DELTA8 = 0, 1, 2, 3
 SPMV_FORMAT_DELTA_AUTO, SPMV_FORMAT_SELL, SPMV_FORMAT_AUTO, SPMV_FORMAT_FEM = 4, 5, 6, 7
 SPMV_SELL_C = 32
 SPMV_DELTA_FEWEST_BYTES, SPMV_DELTA_SPARSITY_TABLE = 0, 1
+SPMV_ADAPTER_MAX_RANK, SPMV_ADAPTER_MAX_SLOTS = 256, 16384
 
 STATUS_NAMES = {
     0: "SPMV_OK", 1: "SPMV_ERR_INVALID_ARG", 2: "SPMV_ERR_BAD_ROW_PTR",
@@ -81,6 +82,17 @@ class spmv_plan_info(ctypes.Structure):
                 ("reserved", c_i64 * 5)]
 
 
+class spmv_logits(ctypes.Structure):
+    _fields_ = [("n_requests", c_i32), ("vocab", c_i32), ("logits", c_p), ("stride", c_i64),
+                ("out", c_p), ("out_stride", c_i64), ("dtype", ctypes.c_int),
+                ("out_dtype", ctypes.c_int), ("prompt_tokens", c_p), ("prompt_offsets", c_p),
+                ("output_tokens", c_p), ("output_offsets", c_p), ("repetition", c_p),
+                ("frequency", c_p), ("presence", c_p), ("bias_tokens", c_p),
+                ("bias_values", c_p), ("bias_offsets", c_p), ("mask", c_p),
+                ("mask_stride", c_i64), ("mask_rows", c_p), ("n_masks", c_i32),
+                ("reserved", c_i32)]
+
+
 # name -> (restype, argtypes); every function declared in include/spmv.h
 SIGNATURES = {
     "spmv_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -124,6 +136,18 @@ SIGNATURES = {
     "spmv_checked_build": (c_i32, []),
     "spmv_noalloc_check": (ctypes.c_int, []),
     "spmv_plan_destroy": (None, [c_p]),
+    "spmv_layernorm": (ctypes.c_int, [c_i64, c_i32, c_p, ctypes.c_int, c_i64, c_p, c_p,
+                                      ctypes.c_int, ctypes.c_float, c_p, ctypes.c_int, c_i64,
+                                      c_p, c_p, c_p]),
+    "spmv_layernorm_backward_workspace": (c_i64, [c_i64, c_i32, c_i32]),
+    "spmv_layernorm_backward": (ctypes.c_int, [c_i64, c_i32, c_p, ctypes.c_int, c_i64, c_p,
+                                               ctypes.c_int, c_i64, c_p, ctypes.c_int, c_p, c_p,
+                                               c_p, c_i64, c_p, c_p, c_p, c_i64, c_p]),
+    "spmv_adapters_workspace": (c_i64, [c_i32, c_i32, c_i32]),
+    "spmv_adapters_run": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i32, c_i32, ctypes.c_int, c_p,
+                                         c_i64, c_p, c_p, c_p, c_p, c_p, c_p, c_i64, c_p,
+                                         ctypes.c_int, c_i64, c_p, c_i64, c_p]),
+    "spmv_logits_process": (ctypes.c_int, [ctypes.POINTER(spmv_logits), c_p]),
 }
 
 _lock = threading.Lock()

@@ -1,6 +1,7 @@
 // Layer norm of rows and its gradient (spmv_layernorm,
 // spmv_layernorm_backward).
 #include <climits>
+#include <type_traits>
 
 #include "spmv_device.cuh"
 #include "spmv_types.cuh"
@@ -8,35 +9,99 @@
 namespace spmv {
 namespace {
 
-// Sum over the CTA, in every thread. Fixed order.
+// Sum over the CTA, in every thread, in a fixed order. One barrier; s_red
+// (32 floats) must not be in use by an earlier call when this one starts.
 __device__ __forceinline__ float cta_sum_all(float v, float* s_red) {
-  const float t = cta_sum(v, s_red);
+  v = warp_sum(v);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) s_red[warp] = v;
   __syncthreads();
-  if (threadIdx.x == 0) s_red[0] = t;
-  __syncthreads();
-  const float r = s_red[0];
-  __syncthreads();
-  return r;
+  return warp_sum(lane < (int)(blockDim.x >> 5) ? s_red[lane] : 0.f);
 }
 
-// One row per CTA step; three passes over the row (mean, variance, output).
+// Threads of a CTA that holds a row with `cols` columns per thread.
+constexpr int forward_max_threads(int cols) { return cols == 32 ? 1024 : cols == 16 ? 768 : 512; }
+
+// Forward, rows held in registers. Each row belongs to a group of threads (a
+// warp, or the whole CTA), each thread holding CPT columns of it in vectors of
+// VEC: the row is read once, and mean and variance are taken one after the
+// other (the variance from the centred values: no cancellation).
+template <typename XT, typename YT, int VEC, int CPT, bool WARP>
+__global__ void __launch_bounds__(WARP ? kThreads : forward_max_threads(CPT),
+                                  !WARP && CPT != 32 && CPT != 16 ? 2 : 1)
+layernorm_regs(int64_t n_rows, int n_cols, const XT* x, int64_t xs, const void* w, const void* b,
+               int pt, float eps, YT* y, int64_t ys, float* mean_out, float* rstd_out) {
+  constexpr int NV = CPT / VEC;
+  constexpr int kOut = NV % 2 ? 1 : VEC == 1 ? 4 : 2;  // vectors of y made at a time
+  __shared__ float s_red[2][32];
+  const int group = WARP ? 32 : blockDim.x, me = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int per_cta = WARP ? kWarps : 1;
+  const int first = me * VEC, step = group * VEC;
+  const float inv = 1.f / (float)n_cols;
+  for (int64_t r = (int64_t)blockIdx.x * per_cta + (WARP ? threadIdx.x >> 5 : 0); r < n_rows;
+       r += (int64_t)gridDim.x * per_cta) {
+    const XT* xr = x + r * xs;
+    YT* yr = y + r * ys;
+    Pack<XT, VEC> in[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      in[i] = load_vec<XT, VEC>(xr, first + i * step, n_cols, true);
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) s += first + i * step < n_cols ? to_f32(in[i].v[k]) : 0.f;
+    const float mean = (WARP ? warp_sum(s) : cta_sum_all(s, s_red[0])) * inv;
+    float q = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        const float c = to_f32(in[i].v[k]) - mean;
+        q += first + i * step < n_cols ? c * c : 0.f;
+      }
+    const float rstd = rsqrtf((WARP ? warp_sum(q) : cta_sum_all(q, s_red[1])) * inv + eps);
+#pragma unroll
+    for (int i = 0; i < NV; i += kOut) {
+      float g[kOut][VEC], o[kOut][VEC];
+      load_cols<kOut, VEC>(w, pt, first + i * step, step, n_cols, 1.f, g);
+      load_cols<kOut, VEC>(b, pt, first + i * step, step, n_cols, 0.f, o);
+#pragma unroll
+      for (int h = 0; h < kOut; ++h) {
+        const int c = first + (i + h) * step;
+        Pack<YT, VEC> out;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+          out.v[k] = from_f32<YT>((to_f32(in[i + h].v[k]) - mean) * rstd * g[h][k] + o[h][k]);
+        if (c < n_cols) store_pack<YT, VEC>(yr + c, out);
+      }
+    }
+    if (me == 0) {
+      if (mean_out) mean_out[r] = mean;
+      if (rstd_out) rstd_out[r] = rstd;
+    }
+  }
+}
+
+// Forward, rows too long for registers: one row per CTA step, three passes
+// over it (mean, variance, output), the second and third mostly from L2.
 template <typename XT, typename YT>
 __global__ void __launch_bounds__(kThreads)
 layernorm_rows(int64_t n_rows, int n_cols, const XT* x, int64_t xs, const void* w, const void* b,
                int pt, float eps, YT* y, int64_t ys, float* mean_out, float* rstd_out) {
-  __shared__ float s_red[kWarps];
+  __shared__ float s_red[2][32];
   for (int64_t r = blockIdx.x; r < n_rows; r += gridDim.x) {
     const XT* xr = x + r * xs;
     YT* yr = y + r * ys;
     float s = 0.f;
     for (int j = threadIdx.x; j < n_cols; j += kThreads) s += to_f32(xr[j]);
-    const float mean = cta_sum_all(s, s_red) / (float)n_cols;
+    const float mean = cta_sum_all(s, s_red[0]) / (float)n_cols;
     float q = 0.f;
     for (int j = threadIdx.x; j < n_cols; j += kThreads) {
       const float c = to_f32(xr[j]) - mean;
       q += c * c;
     }
-    const float rstd = rsqrtf(cta_sum_all(q, s_red) / (float)n_cols + eps);
+    const float rstd = rsqrtf(cta_sum_all(q, s_red[1]) / (float)n_cols + eps);
     for (int j = threadIdx.x; j < n_cols; j += kThreads) {
       const float g = w ? load_as_f32(w, pt, j) : 1.f, o = b ? load_as_f32(b, pt, j) : 0.f;
       yr[j] = from_f32<YT>((to_f32(xr[j]) - mean) * rstd * g + o);
@@ -48,68 +113,370 @@ layernorm_rows(int64_t n_rows, int n_cols, const XT* x, int64_t xs, const void* 
   }
 }
 
-// dx, one row per CTA step.
+// This thread's asynchronous copies of 4, 8 or 16 bytes into shared memory,
+// in groups; each thread reads back only what it copied itself, so waiting
+// for its own groups is all the synchronisation there is.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src),
+                 "n"(BYTES)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// Sum of two values over the CTA, in every thread, in a fixed order. One
+// barrier; s_red (32 pairs) must not be in use by an earlier call.
+__device__ __forceinline__ float2 cta_sum2_all(float a, float b, float2* s_red) {
+  a = warp_sum(a);
+  b = warp_sum(b);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) s_red[warp] = make_float2(a, b);
+  __syncthreads();
+  const float2 v = lane < (int)(blockDim.x >> 5) ? s_red[lane] : make_float2(0.f, 0.f);
+  return make_float2(warp_sum(v.x), warp_sum(v.y));
+}
+
 template <typename XT, typename YT>
-__global__ void __launch_bounds__(kThreads)
-layernorm_dx_rows(int64_t n_rows, int n_cols, const YT* dy, int64_t dys, const XT* x, int64_t xs,
-                  const void* w, int pt, const float* mean, const float* rstd, XT* dx,
-                  int64_t dxs) {
-  __shared__ float s_red[kWarps];
-  for (int64_t r = blockIdx.x; r < n_rows; r += gridDim.x) {
-    const float m = mean[r], rs = rstd[r];
-    float sg = 0.f, sgx = 0.f;
-    for (int j = threadIdx.x; j < n_cols; j += kThreads) {
-      const float g = to_f32(dy[r * dys + j]) * (w ? load_as_f32(w, pt, j) : 1.f);
-      sg += g;
-      sgx += g * ((to_f32(x[r * xs + j]) - m) * rs);
+struct BackwardArgs {
+  int64_t n_rows;
+  int n_cols;
+  const YT* dy;
+  int64_t dys;
+  const XT* x;
+  int64_t xs;
+  const void* w;
+  int pt;
+  const float *mean, *rstd;
+  XT* dx;        // or null
+  int64_t dxs;
+  float* part;   // gridDim.x x {dweight, dbias} x n_cols partial sums, or null
+};
+
+// Columns a thread holds of its row; more of them cost registers (two fp32
+// sums per column), so wider groups take fewer threads.
+constexpr int backward_max_threads(int cols) { return cols == 16 ? 768 : 512; }
+
+// Backward, one pass over x and dy: a group of threads (a warp, or the CTA)
+// takes rows in turn, each thread the same CPT columns of every row, whose
+// dweight and dbias it sums in registers. STAGES - 1 rows are on their way
+// into shared memory while one is worked on. STAGES 0: rows that are not
+// 16-byte aligned go element by element, read once from memory and, for dx,
+// once more from the caches.
+template <typename XT, typename YT, int VEC, int CPT, int STAGES, bool WARP, bool W_SMEM>
+__global__ void __launch_bounds__(WARP ? kThreads : backward_max_threads(CPT))
+layernorm_backward_fused(BackwardArgs<XT, YT> p) {
+  constexpr int NV = CPT / VEC;
+  constexpr int kHeld = STAGES > 0 ? NV : 4;  // vectors of x and dy in registers
+  using PX = Pack<XT, VEC>;
+  using PY = Pack<YT, VEC>;
+  extern __shared__ __align__(16) unsigned char s_dyn[];
+  __shared__ float2 s_red[2][32];
+  const int group = WARP ? 32 : blockDim.x, me = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int n = p.n_cols, c0 = me * VEC, dc = group * VEC;
+  const int64_t step = (int64_t)gridDim.x * (WARP ? kWarps : 1);
+  const int64_t first = (int64_t)blockIdx.x * (WARP ? kWarps : 1) + (WARP ? threadIdx.x >> 5 : 0);
+  const float inv = 1.f / (float)n;
+  // ring of stages, vector i of thread t at [stage][i][t]
+  PX* ring_x = reinterpret_cast<PX*>(s_dyn);
+  PY* ring_y = reinterpret_cast<PY*>(s_dyn + (size_t)STAGES * NV * blockDim.x * sizeof(PX));
+  const auto slot = [&](int stage, int i) {
+    return (stage * NV + i) * (int)blockDim.x + (int)threadIdx.x;
+  };
+  const auto fetch = [&](int64_t r, int stage) {
+    if constexpr (STAGES > 0) {
+      if (r < p.n_rows) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = (i * group + me) * VEC;
+          if (c < n) {
+            copy_async<sizeof(PX)>(&ring_x[slot(stage, i)], p.x + r * p.xs + c);
+            copy_async<sizeof(PY)>(&ring_y[slot(stage, i)], p.dy + r * p.dys + c);
+          }
+        }
+      }
+      copy_commit();
     }
-    sg = cta_sum_all(sg, s_red) / (float)n_cols;
-    sgx = cta_sum_all(sgx, s_red) / (float)n_cols;
-    for (int j = threadIdx.x; j < n_cols; j += kThreads) {
-      const float g = to_f32(dy[r * dys + j]) * (w ? load_as_f32(w, pt, j) : 1.f);
-      const float xh = (to_f32(x[r * xs + j]) - m) * rs;
-      dx[r * dxs + j] = from_f32<XT>(rs * (g - sg - xh * sgx));
+  };
+
+  // the weight of this thread's columns: in shared memory for the whole call
+  // where it fits (vector i of thread t at [i][t]; a warp's lanes hold the
+  // same columns in every warp), else read again for every row
+  Pack<float, VEC>* s_w = reinterpret_cast<Pack<float, VEC>*>(
+      s_dyn + (size_t)STAGES * NV * blockDim.x * (sizeof(PX) + sizeof(PY)));
+  if constexpr (W_SMEM) {
+    float g[NV][VEC];
+    load_cols<NV, VEC>(p.w, p.pt, c0, dc, n, 1.f, g);
+    // (warps that share columns write the same values: no barrier needed)
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) s_w[i * group + me].v[k] = g[i][k];
+  }
+  const auto weight = [&](int h, float (&g)[kHeld][VEC]) {
+    if constexpr (W_SMEM) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        const Pack<float, VEC> v = load_pack<float, VEC>(s_w[(h + i) * group + me].v);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) g[i][k] = v.v[k];
+      }
+    } else {
+      load_cols<kHeld, VEC>(p.w, p.pt, c0 + h * dc, dc, n, 1.f, g);
+    }
+  };
+  const auto load_part = [&](int64_t r, int h, PX* x, PY* dy) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      x[i] = load_vec<XT, VEC>(p.x + r * p.xs, c0 + (h + i) * dc, n, false);
+      dy[i] = load_vec<YT, VEC>(p.dy + r * p.dys, c0 + (h + i) * dc, n, false);
+    }
+  };
+
+  float dw[CPT], db[CPT];
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) dw[k] = db[k] = 0.f;
+#pragma unroll
+  for (int k = 0; k < STAGES - 1; ++k) fetch(first + k * step, k);
+  float m_next = 0.f, rs_next = 0.f;
+  if (first < p.n_rows) m_next = p.mean[first], rs_next = p.rstd[first];
+  int stage = 0, turn = 0;
+  for (int64_t r = first; r < p.n_rows; r += step) {
+    const float m = m_next, rs = rs_next;
+    if (r + step < p.n_rows) m_next = p.mean[r + step], rs_next = p.rstd[r + step];
+    float sg = 0.f, sgx = 0.f;
+    PX x[kHeld];
+    PY dy[kHeld];
+    float g[kHeld][VEC];
+    if constexpr (STAGES > 0) {
+      // the stage before this one is free: this thread read it a row ago
+      fetch(r + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+      copy_wait<STAGES - 1>();
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (c0 + i * dc < n) {
+          x[i] = ring_x[slot(stage, i)];
+          dy[i] = ring_y[slot(stage, i)];
+        }
+      }
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+    }
+#pragma unroll
+    for (int h = 0; h < NV; h += kHeld) {
+      if constexpr (STAGES == 0) load_part(r, h, x, dy);
+      weight(h, g);
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        if (c0 + (h + i) * dc < n) {
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) {
+            const float d = to_f32(dy[i].v[k]), xh = (to_f32(x[i].v[k]) - m) * rs;
+            const float gk = d * g[i][k];
+            sg += gk;
+            sgx += gk * xh;
+            dw[(h + i) * VEC + k] += d * xh;
+            db[(h + i) * VEC + k] += d;
+          }
+        }
+      }
+    }
+    if (!p.dx) continue;
+    if constexpr (WARP) {
+      sg = warp_sum(sg) * inv;
+      sgx = warp_sum(sgx) * inv;
+    } else {
+      const float2 t = cta_sum2_all(sg, sgx, s_red[turn]);
+      turn ^= 1;
+      sg = t.x * inv;
+      sgx = t.y * inv;
+    }
+#pragma unroll
+    for (int h = 0; h < NV; h += kHeld) {
+      if constexpr (STAGES == 0) load_part(r, h, x, dy);
+      weight(h, g);
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        const int c = c0 + (h + i) * dc;
+        if (c < n) {
+          PX out;
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) {
+            const float d = to_f32(dy[i].v[k]), xh = (to_f32(x[i].v[k]) - m) * rs;
+            out.v[k] = from_f32<XT>(rs * (d * g[i][k] - sg - xh * sgx));
+          }
+          store_pack<XT, VEC>(p.dx + r * p.dxs + c, out);
+        }
+      }
+    }
+  }
+  pdl_launch_dependents();
+  if (!p.part) return;
+  float* part = p.part + (int64_t)blockIdx.x * 2 * n;
+  if constexpr (WARP) {
+    // the warps' sums, added up in warp order in shared memory
+    if constexpr (STAGES > 0) copy_wait<0>();
+    float* s_dw = reinterpret_cast<float*>(s_dyn);
+    float* s_db = s_dw + n;
+    for (int k = 0; k < kWarps; ++k) {
+      __syncthreads();
+      if ((int)(threadIdx.x >> 5) != k) continue;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * group + me) * VEC;
+        if (c < n) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) {
+            s_dw[c + j] = k ? s_dw[c + j] + dw[i * VEC + j] : dw[i * VEC + j];
+            s_db[c + j] = k ? s_db[c + j] + db[i * VEC + j] : db[i * VEC + j];
+          }
+        }
+      }
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * n; c += kThreads) part[c] = s_dw[c];
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * group + me) * VEC;
+      if (c < n) {
+        Pack<float, VEC> a, b;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          a.v[j] = dw[i * VEC + j];
+          b.v[j] = db[i * VEC + j];
+        }
+        store_pack<float, VEC>(part + c, a);
+        store_pack<float, VEC>(part + n + c, b);
+      }
     }
   }
 }
 
-// dweight and dbias of kThreads columns: partial sums of a block of rows,
-// then (layernorm_params_sum) the blocks in order.
-constexpr int kParamBlocks = 64;
+// Backward, rows too long for registers: dx, one row per CTA step.
+template <typename XT, typename YT>
+__global__ void __launch_bounds__(kThreads) layernorm_dx_rows(BackwardArgs<XT, YT> p) {
+  __shared__ float2 s_red[2][32];
+  int turn = 0;
+  for (int64_t r = blockIdx.x; r < p.n_rows; r += gridDim.x) {
+    const float m = p.mean[r], rs = p.rstd[r];
+    const YT* dy = p.dy + r * p.dys;
+    const XT* x = p.x + r * p.xs;
+    float sg = 0.f, sgx = 0.f;
+    for (int j = threadIdx.x; j < p.n_cols; j += kThreads) {
+      const float g = to_f32(dy[j]) * (p.w ? load_as_f32(p.w, p.pt, j) : 1.f);
+      sg += g;
+      sgx += g * ((to_f32(x[j]) - m) * rs);
+    }
+    const float2 t = cta_sum2_all(sg, sgx, s_red[turn]);
+    turn ^= 1;
+    sg = t.x / (float)p.n_cols;
+    sgx = t.y / (float)p.n_cols;
+    for (int j = threadIdx.x; j < p.n_cols; j += kThreads) {
+      const float g = to_f32(dy[j]) * (p.w ? load_as_f32(p.w, p.pt, j) : 1.f);
+      const float xh = (to_f32(x[j]) - m) * rs;
+      p.dx[r * p.dxs + j] = from_f32<XT>(rs * (g - sg - xh * sgx));
+    }
+  }
+}
+
+// ... and dweight and dbias: partial sums of a block of rows, a thread per
+// column.
+constexpr int kLongParts = 64;
 
 template <typename XT, typename YT>
-__global__ void __launch_bounds__(kThreads)
-layernorm_params_part(int64_t n_rows, int n_cols, const YT* dy, int64_t dys, const XT* x,
-                      int64_t xs, const float* mean, const float* rstd, float* part) {
+__global__ void __launch_bounds__(kThreads) layernorm_params_part(BackwardArgs<XT, YT> p) {
   const int j = blockIdx.x * kThreads + threadIdx.x;
-  if (j >= n_cols) return;
-  const int64_t per = (n_rows + kParamBlocks - 1) / kParamBlocks;
-  const int64_t lo = blockIdx.y * per, hi = lo + per < n_rows ? lo + per : n_rows;
+  if (j >= p.n_cols) return;
+  const int64_t per = (p.n_rows + kLongParts - 1) / kLongParts;
+  const int64_t lo = blockIdx.y * per, hi = lo + per < p.n_rows ? lo + per : p.n_rows;
   float dw = 0.f, db = 0.f;
   for (int64_t r = lo; r < hi; ++r) {
-    const float d = to_f32(dy[r * dys + j]);
-    dw += d * ((to_f32(x[r * xs + j]) - mean[r]) * rstd[r]);
+    const float d = to_f32(p.dy[r * p.dys + j]);
+    dw += d * ((to_f32(p.x[r * p.xs + j]) - p.mean[r]) * p.rstd[r]);
     db += d;
   }
-  part[(int64_t)blockIdx.y * 2 * n_cols + j] = dw;
-  part[((int64_t)blockIdx.y * 2 + 1) * n_cols + j] = db;
+  p.part[(int64_t)blockIdx.y * 2 * p.n_cols + j] = dw;
+  p.part[((int64_t)blockIdx.y * 2 + 1) * p.n_cols + j] = db;
 }
 
+// dweight and dbias from `parts` partial sums: 32 columns per CTA, eight
+// warps taking every eighth part, then the warps' sums in order.
 __global__ void __launch_bounds__(kThreads)
-layernorm_params_sum(int n_cols, const float* part, void* dw_out, void* db_out, int pt) {
-  const int j = blockIdx.x * kThreads + threadIdx.x;
-  if (j >= n_cols) return;
-  float dw = 0.f, db = 0.f;
-  for (int k = 0; k < kParamBlocks; ++k) {
-    dw += part[(int64_t)k * 2 * n_cols + j];
-    db += part[((int64_t)k * 2 + 1) * n_cols + j];
+layernorm_params_sum(int n_cols, int parts, const float* part, void* dw_out, void* db_out, int pt) {
+  __shared__ float s_part[kWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;  // column of {dweight, dbias}
+  pdl_wait();
+  float v = 0.f;
+  if (c < 2ll * n_cols) {
+    const float* q = part + c;
+#pragma unroll 8
+    for (int k = warp; k < parts; k += kWarps) v += q[(int64_t)k * 2 * n_cols];
   }
-  if (dw_out) store_from_f32(dw_out, pt, j, dw);
-  if (db_out) store_from_f32(db_out, pt, j, db);
+  s_part[warp][lane] = v;
+  __syncthreads();
+  if (warp != 0 || c >= 2ll * n_cols) return;
+  v = 0.f;
+#pragma unroll
+  for (int k = 0; k < kWarps; ++k) v += s_part[k][lane];
+  if (c < n_cols) {
+    if (dw_out) store_from_f32(dw_out, pt, c, v);
+  } else if (db_out) {
+    store_from_f32(db_out, pt, c - n_cols, v);
+  }
+}
+
+constexpr int kSms = 152;
+
+// How the rows of a call are cut: columns per thread (0: the long-row
+// kernels), threads, and CTAs.
+struct BackwardShape {
+  bool warp;
+  int cols, threads, grid;
+};
+
+BackwardShape backward_shape(int64_t n_rows, int n_cols, bool aligned) {
+  BackwardShape s{};
+  if (aligned && n_cols <= 512) {
+    s.warp = true;
+    s.cols = n_cols <= 256 ? 8 : 16;
+    s.threads = kThreads;
+    const int64_t rows = (n_rows + kWarps - 1) / kWarps;
+    s.grid = (int)(rows < 2 * kSms ? rows : 2 * kSms);
+    return s;
+  }
+  const int cols = n_cols <= 4096 ? 8 : n_cols <= 16 * 768 ? 16 : n_cols <= 32 * 512 ? 32 : 0;
+  s.cols = (!aligned && cols == 32) ? 0 : cols;
+  if (!s.cols) return s;
+  s.threads = ((n_cols + s.cols - 1) / s.cols + 31) / 32 * 32;
+  const int per_sm = s.threads >= 512 ? 1 : s.threads >= 352 ? 2 : s.threads >= 256 ? 3 : 4;
+  s.grid = (int)(n_rows < (int64_t)per_sm * kSms ? n_rows : (int64_t)per_sm * kSms);
+  return s;
 }
 
 constexpr int kMaxCols = INT32_MAX - 4096;
-constexpr int kRowGrid = 152 * 8;
+constexpr int kRowGrid = kSms * 8;
+constexpr size_t kSmemBudget = 225 * 1024;  // of an SM's shared memory, for rings
+
+// Partial sums of dweight and dbias, at most (whichever kernel runs).
+int64_t backward_workspace(int64_t n_rows, int n_cols, bool want_params) {
+  if (!want_params || n_rows == 0) return 0;
+  int64_t parts = kLongParts;
+  for (const bool aligned : {false, true}) {
+    const BackwardShape s = backward_shape(n_rows, n_cols, aligned);
+    if (s.cols && s.grid > parts) parts = s.grid;
+  }
+  return parts * 2 * n_cols * 4;
+}
+
+spmv_status launched() { return cudaGetLastError() == cudaSuccess ? SPMV_OK : SPMV_ERR_CUDA; }
 
 template <typename F>
 spmv_status by_types(spmv_dtype x, spmv_dtype y, F&& f) {
@@ -122,11 +489,120 @@ spmv_status by_types(spmv_dtype x, spmv_dtype y, F&& f) {
   return SPMV_ERR_UNSUPPORTED;
 }
 
-int64_t backward_workspace(int64_t n_rows, int n_cols, bool want_params) {
-  return want_params && n_rows > 0 ? (int64_t)kParamBlocks * 2 * n_cols * 4 : 0;
+// Rows of a matrix that vectors of `vec` elements can be loaded from: every
+// row starts on a whole vector (of at most 16 bytes).
+bool rows_aligned(const void* p, int64_t rows, int64_t stride, int64_t size, int vec) {
+  const int64_t bytes = size * vec > 16 ? 16 : size * vec;
+  return aligned_to(p, bytes) && (rows <= 1 || (stride * size) % bytes == 0);
 }
 
-spmv_status launched() { return cudaGetLastError() == cudaSuccess ? SPMV_OK : SPMV_ERR_CUDA; }
+template <typename XT, typename YT, int VEC, int CPT, bool WARP>
+spmv_status forward_launch(int64_t n_rows, int n_cols, const XT* x, int64_t xs,
+                           const void* w, const void* b, int pt, float eps, YT* y, int64_t ys,
+                           float* mean, float* rstd, cudaStream_t st) {
+  const int64_t ctas = WARP ? (n_rows + kWarps - 1) / kWarps : n_rows;
+  const int grid = (int)(ctas < INT_MAX ? ctas : INT_MAX);
+  const int threads = WARP ? kThreads : ((n_cols + CPT - 1) / CPT + 31) / 32 * 32;
+  layernorm_regs<XT, YT, VEC, CPT, WARP>
+      <<<grid, threads, 0, st>>>(n_rows, n_cols, x, xs, w, b, pt, eps, y, ys, mean, rstd);
+  return launched();
+}
+
+template <typename XT, typename YT, int VEC>
+spmv_status forward(int64_t n_rows, int n_cols, const XT* x, int64_t xs, const void* w,
+                    const void* b, int pt, float eps, YT* y, int64_t ys, float* mean, float* rstd,
+                    cudaStream_t st) {
+#define SPMV_FORWARD(CPT, WARP)                                                              \
+  return forward_launch<XT, YT, VEC, CPT, WARP>(n_rows, n_cols, x, xs, w, b, pt, eps, y, ys, mean, \
+                                                rstd, st)
+  // a warp per row while a lane holds at most 32 columns (of 16 loads each
+  // where they go element by element)
+  if (n_cols <= 32 * 8) SPMV_FORWARD(8, true);
+  if (VEC > 1 && n_cols <= 32 * 32) SPMV_FORWARD(32, true);
+  if (n_cols <= 8 * 512) SPMV_FORWARD(8, false);
+  if constexpr (VEC > 1) {
+    if (n_cols <= 24 * 512) SPMV_FORWARD(24, false);
+  } else {
+    if (n_cols <= 16 * 768) SPMV_FORWARD(16, false);
+  }
+  if (n_cols <= 32 * 1024) SPMV_FORWARD(32, false);
+#undef SPMV_FORWARD
+  const int grid = (int)(n_rows < kRowGrid ? n_rows : kRowGrid);
+  layernorm_rows<XT, YT><<<grid, kThreads, 0, st>>>(n_rows, n_cols, x, xs, w, b, pt, eps, y, ys,
+                                                    mean, rstd);
+  return launched();
+}
+
+template <typename XT, typename YT, int VEC, int CPT, int STAGES, bool WARP, bool W_SMEM>
+spmv_status backward_launch(const BackwardShape& s, size_t smem, const BackwardArgs<XT, YT>& p,
+                            cudaStream_t st) {
+  const auto fn = layernorm_backward_fused<XT, YT, VEC, CPT, STAGES, WARP, W_SMEM>;
+  if (smem > 40 * 1024 &&  // 48 KB less the static part need no opt-in
+      cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return SPMV_ERR_CUDA;
+  fn<<<s.grid, s.threads, smem, st>>>(p);
+  return launched();
+}
+
+template <typename XT, typename YT, int VEC, int CPT, bool WARP>
+spmv_status backward_stages(const BackwardShape& s, const BackwardArgs<XT, YT>& p,
+                            cudaStream_t st) {
+  const size_t w = (size_t)(WARP ? 32 : s.threads) * CPT * 4;  // weights
+  if constexpr (VEC == 1) {
+    return backward_launch<XT, YT, VEC, CPT, 0, WARP, true>(s, w, p, st);
+  } else {
+    const size_t stage = (size_t)s.threads * CPT * (sizeof(XT) + sizeof(YT));
+    // (a warp group's ring is larger than the two sums per column that the
+    // warps leave in its place at the end)
+    const int per_sm = WARP ? 2 : (s.grid + kSms - 1) / kSms;
+    const size_t room = kSmemBudget / (size_t)per_sm;
+    if constexpr (CPT < 32)
+      if (4 * stage + w <= room)
+        return backward_launch<XT, YT, VEC, CPT, 4, WARP, true>(s, 4 * stage + w, p, st);
+    if (2 * stage + w <= room)
+      return backward_launch<XT, YT, VEC, CPT, 2, WARP, true>(s, 2 * stage + w, p, st);
+    if constexpr (CPT >= 16 && !WARP)
+      return backward_launch<XT, YT, VEC, CPT, 2, WARP, false>(s, 2 * stage, p, st);
+    return SPMV_ERR_UNSUPPORTED;  // (rows of fewer columns always fit)
+  }
+}
+
+template <typename XT, typename YT, int VEC>
+spmv_status backward(const BackwardArgs<XT, YT>& p, void* dweight, void* dbias, cudaStream_t st) {
+  const BackwardShape s = backward_shape(p.n_rows, p.n_cols, VEC > 1);
+  int parts = s.grid;
+  spmv_status status = SPMV_OK;
+  if (s.cols) {
+    if (s.warp) {
+      if constexpr (VEC > 1)
+        status = s.cols == 8 ? backward_stages<XT, YT, VEC, 8, true>(s, p, st)
+                             : backward_stages<XT, YT, VEC, 16, true>(s, p, st);
+    } else if (s.cols == 8) {
+      status = backward_stages<XT, YT, VEC, 8, false>(s, p, st);
+    } else if (s.cols == 16) {
+      status = backward_stages<XT, YT, VEC, 16, false>(s, p, st);
+    } else {
+      if constexpr (VEC > 1) status = backward_stages<XT, YT, VEC, 32, false>(s, p, st);
+    }
+  } else {
+    const int grid = (int)(p.n_rows < kRowGrid ? p.n_rows : kRowGrid);
+    parts = kLongParts;
+    if (p.part)
+      layernorm_params_part<XT, YT>
+          <<<dim3((p.n_cols + kThreads - 1) / kThreads, kLongParts), kThreads, 0, st>>>(p);
+    if (p.dx) layernorm_dx_rows<XT, YT><<<grid, kThreads, 0, st>>>(p);
+    status = launched();
+  }
+  if (status != SPMV_OK || !p.part) return status;
+  int n_cols = p.n_cols, pt = p.pt;
+  const float* part = p.part;
+  void* args[] = {&n_cols, &parts, &part, &dweight, &dbias, &pt};
+  return launch_pdl(reinterpret_cast<const void*>(&layernorm_params_sum),
+                    (int)((2ll * n_cols + 31) / 32), kThreads, 0, st, args) == 0
+             ? SPMV_OK
+             : SPMV_ERR_CUDA;
+}
 
 }  // namespace
 }  // namespace spmv
@@ -155,14 +631,21 @@ extern "C" spmv_status spmv_layernorm(int64_t n_rows, int32_t n_cols, const void
       spans_overlap(x, n_rows, n_cols, x_stride, xs, y, n_rows, n_cols, y_stride, ysz))
     return SPMV_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int grid = (int)(n_rows < kRowGrid ? n_rows : kRowGrid);
   return by_types(x_dtype, y_dtype, [&](auto* xt, auto* yt) {
     using XT = std::remove_pointer_t<decltype(xt)>;
     using YT = std::remove_pointer_t<decltype(yt)>;
-    layernorm_rows<XT, YT><<<grid, kThreads, 0, st>>>(
-        n_rows, n_cols, static_cast<const XT*>(x), x_stride, weight, bias, param_dtype, eps,
-        static_cast<YT*>(y), y_stride, mean_out, rstd_out);
-    return launched();
+    constexpr int kVec = 16 / (int)sizeof(XT);
+    const XT* xp = static_cast<const XT*>(x);
+    YT* yp = static_cast<YT*>(y);
+    // whole vectors need every row of x and y, weight and bias on vector
+    // boundaries and a whole number of vectors per row
+    if (n_cols % kVec == 0 && rows_aligned(x, n_rows, x_stride, xs, kVec) &&
+        rows_aligned(y, n_rows, y_stride, ysz, kVec) && aligned_to(weight, 16) &&
+        aligned_to(bias, 16))
+      return forward<XT, YT, kVec>(n_rows, n_cols, xp, x_stride, weight, bias, param_dtype, eps,
+                                   yp, y_stride, mean_out, rstd_out, st);
+    return forward<XT, YT, 1>(n_rows, n_cols, xp, x_stride, weight, bias, param_dtype, eps, yp,
+                              y_stride, mean_out, rstd_out, st);
   });
 }
 
@@ -206,23 +689,18 @@ extern "C" spmv_status spmv_layernorm_backward(
       return SPMV_ERR_CUDA;
     return SPMV_OK;
   }
-  const int grid = (int)(n_rows < kRowGrid ? n_rows : kRowGrid);
   return by_types(x_dtype, dy_dtype, [&](auto* xt, auto* yt) {
     using XT = std::remove_pointer_t<decltype(xt)>;
     using YT = std::remove_pointer_t<decltype(yt)>;
-    const int col_blocks = (n_cols + kThreads - 1) / kThreads;
-    if (params) {
-      float* part = static_cast<float*>(workspace);
-      layernorm_params_part<XT, YT><<<dim3(col_blocks, kParamBlocks), kThreads, 0, st>>>(
-          n_rows, n_cols, static_cast<const YT*>(dy), dy_stride, static_cast<const XT*>(x),
-          x_stride, mean, rstd, part);
-      layernorm_params_sum<<<col_blocks, kThreads, 0, st>>>(n_cols, part, dweight, dbias,
-                                                            param_dtype);
-    }
-    if (dx)
-      layernorm_dx_rows<XT, YT><<<grid, kThreads, 0, st>>>(
-          n_rows, n_cols, static_cast<const YT*>(dy), dy_stride, static_cast<const XT*>(x),
-          x_stride, weight, param_dtype, mean, rstd, static_cast<XT*>(dx), dx_stride);
-    return launched();
+    constexpr int kVec = 16 / (int)sizeof(XT);
+    BackwardArgs<XT, YT> p{n_rows, n_cols, static_cast<const YT*>(dy), dy_stride,
+                           static_cast<const XT*>(x), x_stride, weight, param_dtype, mean, rstd,
+                           static_cast<XT*>(dx), dx_stride,
+                           params ? static_cast<float*>(workspace) : nullptr};
+    if (n_cols % kVec == 0 && rows_aligned(x, n_rows, x_stride, xs, kVec) &&
+        rows_aligned(dy, n_rows, dy_stride, dys, kVec) &&
+        (!dx || rows_aligned(dx, n_rows, dx_stride, xs, kVec)) && aligned_to(weight, 16))
+      return backward<XT, YT, kVec>(p, dweight, dbias, st);
+    return backward<XT, YT, 1>(p, dweight, dbias, st);
   });
 }

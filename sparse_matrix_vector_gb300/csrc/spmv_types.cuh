@@ -45,6 +45,94 @@ __device__ __forceinline__ void store_from_f32(void* p, int dtype, int64_t i, fl
     static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
+// N elements as one or two vector loads (N * sizeof(T) of 2, 4, 8, 16 or 32
+// bytes, aligned to it, at most 16), widened to fp32. `stream`: data that is
+// read once and should leave the caches first.
+template <int BYTES>
+struct Bits;
+template <>
+struct Bits<2> { using type = unsigned short; };
+template <>
+struct Bits<4> { using type = unsigned; };
+template <>
+struct Bits<8> { using type = uint2; };
+template <>
+struct Bits<16> { using type = uint4; };
+
+template <typename T, int N>
+struct alignas(N * sizeof(T) > 16 ? 16 : N * sizeof(T)) Pack {
+  T v[N];
+};
+
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> load_pack(const T* p, bool stream = false) {
+  constexpr int kBytes = N * (int)sizeof(T), kPart = kBytes > 16 ? 16 : kBytes;
+  using B = typename Bits<kPart>::type;
+  Pack<T, N> r;
+#pragma unroll
+  for (int i = 0; i < kBytes / kPart; ++i) {
+    const B* q = reinterpret_cast<const B*>(p) + i;
+    reinterpret_cast<B*>(&r)[i] = stream ? __ldcs(q) : *q;
+  }
+  return r;
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store_pack(T* p, const Pack<T, N>& r) {
+  constexpr int kBytes = N * (int)sizeof(T), kPart = kBytes > 16 ? 16 : kBytes;
+  using B = typename Bits<kPart>::type;
+#pragma unroll
+  for (int i = 0; i < kBytes / kPart; ++i)
+    reinterpret_cast<B*>(p)[i] = reinterpret_cast<const B*>(&r)[i];
+}
+
+// VEC elements at column c of a row of n: a vector past the end repeats the
+// last one (an unconditional load, so that loads of several vectors go out
+// together); a single element past the end is zero.
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> load_vec(const T* row, int c, int n, bool stream) {
+  if constexpr (VEC == 1) {
+    Pack<T, VEC> r;
+    r.v[0] = from_f32<T>(0.f);
+    if (c < n) r = load_pack<T, VEC>(row + c, stream);
+    return r;
+  } else {
+    return load_pack<T, VEC>(row + min(c, n - VEC), stream);
+  }
+}
+
+// A thread's columns of a vector of runtime type, as fp32: vectors of VEC
+// columns at first + i * step, i < NV (as load_vec past the end); `fill` for a null pointer. The type is tested once, so that
+// all of the loads are under way together.
+template <typename T, int NV, int VEC>
+__device__ __forceinline__ void load_cols_as(const T* p, int first, int step, int n,
+                                             float (&v)[NV][VEC]) {
+  Pack<T, VEC> r[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) r[i] = load_vec<T, VEC>(p, first + i * step, n, false);
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) v[i][k] = to_f32(r[i].v[k]);
+}
+
+template <int NV, int VEC>
+__device__ __forceinline__ void load_cols(const void* p, int dtype, int first, int step, int n,
+                                          float fill, float (&v)[NV][VEC]) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) v[i][k] = fill;
+  } else if (dtype == SPMV_F32) {
+    load_cols_as<float, NV, VEC>(static_cast<const float*>(p), first, step, n, v);
+  } else if (dtype == SPMV_F16) {
+    load_cols_as<__half, NV, VEC>(static_cast<const __half*>(p), first, step, n, v);
+  } else {
+    load_cols_as<__nv_bfloat16, NV, VEC>(static_cast<const __nv_bfloat16*>(p), first, step, n, v);
+  }
+}
+
 }  // namespace
 
 inline bool op_dtype(int t) { return t == SPMV_F32 || t == SPMV_F16 || t == SPMV_BF16; }

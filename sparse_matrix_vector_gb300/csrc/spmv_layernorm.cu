@@ -19,100 +19,6 @@ __device__ __forceinline__ float cta_sum_all(float v, float* s_red) {
   return warp_sum(lane < (int)(blockDim.x >> 5) ? s_red[lane] : 0.f);
 }
 
-// Threads of a CTA that holds a row with `cols` columns per thread.
-constexpr int forward_max_threads(int cols) { return cols == 32 ? 1024 : cols == 16 ? 768 : 512; }
-
-// Forward, rows held in registers. Each row belongs to a group of threads (a
-// warp, or the whole CTA), each thread holding CPT columns of it in vectors of
-// VEC: the row is read once, and mean and variance are taken one after the
-// other (the variance from the centred values: no cancellation).
-template <typename XT, typename YT, int VEC, int CPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? kThreads : forward_max_threads(CPT),
-                                  !WARP && CPT != 32 && CPT != 16 ? 2 : 1)
-layernorm_regs(int64_t n_rows, int n_cols, const XT* x, int64_t xs, const void* w, const void* b,
-               int pt, float eps, YT* y, int64_t ys, float* mean_out, float* rstd_out) {
-  constexpr int NV = CPT / VEC;
-  constexpr int kOut = NV % 2 ? 1 : VEC == 1 ? 4 : 2;  // vectors of y made at a time
-  __shared__ float s_red[2][32];
-  const int group = WARP ? 32 : blockDim.x, me = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const int per_cta = WARP ? kWarps : 1;
-  const int first = me * VEC, step = group * VEC;
-  const float inv = 1.f / (float)n_cols;
-  for (int64_t r = (int64_t)blockIdx.x * per_cta + (WARP ? threadIdx.x >> 5 : 0); r < n_rows;
-       r += (int64_t)gridDim.x * per_cta) {
-    const XT* xr = x + r * xs;
-    YT* yr = y + r * ys;
-    Pack<XT, VEC> in[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      in[i] = load_vec<XT, VEC>(xr, first + i * step, n_cols, true);
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) s += first + i * step < n_cols ? to_f32(in[i].v[k]) : 0.f;
-    const float mean = (WARP ? warp_sum(s) : cta_sum_all(s, s_red[0])) * inv;
-    float q = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        const float c = to_f32(in[i].v[k]) - mean;
-        q += first + i * step < n_cols ? c * c : 0.f;
-      }
-    const float rstd = rsqrtf((WARP ? warp_sum(q) : cta_sum_all(q, s_red[1])) * inv + eps);
-#pragma unroll
-    for (int i = 0; i < NV; i += kOut) {
-      float g[kOut][VEC], o[kOut][VEC];
-      load_cols<kOut, VEC>(w, pt, first + i * step, step, n_cols, 1.f, g);
-      load_cols<kOut, VEC>(b, pt, first + i * step, step, n_cols, 0.f, o);
-#pragma unroll
-      for (int h = 0; h < kOut; ++h) {
-        const int c = first + (i + h) * step;
-        Pack<YT, VEC> out;
-#pragma unroll
-        for (int k = 0; k < VEC; ++k)
-          out.v[k] = from_f32<YT>((to_f32(in[i + h].v[k]) - mean) * rstd * g[h][k] + o[h][k]);
-        if (c < n_cols) store_pack<YT, VEC>(yr + c, out);
-      }
-    }
-    if (me == 0) {
-      if (mean_out) mean_out[r] = mean;
-      if (rstd_out) rstd_out[r] = rstd;
-    }
-  }
-}
-
-// Forward, rows too long for registers: one row per CTA step, three passes
-// over it (mean, variance, output), the second and third mostly from L2.
-template <typename XT, typename YT>
-__global__ void __launch_bounds__(kThreads)
-layernorm_rows(int64_t n_rows, int n_cols, const XT* x, int64_t xs, const void* w, const void* b,
-               int pt, float eps, YT* y, int64_t ys, float* mean_out, float* rstd_out) {
-  __shared__ float s_red[2][32];
-  for (int64_t r = blockIdx.x; r < n_rows; r += gridDim.x) {
-    const XT* xr = x + r * xs;
-    YT* yr = y + r * ys;
-    float s = 0.f;
-    for (int j = threadIdx.x; j < n_cols; j += kThreads) s += to_f32(xr[j]);
-    const float mean = cta_sum_all(s, s_red[0]) / (float)n_cols;
-    float q = 0.f;
-    for (int j = threadIdx.x; j < n_cols; j += kThreads) {
-      const float c = to_f32(xr[j]) - mean;
-      q += c * c;
-    }
-    const float rstd = rsqrtf(cta_sum_all(q, s_red[1]) / (float)n_cols + eps);
-    for (int j = threadIdx.x; j < n_cols; j += kThreads) {
-      const float g = w ? load_as_f32(w, pt, j) : 1.f, o = b ? load_as_f32(b, pt, j) : 0.f;
-      yr[j] = from_f32<YT>((to_f32(xr[j]) - mean) * rstd * g + o);
-    }
-    if (threadIdx.x == 0) {
-      if (mean_out) mean_out[r] = mean;
-      if (rstd_out) rstd_out[r] = rstd;
-    }
-  }
-}
-
 // This thread's asynchronous copies of 4, 8 or 16 bytes into shared memory,
 // in groups; each thread reads back only what it copied itself, so waiting
 // for its own groups is all the synchronisation there is.
@@ -130,6 +36,160 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int LEFT>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// Columns a thread holds of its rows, and the threads a CTA has at most with
+// them: more columns, or the addresses of single elements, take more
+// registers and leave room for fewer threads.
+constexpr int most_threads(int cols, bool aligned) { return cols == 16 && aligned ? 768 : 512; }
+
+template <typename XT, typename YT>
+struct ForwardArgs {
+  int64_t n_rows;
+  int n_cols;
+  const XT* x;
+  int64_t xs;
+  const void *w, *b;
+  int pt;
+  float eps;
+  YT* y;
+  int64_t ys;
+  float *mean, *rstd;
+};
+
+// Forward, one pass over x: a group of threads (a warp, or the CTA) takes
+// rows in turn, each thread the same CPT columns of every row, whose weight
+// and bias it keeps in registers. STAGES - 1 rows are on their way into
+// shared memory while one is worked on (STAGES 0: rows that are not 16-byte
+// aligned, loaded directly, the next one asked from L2 a row ahead). Mean and
+// variance are taken one after the other, the variance from the centred
+// values: no cancellation. The arithmetic is on pairs (fp32x2 instructions).
+template <typename XT, typename YT, int VEC, int CPT, int STAGES, bool WARP>
+__global__ void __launch_bounds__(WARP ? kThreads : most_threads(CPT, STAGES > 0))
+layernorm_fused(ForwardArgs<XT, YT> p) {
+  constexpr int NV = CPT / VEC;
+  constexpr bool kAligned = STAGES > 0;
+  using PX = Pack<XT, VEC>;
+  extern __shared__ __align__(16) unsigned char s_dyn[];
+  __shared__ float s_red[2][32];
+  const Cols<VEC, kAligned> cols{WARP ? (int)threadIdx.x & 31 : (int)threadIdx.x,
+                                 WARP ? 32 : (int)blockDim.x, p.n_cols};
+  const int64_t step = (int64_t)gridDim.x * (WARP ? kWarps : 1);
+  const int64_t first = (int64_t)blockIdx.x * (WARP ? kWarps : 1) + (WARP ? threadIdx.x >> 5 : 0);
+  const float inv = 1.f / (float)p.n_cols;
+  // ring of stages, vector i of thread t at [stage][i][t]
+  PX* ring = reinterpret_cast<PX*>(s_dyn);
+  const auto slot = [&](int stage, int i) {
+    return (stage * NV + i) * (int)blockDim.x + (int)threadIdx.x;
+  };
+  const auto fetch = [&](int64_t r, int stage) {
+    if (r < p.n_rows) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (cols.has(i))
+          copy_async<sizeof(PX)>(&ring[slot(stage, i)], p.x + r * p.xs + cols.col(i, 0));
+    }
+    copy_commit();
+  };
+  if constexpr (STAGES > 0) {
+#pragma unroll
+    for (int k = 0; k < STAGES - 1; ++k) fetch(first + k * step, k);
+  }
+  float2 g[NV][VEC / 2], o[NV][VEC / 2];
+  cols.load_param(p.w, p.pt, 1.f, g);
+  cols.load_param(p.b, p.pt, 0.f, o);
+  int stage = 0;
+  for (int64_t r = first; r < p.n_rows; r += step) {
+    PX in[NV];
+    if constexpr (STAGES > 0) {
+      // the stage before this one is free: this thread read it a row ago
+      fetch(r + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+      copy_wait<STAGES - 1>();
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (cols.has(i)) in[i] = ring[slot(stage, i)];
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+    } else {
+      cols.load(p.x + r * p.xs, in, true);
+      if (r + step < p.n_rows) cols.prefetch(p.x + (r + step) * p.xs);
+    }
+    float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (cols.has(i)) {
+#pragma unroll
+        for (int k = 0; k < VEC / 2; ++k) {
+          float2 v = pair_f32(in[i], k);
+          if (!cols.has(i, 2 * k)) v.x = 0.f;
+          if (!cols.has(i, 2 * k + 1)) v.y = 0.f;
+          s2 = __fadd2_rn(s2, v);
+        }
+      }
+    const float s = s2.x + s2.y;
+    const float mean = (WARP ? warp_sum(s) : cta_sum_all(s, s_red[0])) * inv;
+    const float2 off = make_float2(-mean, -mean);
+    float2 q2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (cols.has(i)) {
+#pragma unroll
+        for (int k = 0; k < VEC / 2; ++k) {
+          float2 c = __fadd2_rn(pair_f32(in[i], k), off);
+          if (!cols.has(i, 2 * k)) c.x = 0.f;
+          if (!cols.has(i, 2 * k + 1)) c.y = 0.f;
+          q2 = __ffma2_rn(c, c, q2);
+        }
+      }
+    const float q = q2.x + q2.y;
+    const float rstd = rsqrtf((WARP ? warp_sum(q) : cta_sum_all(q, s_red[1])) * inv + p.eps);
+    const float2 scale = make_float2(rstd, rstd);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (cols.has(i)) {
+        Pack<YT, VEC> out;
+#pragma unroll
+        for (int k = 0; k < VEC / 2; ++k) {
+          const float2 c = __fadd2_rn(pair_f32(in[i], k), off);
+          set_pair(out, k, __ffma2_rn(__fmul2_rn(c, scale), g[i][k], o[i][k]));
+        }
+        cols.store(p.y + r * p.ys, i, out);
+      }
+    if (cols.me == 0) {
+      if (p.mean) p.mean[r] = mean;
+      if (p.rstd) p.rstd[r] = rstd;
+    }
+  }
+}
+
+// Forward, rows too long for registers: one row per CTA step, three passes
+// over it (mean, variance, output), the second and third mostly from L2.
+template <typename XT, typename YT>
+__global__ void __launch_bounds__(kThreads)
+layernorm_rows(ForwardArgs<XT, YT> p) {
+  __shared__ float s_red[2][32];
+  const int n_cols = p.n_cols;
+  for (int64_t r = blockIdx.x; r < p.n_rows; r += gridDim.x) {
+    const XT* xr = p.x + r * p.xs;
+    YT* yr = p.y + r * p.ys;
+    float s = 0.f;
+    for (int j = threadIdx.x; j < n_cols; j += kThreads) s += to_f32(xr[j]);
+    const float mean = cta_sum_all(s, s_red[0]) / (float)n_cols;
+    float q = 0.f;
+    for (int j = threadIdx.x; j < n_cols; j += kThreads) {
+      const float c = to_f32(xr[j]) - mean;
+      q += c * c;
+    }
+    const float rstd = rsqrtf(cta_sum_all(q, s_red[1]) / (float)n_cols + p.eps);
+    for (int j = threadIdx.x; j < n_cols; j += kThreads) {
+      const float g = p.w ? load_as_f32(p.w, p.pt, j) : 1.f;
+      const float o = p.b ? load_as_f32(p.b, p.pt, j) : 0.f;
+      yr[j] = from_f32<YT>((to_f32(xr[j]) - mean) * rstd * g + o);
+    }
+    if (threadIdx.x == 0) {
+      if (p.mean) p.mean[r] = mean;
+      if (p.rstd) p.rstd[r] = rstd;
+    }
+  }
 }
 
 // Sum of two values over the CTA, in every thread, in a fixed order. One
@@ -160,27 +220,24 @@ struct BackwardArgs {
   float* part;   // gridDim.x x {dweight, dbias} x n_cols partial sums, or null
 };
 
-// Columns a thread holds of its row; more of them cost registers (two fp32
-// sums per column), so wider groups take fewer threads.
-constexpr int backward_max_threads(int cols) { return cols == 16 ? 768 : 512; }
-
 // Backward, one pass over x and dy: a group of threads (a warp, or the CTA)
 // takes rows in turn, each thread the same CPT columns of every row, whose
 // dweight and dbias it sums in registers. STAGES - 1 rows are on their way
-// into shared memory while one is worked on. STAGES 0: rows that are not
-// 16-byte aligned go element by element, read once from memory and, for dx,
-// once more from the caches.
+// into shared memory while one is worked on (STAGES 0: as in the forward
+// kernel). With c = x - mean, the row needs the sums of g and of g * c:
+//   dx = rstd * g - rstd * mean(g) - c * rstd^3 * mean(g * c).
 template <typename XT, typename YT, int VEC, int CPT, int STAGES, bool WARP, bool W_SMEM>
-__global__ void __launch_bounds__(WARP ? kThreads : backward_max_threads(CPT))
+__global__ void __launch_bounds__(WARP ? kThreads : most_threads(CPT, STAGES > 0))
 layernorm_backward_fused(BackwardArgs<XT, YT> p) {
   constexpr int NV = CPT / VEC;
-  constexpr int kHeld = STAGES > 0 ? NV : 4;  // vectors of x and dy in registers
+  constexpr bool kAligned = STAGES > 0;
   using PX = Pack<XT, VEC>;
   using PY = Pack<YT, VEC>;
   extern __shared__ __align__(16) unsigned char s_dyn[];
   __shared__ float2 s_red[2][32];
-  const int group = WARP ? 32 : blockDim.x, me = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const int n = p.n_cols, c0 = me * VEC, dc = group * VEC;
+  const Cols<VEC, kAligned> cols{WARP ? (int)threadIdx.x & 31 : (int)threadIdx.x,
+                                 WARP ? 32 : (int)blockDim.x, p.n_cols};
+  const int n = p.n_cols;
   const int64_t step = (int64_t)gridDim.x * (WARP ? kWarps : 1);
   const int64_t first = (int64_t)blockIdx.x * (WARP ? kWarps : 1) + (WARP ? threadIdx.x >> 5 : 0);
   const float inv = 1.f / (float)n;
@@ -191,171 +248,167 @@ layernorm_backward_fused(BackwardArgs<XT, YT> p) {
     return (stage * NV + i) * (int)blockDim.x + (int)threadIdx.x;
   };
   const auto fetch = [&](int64_t r, int stage) {
-    if constexpr (STAGES > 0) {
-      if (r < p.n_rows) {
+    if (r < p.n_rows) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int c = (i * group + me) * VEC;
-          if (c < n) {
-            copy_async<sizeof(PX)>(&ring_x[slot(stage, i)], p.x + r * p.xs + c);
-            copy_async<sizeof(PY)>(&ring_y[slot(stage, i)], p.dy + r * p.dys + c);
-          }
+      for (int i = 0; i < NV; ++i)
+        if (cols.has(i)) {
+          copy_async<sizeof(PX)>(&ring_x[slot(stage, i)], p.x + r * p.xs + cols.col(i, 0));
+          copy_async<sizeof(PY)>(&ring_y[slot(stage, i)], p.dy + r * p.dys + cols.col(i, 0));
         }
-      }
-      copy_commit();
     }
+    copy_commit();
   };
-
   // the weight of this thread's columns: in shared memory for the whole call
   // where it fits (vector i of thread t at [i][t]; a warp's lanes hold the
   // same columns in every warp), else read again for every row
   Pack<float, VEC>* s_w = reinterpret_cast<Pack<float, VEC>*>(
       s_dyn + (size_t)STAGES * NV * blockDim.x * (sizeof(PX) + sizeof(PY)));
   if constexpr (W_SMEM) {
-    float g[NV][VEC];
-    load_cols<NV, VEC>(p.w, p.pt, c0, dc, n, 1.f, g);
+    float2 g[NV][VEC / 2];
+    cols.load_param(p.w, p.pt, 1.f, g);
     // (warps that share columns write the same values: no barrier needed)
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) s_w[i * group + me].v[k] = g[i][k];
+      for (int k = 0; k < VEC / 2; ++k) set_pair(s_w[i * cols.group + cols.me], k, g[i][k]);
   }
-  const auto weight = [&](int h, float (&g)[kHeld][VEC]) {
+  const auto weight = [&](float2 (&g)[NV][VEC / 2]) {
     if constexpr (W_SMEM) {
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        const Pack<float, VEC> v = load_pack<float, VEC>(s_w[(h + i) * group + me].v);
+      for (int i = 0; i < NV; ++i) {
+        const Pack<float, VEC> v = load_pack<float, VEC>(s_w[i * cols.group + cols.me].v);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) g[i][k] = v.v[k];
+        for (int k = 0; k < VEC / 2; ++k) g[i][k] = pair_f32(v, k);
       }
     } else {
-      load_cols<kHeld, VEC>(p.w, p.pt, c0 + h * dc, dc, n, 1.f, g);
-    }
-  };
-  const auto load_part = [&](int64_t r, int h, PX* x, PY* dy) {
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      x[i] = load_vec<XT, VEC>(p.x + r * p.xs, c0 + (h + i) * dc, n, false);
-      dy[i] = load_vec<YT, VEC>(p.dy + r * p.dys, c0 + (h + i) * dc, n, false);
+      cols.load_param(p.w, p.pt, 1.f, g);
     }
   };
 
-  float dw[CPT], db[CPT];
+  float2 dw[NV][VEC / 2], db[NV][VEC / 2];
 #pragma unroll
-  for (int k = 0; k < CPT; ++k) dw[k] = db[k] = 0.f;
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
-  for (int k = 0; k < STAGES - 1; ++k) fetch(first + k * step, k);
+    for (int k = 0; k < VEC / 2; ++k) dw[i][k] = db[i][k] = make_float2(0.f, 0.f);
+  if constexpr (STAGES > 0) {
+#pragma unroll
+    for (int k = 0; k < STAGES - 1; ++k) fetch(first + k * step, k);
+  }
   float m_next = 0.f, rs_next = 0.f;
   if (first < p.n_rows) m_next = p.mean[first], rs_next = p.rstd[first];
   int stage = 0, turn = 0;
   for (int64_t r = first; r < p.n_rows; r += step) {
     const float m = m_next, rs = rs_next;
     if (r + step < p.n_rows) m_next = p.mean[r + step], rs_next = p.rstd[r + step];
-    float sg = 0.f, sgx = 0.f;
-    PX x[kHeld];
-    PY dy[kHeld];
-    float g[kHeld][VEC];
+    PX x[NV];
+    PY dy[NV];
     if constexpr (STAGES > 0) {
       // the stage before this one is free: this thread read it a row ago
       fetch(r + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
       copy_wait<STAGES - 1>();
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (c0 + i * dc < n) {
+      for (int i = 0; i < NV; ++i)
+        if (cols.has(i)) {
           x[i] = ring_x[slot(stage, i)];
           dy[i] = ring_y[slot(stage, i)];
         }
-      }
       stage = stage + 1 == STAGES ? 0 : stage + 1;
-    }
-#pragma unroll
-    for (int h = 0; h < NV; h += kHeld) {
-      if constexpr (STAGES == 0) load_part(r, h, x, dy);
-      weight(h, g);
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        if (c0 + (h + i) * dc < n) {
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) {
-            const float d = to_f32(dy[i].v[k]), xh = (to_f32(x[i].v[k]) - m) * rs;
-            const float gk = d * g[i][k];
-            sg += gk;
-            sgx += gk * xh;
-            dw[(h + i) * VEC + k] += d * xh;
-            db[(h + i) * VEC + k] += d;
-          }
-        }
-      }
-    }
-    if (!p.dx) continue;
-    if constexpr (WARP) {
-      sg = warp_sum(sg) * inv;
-      sgx = warp_sum(sgx) * inv;
     } else {
-      const float2 t = cta_sum2_all(sg, sgx, s_red[turn]);
-      turn ^= 1;
-      sg = t.x * inv;
-      sgx = t.y * inv;
-    }
+      cols.load(p.x + r * p.xs, x, true);
+      cols.load(p.dy + r * p.dys, dy, true);
+      // columns past the end count nothing
 #pragma unroll
-    for (int h = 0; h < NV; h += kHeld) {
-      if constexpr (STAGES == 0) load_part(r, h, x, dy);
-      weight(h, g);
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        const int c = c0 + (h + i) * dc;
-        if (c < n) {
-          PX out;
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) {
-            const float d = to_f32(dy[i].v[k]), xh = (to_f32(x[i].v[k]) - m) * rs;
-            out.v[k] = from_f32<XT>(rs * (d * g[i][k] - sg - xh * sgx));
-          }
-          store_pack<XT, VEC>(p.dx + r * p.dxs + c, out);
-        }
+        for (int k = 0; k < VEC; ++k)
+          if (!cols.has(i, k)) x[i].v[k] = from_f32<XT>(0.f), dy[i].v[k] = from_f32<YT>(0.f);
+      if (r + step < p.n_rows) {
+        cols.prefetch(p.x + (r + step) * p.xs);
+        cols.prefetch(p.dy + (r + step) * p.dys);
       }
     }
+    const float2 off = make_float2(-m, -m), scale = make_float2(rs, rs);
+    float2 sg = make_float2(0.f, 0.f), sgc = sg, g[NV][VEC / 2];
+    weight(g);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (cols.has(i)) {
+#pragma unroll
+        for (int k = 0; k < VEC / 2; ++k) {
+          const float2 d = pair_f32(dy[i], k), c = __fadd2_rn(pair_f32(x[i], k), off);
+          const float2 gk = __fmul2_rn(d, g[i][k]);
+          sg = __fadd2_rn(sg, gk);
+          sgc = __ffma2_rn(gk, c, sgc);
+          dw[i][k] = __ffma2_rn(__fmul2_rn(d, scale), c, dw[i][k]);
+          db[i][k] = __fadd2_rn(db[i][k], d);
+        }
+      }
+    if (!p.dx) continue;
+    float a = sg.x + sg.y, b = sgc.x + sgc.y;
+    if constexpr (WARP) {
+      a = warp_sum(a);
+      b = warp_sum(b);
+    } else {
+      const float2 t = cta_sum2_all(a, b, s_red[turn]);
+      turn ^= 1;
+      a = t.x;
+      b = t.y;
+    }
+    a = -rs * (a * inv);
+    b = -rs * (rs * (rs * (b * inv)));
+    const float2 fa = make_float2(a, a), fb = make_float2(b, b);
+    weight(g);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (cols.has(i)) {
+        PX out;
+#pragma unroll
+        for (int k = 0; k < VEC / 2; ++k) {
+          const float2 c = __fadd2_rn(pair_f32(x[i], k), off);
+          const float2 gk = __fmul2_rn(pair_f32(dy[i], k), g[i][k]);
+          set_pair(out, k, __ffma2_rn(c, fb, __ffma2_rn(gk, scale, fa)));
+        }
+        cols.store(p.dx + r * p.dxs, i, out);
+      }
   }
   pdl_launch_dependents();
   if (!p.part) return;
   float* part = p.part + (int64_t)blockIdx.x * 2 * n;
   if constexpr (WARP) {
     // the warps' sums, added up in warp order in shared memory
-    if constexpr (STAGES > 0) copy_wait<0>();
+    copy_wait<0>();
     float* s_dw = reinterpret_cast<float*>(s_dyn);
     float* s_db = s_dw + n;
-    for (int k = 0; k < kWarps; ++k) {
+    for (int t = 0; t < kWarps; ++t) {
       __syncthreads();
-      if ((int)(threadIdx.x >> 5) != k) continue;
+      if ((int)(threadIdx.x >> 5) != t) continue;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * group + me) * VEC;
-        if (c < n) {
+      for (int i = 0; i < NV; ++i)
+        if (cols.has(i)) {
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            s_dw[c + j] = k ? s_dw[c + j] + dw[i * VEC + j] : dw[i * VEC + j];
-            s_db[c + j] = k ? s_db[c + j] + db[i * VEC + j] : db[i * VEC + j];
+          for (int k = 0; k < VEC / 2; ++k) {
+            float2* pw = reinterpret_cast<float2*>(s_dw + cols.col(i, 2 * k));
+            float2* pb = reinterpret_cast<float2*>(s_db + cols.col(i, 2 * k));
+            *pw = t ? __fadd2_rn(*pw, dw[i][k]) : dw[i][k];
+            *pb = t ? __fadd2_rn(*pb, db[i][k]) : db[i][k];
           }
         }
-      }
     }
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * n; c += kThreads) part[c] = s_dw[c];
   } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * group + me) * VEC;
-      if (c < n) {
-        Pack<float, VEC> a, b;
+    for (int i = 0; i < NV; ++i)
+      if (cols.has(i)) {
+        Pack<float, VEC> w, b;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          a.v[j] = dw[i * VEC + j];
-          b.v[j] = db[i * VEC + j];
+        for (int k = 0; k < VEC / 2; ++k) {
+          set_pair(w, k, dw[i][k]);
+          set_pair(b, k, db[i][k]);
         }
-        store_pack<float, VEC>(part + c, a);
-        store_pack<float, VEC>(part + n + c, b);
+        cols.store(part, i, w);
+        cols.store(part + n, i, b);
       }
-    }
   }
 }
 
@@ -406,11 +459,13 @@ __global__ void __launch_bounds__(kThreads) layernorm_params_part(BackwardArgs<X
   p.part[((int64_t)blockIdx.y * 2 + 1) * p.n_cols + j] = db;
 }
 
-// dweight and dbias from `parts` partial sums: 32 columns per CTA, eight
-// warps taking every eighth part, then the warps' sums in order.
-__global__ void __launch_bounds__(kThreads)
+// dweight and dbias from `parts` partial sums: 32 columns per CTA, each warp
+// taking every kSumWarps-th part, then the warps' sums in order.
+constexpr int kSumWarps = 16;
+
+__global__ void __launch_bounds__(kSumWarps * 32)
 layernorm_params_sum(int n_cols, int parts, const float* part, void* dw_out, void* db_out, int pt) {
-  __shared__ float s_part[kWarps][32];
+  __shared__ float s_part[kSumWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;  // column of {dweight, dbias}
   pdl_wait();
@@ -418,14 +473,14 @@ layernorm_params_sum(int n_cols, int parts, const float* part, void* dw_out, voi
   if (c < 2ll * n_cols) {
     const float* q = part + c;
 #pragma unroll 8
-    for (int k = warp; k < parts; k += kWarps) v += q[(int64_t)k * 2 * n_cols];
+    for (int k = warp; k < parts; k += kSumWarps) v += q[(int64_t)k * 2 * n_cols];
   }
   s_part[warp][lane] = v;
   __syncthreads();
   if (warp != 0 || c >= 2ll * n_cols) return;
   v = 0.f;
 #pragma unroll
-  for (int k = 0; k < kWarps; ++k) v += s_part[k][lane];
+  for (int k = 0; k < kSumWarps; ++k) v += s_part[k][lane];
   if (c < n_cols) {
     if (dw_out) store_from_f32(dw_out, pt, c, v);
   } else if (db_out) {
@@ -435,29 +490,35 @@ layernorm_params_sum(int n_cols, int parts, const float* part, void* dw_out, voi
 
 constexpr int kSms = 152;
 
-// How the rows of a call are cut: columns per thread (0: the long-row
-// kernels), threads, and CTAs.
-struct BackwardShape {
+// How the rows of a call are cut: a warp per row or a CTA per row, columns
+// per thread (0: rows too long for registers), threads, CTAs.
+struct RowShape {
   bool warp;
   int cols, threads, grid;
 };
 
-BackwardShape backward_shape(int64_t n_rows, int n_cols, bool aligned) {
-  BackwardShape s{};
+RowShape row_shape(int64_t n_rows, int n_cols, bool aligned) {
+  RowShape s{};
+  int per_sm = 0;  // CTAs that an SM's registers hold
+  int64_t groups = n_rows;
   if (aligned && n_cols <= 512) {
     s.warp = true;
     s.cols = n_cols <= 256 ? 8 : 16;
     s.threads = kThreads;
-    const int64_t rows = (n_rows + kWarps - 1) / kWarps;
-    s.grid = (int)(rows < 2 * kSms ? rows : 2 * kSms);
-    return s;
+    per_sm = s.cols == 8 ? 3 : 2;
+    groups = (n_rows + kWarps - 1) / kWarps;
+  } else {
+    if (aligned)
+      s.cols = n_cols <= 2048 ? 8 : n_cols <= 16 * 768 ? 16 : n_cols <= 32 * 512 ? 32 : 0;
+    else
+      s.cols = n_cols <= 2048 ? 8 : n_cols <= 16 * 512 ? 16 : n_cols <= 24 * 512 ? 24 : 0;
+    if (!s.cols) return s;
+    s.threads = ((n_cols + s.cols - 1) / s.cols + 31) / 32 * 32;
+    const int most = (!aligned ? (s.cols == 8 ? 640 : 512)
+                               : s.cols == 8 ? 1024 : s.cols == 16 ? 800 : 512) / s.threads;
+    per_sm = most < 1 ? 1 : most > 8 ? 8 : most;
   }
-  const int cols = n_cols <= 4096 ? 8 : n_cols <= 16 * 768 ? 16 : n_cols <= 32 * 512 ? 32 : 0;
-  s.cols = (!aligned && cols == 32) ? 0 : cols;
-  if (!s.cols) return s;
-  s.threads = ((n_cols + s.cols - 1) / s.cols + 31) / 32 * 32;
-  const int per_sm = s.threads >= 512 ? 1 : s.threads >= 352 ? 2 : s.threads >= 256 ? 3 : 4;
-  s.grid = (int)(n_rows < (int64_t)per_sm * kSms ? n_rows : (int64_t)per_sm * kSms);
+  s.grid = (int)(groups < (int64_t)per_sm * kSms ? groups : (int64_t)per_sm * kSms);
   return s;
 }
 
@@ -470,7 +531,7 @@ int64_t backward_workspace(int64_t n_rows, int n_cols, bool want_params) {
   if (!want_params || n_rows == 0) return 0;
   int64_t parts = kLongParts;
   for (const bool aligned : {false, true}) {
-    const BackwardShape s = backward_shape(n_rows, n_cols, aligned);
+    const RowShape s = row_shape(n_rows, n_cols, aligned);
     if (s.cols && s.grid > parts) parts = s.grid;
   }
   return parts * 2 * n_cols * 4;
@@ -496,47 +557,9 @@ bool rows_aligned(const void* p, int64_t rows, int64_t stride, int64_t size, int
   return aligned_to(p, bytes) && (rows <= 1 || (stride * size) % bytes == 0);
 }
 
-template <typename XT, typename YT, int VEC, int CPT, bool WARP>
-spmv_status forward_launch(int64_t n_rows, int n_cols, const XT* x, int64_t xs,
-                           const void* w, const void* b, int pt, float eps, YT* y, int64_t ys,
-                           float* mean, float* rstd, cudaStream_t st) {
-  const int64_t ctas = WARP ? (n_rows + kWarps - 1) / kWarps : n_rows;
-  const int grid = (int)(ctas < INT_MAX ? ctas : INT_MAX);
-  const int threads = WARP ? kThreads : ((n_cols + CPT - 1) / CPT + 31) / 32 * 32;
-  layernorm_regs<XT, YT, VEC, CPT, WARP>
-      <<<grid, threads, 0, st>>>(n_rows, n_cols, x, xs, w, b, pt, eps, y, ys, mean, rstd);
-  return launched();
-}
-
-template <typename XT, typename YT, int VEC>
-spmv_status forward(int64_t n_rows, int n_cols, const XT* x, int64_t xs, const void* w,
-                    const void* b, int pt, float eps, YT* y, int64_t ys, float* mean, float* rstd,
-                    cudaStream_t st) {
-#define SPMV_FORWARD(CPT, WARP)                                                              \
-  return forward_launch<XT, YT, VEC, CPT, WARP>(n_rows, n_cols, x, xs, w, b, pt, eps, y, ys, mean, \
-                                                rstd, st)
-  // a warp per row while a lane holds at most 32 columns (of 16 loads each
-  // where they go element by element)
-  if (n_cols <= 32 * 8) SPMV_FORWARD(8, true);
-  if (VEC > 1 && n_cols <= 32 * 32) SPMV_FORWARD(32, true);
-  if (n_cols <= 8 * 512) SPMV_FORWARD(8, false);
-  if constexpr (VEC > 1) {
-    if (n_cols <= 24 * 512) SPMV_FORWARD(24, false);
-  } else {
-    if (n_cols <= 16 * 768) SPMV_FORWARD(16, false);
-  }
-  if (n_cols <= 32 * 1024) SPMV_FORWARD(32, false);
-#undef SPMV_FORWARD
-  const int grid = (int)(n_rows < kRowGrid ? n_rows : kRowGrid);
-  layernorm_rows<XT, YT><<<grid, kThreads, 0, st>>>(n_rows, n_cols, x, xs, w, b, pt, eps, y, ys,
-                                                    mean, rstd);
-  return launched();
-}
-
-template <typename XT, typename YT, int VEC, int CPT, int STAGES, bool WARP, bool W_SMEM>
-spmv_status backward_launch(const BackwardShape& s, size_t smem, const BackwardArgs<XT, YT>& p,
-                            cudaStream_t st) {
-  const auto fn = layernorm_backward_fused<XT, YT, VEC, CPT, STAGES, WARP, W_SMEM>;
+template <typename Args>
+spmv_status launch_rows(void (*fn)(Args), const RowShape& s, size_t smem, const Args& p,
+                        cudaStream_t st) {
   if (smem > 40 * 1024 &&  // 48 KB less the static part need no opt-in
       cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
                            cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
@@ -545,46 +568,76 @@ spmv_status backward_launch(const BackwardShape& s, size_t smem, const BackwardA
   return launched();
 }
 
-template <typename XT, typename YT, int VEC, int CPT, bool WARP>
-spmv_status backward_stages(const BackwardShape& s, const BackwardArgs<XT, YT>& p,
-                            cudaStream_t st) {
+// Vectors are 16 bytes of x; rows that they do not fit take the same columns
+// per thread element by element.
+template <typename XT, typename YT, int CPT, bool WARP, bool ALIGNED>
+spmv_status forward_launch(const RowShape& s, const ForwardArgs<XT, YT>& p, cudaStream_t st) {
+  constexpr int kVec = 16 / (int)sizeof(XT);
+  // four stages of fp32 are at most 192 KB of an SM's shared memory (three of
+  // rows with 32 columns per thread)
+  constexpr int kStages = !ALIGNED ? 0 : CPT == 32 ? 3 : 4;
+  return launch_rows(layernorm_fused<XT, YT, kVec, CPT, kStages, WARP>, s,
+                     (size_t)kStages * s.threads * CPT * sizeof(XT), p, st);
+}
+
+template <typename XT, typename YT, bool ALIGNED>
+spmv_status forward(const ForwardArgs<XT, YT>& p, cudaStream_t st) {
+  RowShape s = row_shape(p.n_rows, p.n_cols, ALIGNED);
+  if constexpr (ALIGNED) {
+    if (s.cols == 32) return forward_launch<XT, YT, 32, false, true>(s, p, st);
+    if (s.warp)
+      return s.cols == 8 ? forward_launch<XT, YT, 8, true, true>(s, p, st)
+                         : forward_launch<XT, YT, 16, true, true>(s, p, st);
+  }
+  if (s.cols == 8) return forward_launch<XT, YT, 8, false, ALIGNED>(s, p, st);
+  if (s.cols == 16) return forward_launch<XT, YT, 16, false, ALIGNED>(s, p, st);
+  if constexpr (!ALIGNED)
+    if (s.cols == 24) return forward_launch<XT, YT, 24, false, false>(s, p, st);
+  s.threads = kThreads;
+  s.grid = (int)(p.n_rows < kRowGrid ? p.n_rows : kRowGrid);
+  return launch_rows(layernorm_rows<XT, YT>, s, 0, p, st);
+}
+
+template <typename XT, typename YT, int CPT, bool WARP, bool ALIGNED>
+spmv_status backward_launch(const RowShape& s, const BackwardArgs<XT, YT>& p, cudaStream_t st) {
+  constexpr int kVec = 16 / (int)sizeof(XT);
   const size_t w = (size_t)(WARP ? 32 : s.threads) * CPT * 4;  // weights
-  if constexpr (VEC == 1) {
-    return backward_launch<XT, YT, VEC, CPT, 0, WARP, true>(s, w, p, st);
+  if constexpr (!ALIGNED) {
+    return launch_rows(layernorm_backward_fused<XT, YT, kVec, CPT, 0, WARP, true>, s, w, p, st);
   } else {
     const size_t stage = (size_t)s.threads * CPT * (sizeof(XT) + sizeof(YT));
     // (a warp group's ring is larger than the two sums per column that the
     // warps leave in its place at the end)
-    const int per_sm = WARP ? 2 : (s.grid + kSms - 1) / kSms;
-    const size_t room = kSmemBudget / (size_t)per_sm;
+    const size_t room = kSmemBudget / (size_t)((s.grid + kSms - 1) / kSms);
     if constexpr (CPT < 32)
-      if (4 * stage + w <= room)
-        return backward_launch<XT, YT, VEC, CPT, 4, WARP, true>(s, 4 * stage + w, p, st);
-    if (2 * stage + w <= room)
-      return backward_launch<XT, YT, VEC, CPT, 2, WARP, true>(s, 2 * stage + w, p, st);
-    if constexpr (CPT >= 16 && !WARP)
-      return backward_launch<XT, YT, VEC, CPT, 2, WARP, false>(s, 2 * stage, p, st);
-    return SPMV_ERR_UNSUPPORTED;  // (rows of fewer columns always fit)
+      if (3 * stage + w <= room)
+        return launch_rows(layernorm_backward_fused<XT, YT, kVec, CPT, 3, WARP, true>, s,
+                           3 * stage + w, p, st);
+    if (2 * stage + w <= room || CPT == 8 || WARP)
+      return launch_rows(layernorm_backward_fused<XT, YT, kVec, CPT, 2, WARP, true>, s,
+                         2 * stage + w, p, st);
+    if constexpr (CPT > 8 && !WARP)
+      return launch_rows(layernorm_backward_fused<XT, YT, kVec, CPT, 2, WARP, false>, s,
+                         2 * stage, p, st);
+    return SPMV_ERR_UNSUPPORTED;
   }
 }
 
-template <typename XT, typename YT, int VEC>
+template <typename XT, typename YT, bool ALIGNED>
 spmv_status backward(const BackwardArgs<XT, YT>& p, void* dweight, void* dbias, cudaStream_t st) {
-  const BackwardShape s = backward_shape(p.n_rows, p.n_cols, VEC > 1);
+  const RowShape s = row_shape(p.n_rows, p.n_cols, ALIGNED);
   int parts = s.grid;
   spmv_status status = SPMV_OK;
-  if (s.cols) {
-    if (s.warp) {
-      if constexpr (VEC > 1)
-        status = s.cols == 8 ? backward_stages<XT, YT, VEC, 8, true>(s, p, st)
-                             : backward_stages<XT, YT, VEC, 16, true>(s, p, st);
-    } else if (s.cols == 8) {
-      status = backward_stages<XT, YT, VEC, 8, false>(s, p, st);
-    } else if (s.cols == 16) {
-      status = backward_stages<XT, YT, VEC, 16, false>(s, p, st);
-    } else {
-      if constexpr (VEC > 1) status = backward_stages<XT, YT, VEC, 32, false>(s, p, st);
-    }
+  if (s.warp) {
+    if constexpr (ALIGNED)
+      status = s.cols == 8 ? backward_launch<XT, YT, 8, true, true>(s, p, st)
+                           : backward_launch<XT, YT, 16, true, true>(s, p, st);
+  } else if (s.cols == 8) {
+    status = backward_launch<XT, YT, 8, false, ALIGNED>(s, p, st);
+  } else if (s.cols == 16) {
+    status = backward_launch<XT, YT, 16, false, ALIGNED>(s, p, st);
+  } else if (s.cols) {
+    status = backward_launch<XT, YT, ALIGNED ? 32 : 24, false, ALIGNED>(s, p, st);
   } else {
     const int grid = (int)(p.n_rows < kRowGrid ? p.n_rows : kRowGrid);
     parts = kLongParts;
@@ -599,7 +652,7 @@ spmv_status backward(const BackwardArgs<XT, YT>& p, void* dweight, void* dbias, 
   const float* part = p.part;
   void* args[] = {&n_cols, &parts, &part, &dweight, &dbias, &pt};
   return launch_pdl(reinterpret_cast<const void*>(&layernorm_params_sum),
-                    (int)((2ll * n_cols + 31) / 32), kThreads, 0, st, args) == 0
+                    (int)((2ll * n_cols + 31) / 32), kSumWarps * 32, 0, st, args) == 0
              ? SPMV_OK
              : SPMV_ERR_CUDA;
 }
@@ -635,17 +688,16 @@ extern "C" spmv_status spmv_layernorm(int64_t n_rows, int32_t n_cols, const void
     using XT = std::remove_pointer_t<decltype(xt)>;
     using YT = std::remove_pointer_t<decltype(yt)>;
     constexpr int kVec = 16 / (int)sizeof(XT);
-    const XT* xp = static_cast<const XT*>(x);
-    YT* yp = static_cast<YT*>(y);
+    const ForwardArgs<XT, YT> p{n_rows, n_cols, static_cast<const XT*>(x), x_stride, weight, bias,
+                                param_dtype, eps, static_cast<YT*>(y), y_stride, mean_out,
+                                rstd_out};
     // whole vectors need every row of x and y, weight and bias on vector
     // boundaries and a whole number of vectors per row
     if (n_cols % kVec == 0 && rows_aligned(x, n_rows, x_stride, xs, kVec) &&
         rows_aligned(y, n_rows, y_stride, ysz, kVec) && aligned_to(weight, 16) &&
         aligned_to(bias, 16))
-      return forward<XT, YT, kVec>(n_rows, n_cols, xp, x_stride, weight, bias, param_dtype, eps,
-                                   yp, y_stride, mean_out, rstd_out, st);
-    return forward<XT, YT, 1>(n_rows, n_cols, xp, x_stride, weight, bias, param_dtype, eps, yp,
-                              y_stride, mean_out, rstd_out, st);
+      return forward<XT, YT, true>(p, st);
+    return forward<XT, YT, false>(p, st);
   });
 }
 
@@ -700,7 +752,7 @@ extern "C" spmv_status spmv_layernorm_backward(
     if (n_cols % kVec == 0 && rows_aligned(x, n_rows, x_stride, xs, kVec) &&
         rows_aligned(dy, n_rows, dy_stride, dys, kVec) &&
         (!dx || rows_aligned(dx, n_rows, dx_stride, xs, kVec)) && aligned_to(weight, 16))
-      return backward<XT, YT, kVec>(p, dweight, dbias, st);
-    return backward<XT, YT, 1>(p, dweight, dbias, st);
+      return backward<XT, YT, true>(p, dweight, dbias, st);
+    return backward<XT, YT, false>(p, dweight, dbias, st);
   });
 }

@@ -86,51 +86,110 @@ __device__ __forceinline__ void store_pack(T* p, const Pack<T, N>& r) {
     reinterpret_cast<B*>(p)[i] = reinterpret_cast<const B*>(&r)[i];
 }
 
-// VEC elements at column c of a row of n: a vector past the end repeats the
-// last one (an unconditional load, so that loads of several vectors go out
-// together); a single element past the end is zero.
-template <typename T, int VEC>
-__device__ __forceinline__ Pack<T, VEC> load_vec(const T* row, int c, int n, bool stream) {
-  if constexpr (VEC == 1) {
-    Pack<T, VEC> r;
-    r.v[0] = from_f32<T>(0.f);
-    if (c < n) r = load_pack<T, VEC>(row + c, stream);
-    return r;
-  } else {
-    return load_pack<T, VEC>(row + min(c, n - VEC), stream);
+// ------------------------------------------------- a thread's columns of a row
+// A group of `group` threads shares a row of n columns, thread `me` holding
+// NV vectors of VEC (even) columns. ALIGNED: rows start on vector boundaries
+// and n is a multiple of VEC; vector i is VEC neighbouring columns at
+// (i * group + me) * VEC, moved as a whole. Otherwise element k of vector i
+// is column (i * VEC + k) * group + me, moved element by element, so that a
+// warp's accesses are still contiguous.
+template <int VEC, bool ALIGNED>
+struct Cols {
+  int me, group, n;
+  __device__ __forceinline__ int col(int i, int k) const {
+    return ALIGNED ? (i * group + me) * VEC + k : (i * VEC + k) * group + me;
   }
-}
-
-// A thread's columns of a vector of runtime type, as fp32: vectors of VEC
-// columns at first + i * step, i < NV (as load_vec past the end); `fill` for a null pointer. The type is tested once, so that
-// all of the loads are under way together.
-template <typename T, int NV, int VEC>
-__device__ __forceinline__ void load_cols_as(const T* p, int first, int step, int n,
-                                             float (&v)[NV][VEC]) {
-  Pack<T, VEC> r[NV];
+  // whether vector i (ALIGNED) is inside the row
+  __device__ __forceinline__ bool has(int i) const { return !ALIGNED || col(i, 0) < n; }
+  __device__ __forceinline__ bool has(int i, int k) const { return ALIGNED || col(i, k) < n; }
+  // Loads of all vectors, under way together: places past the end repeat the
+  // row's last vector or element.
+  template <typename T, int NV>
+  __device__ __forceinline__ void load(const T* row, Pack<T, VEC> (&r)[NV], bool stream) const {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) r[i] = load_vec<T, VEC>(p, first + i * step, n, false);
+    for (int i = 0; i < NV; ++i) {
+      if constexpr (ALIGNED) {
+        r[i] = load_pack<T, VEC>(row + min(col(i, 0), n - VEC), stream);
+      } else {
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+        for (int k = 0; k < VEC; ++k)
+          r[i].v[k] = load_pack<T, 1>(row + min(col(i, k), n - 1), stream).v[0];
+      }
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* row, int i, const Pack<T, VEC>& r) const {
+    if constexpr (ALIGNED) {
+      store_pack<T, VEC>(row + col(i, 0), r);
+    } else {
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) v[i][k] = to_f32(r[i].v[k]);
-}
-
-template <int NV, int VEC>
-__device__ __forceinline__ void load_cols(const void* p, int dtype, int first, int step, int n,
-                                          float fill, float (&v)[NV][VEC]) {
-  if (!p) {
+      for (int k = 0; k < VEC; ++k)
+        if (col(i, k) < n) row[col(i, k)] = r.v[k];
+    }
+  }
+  // The same columns of a vector of runtime type (a layer's parameter), in
+  // fp32; `fill` for a null pointer.
+  template <typename T, int NV>
+  __device__ __forceinline__ void load_as(const void* p, float2 (&v)[NV][VEC / 2]) const {
+    Pack<T, VEC> r[NV];
+    load<T, NV>(static_cast<const T*>(p), r, false);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) v[i][k] = fill;
-  } else if (dtype == SPMV_F32) {
-    load_cols_as<float, NV, VEC>(static_cast<const float*>(p), first, step, n, v);
-  } else if (dtype == SPMV_F16) {
-    load_cols_as<__half, NV, VEC>(static_cast<const __half*>(p), first, step, n, v);
-  } else {
-    load_cols_as<__nv_bfloat16, NV, VEC>(static_cast<const __nv_bfloat16*>(p), first, step, n, v);
+      for (int k = 0; k < VEC / 2; ++k)
+        v[i][k] = make_float2(to_f32(r[i].v[2 * k]), to_f32(r[i].v[2 * k + 1]));
   }
+  template <int NV>
+  __device__ __forceinline__ void load_param(const void* p, int dtype, float fill,
+                                             float2 (&v)[NV][VEC / 2]) const {
+    if (!p) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < VEC / 2; ++k) v[i][k] = make_float2(fill, fill);
+    } else if (dtype == SPMV_F32) {
+      load_as<float, NV>(p, v);
+    } else if (dtype == SPMV_F16) {
+      load_as<__half, NV>(p, v);
+    } else {
+      load_as<__nv_bfloat16, NV>(p, v);
+    }
+  }
+  // Ask L2 for a row (its loads come one row later).
+  template <typename T>
+  __device__ __forceinline__ void prefetch(const T* row) const {
+    for (int c = me * (int)(128 / sizeof(T)); c < n; c += group * (int)(128 / sizeof(T)))
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
+  }
+};
+
+// Elements 2k and 2k + 1 of a vector, in fp32.
+template <typename T, int N>
+__device__ __forceinline__ float2 pair_f32(const Pack<T, N>& r, int k) {
+  return make_float2(to_f32(r.v[2 * k]), to_f32(r.v[2 * k + 1]));
+}
+template <int N>
+__device__ __forceinline__ float2 pair_f32(const Pack<__nv_bfloat16, N>& r, int k) {
+  // bf16 is the upper half of an fp32
+  const uint32_t w = reinterpret_cast<const uint32_t*>(&r)[k];
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <int N>
+__device__ __forceinline__ float2 pair_f32(const Pack<__half, N>& r, int k) {
+  return __half22float2(reinterpret_cast<const __half2*>(&r)[k]);
+}
+template <int N>
+__device__ __forceinline__ void set_pair(Pack<float, N>& r, int k, float2 v) {
+  r.v[2 * k] = v.x;
+  r.v[2 * k + 1] = v.y;
+}
+template <int N>
+__device__ __forceinline__ void set_pair(Pack<__half, N>& r, int k, float2 v) {
+  reinterpret_cast<__half2*>(&r)[k] = __float22half2_rn(v);
+}
+template <int N>
+__device__ __forceinline__ void set_pair(Pack<__nv_bfloat16, N>& r, int k, float2 v) {
+  reinterpret_cast<__nv_bfloat162*>(&r)[k] = __float22bfloat162_rn(v);
 }
 
 }  // namespace

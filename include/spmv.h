@@ -590,7 +590,7 @@ int64_t spmv_adapters_workspace(int32_t n_tokens, int32_t n_slots, int32_t rank)
  * x: n_tokens x n_in of `dtype` (fp16 or bf16). a: n_slots x rank x n_in and
  * b: n_slots x n_out x rank, both contiguous and of `dtype`. ranks: n_slots
  * int32 or NULL: slot s uses the first ranks[s] rows of A_s and columns of
- * B_s (clamped to [0, rank]; the others are not read); NULL: all. scales:
+ * B_s (clamped to [0, rank]; whatever the others hold); NULL: all. scales:
  * n_slots fp32 or NULL (1). base: n_tokens x n_out of y_dtype, the shared
  * projection's output (spmv_run's y of each token), or NULL (0); y: of
  * y_dtype, which is fp32 or `dtype`. y may be base itself (same pointer and
@@ -599,7 +599,8 @@ int64_t spmv_adapters_workspace(int32_t n_tokens, int32_t n_slots, int32_t rank)
  * (NULL when that is 0); no initialisation, no meaning afterwards.
  * Errors: INVALID_ARG (sizes, null or misaligned pointers, strides,
  * overlaps, workspace too small), UNSUPPORTED (types), TOO_LARGE (rank or
- * n_slots above the limits), CUDA. */
+ * n_slots above the limits, more than 2^27 tokens, n_in or n_out above 2^30),
+ * CUDA. */
 spmv_status spmv_adapters_run(int32_t n_tokens, int32_t n_in, int32_t n_out, int32_t n_slots,
                               int32_t rank, spmv_dtype dtype, const void* x, int64_t x_stride,
                               const void* a, const void* b, const int32_t* slot_ids,

@@ -550,13 +550,6 @@ spmv_status by_types(spmv_dtype x, spmv_dtype y, F&& f) {
   return SPMV_ERR_UNSUPPORTED;
 }
 
-// Rows of a matrix that vectors of `vec` elements can be loaded from: every
-// row starts on a whole vector (of at most 16 bytes).
-bool rows_aligned(const void* p, int64_t rows, int64_t stride, int64_t size, int vec) {
-  const int64_t bytes = size * vec > 16 ? 16 : size * vec;
-  return aligned_to(p, bytes) && (rows <= 1 || (stride * size) % bytes == 0);
-}
-
 template <typename Args>
 spmv_status launch_rows(void (*fn)(Args), const RowShape& s, size_t smem, const Args& p,
                         cudaStream_t st) {

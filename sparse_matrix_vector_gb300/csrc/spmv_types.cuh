@@ -211,6 +211,13 @@ inline bool matrix_ok(const void* p, int64_t rows, int64_t cols, int64_t stride,
   return rows <= 1 || stride == 0 || rows <= (INT64_MAX / 16) / stride;
 }
 
+// Rows of a matrix that vectors of `vec` elements can be loaded from: every
+// row starts on a whole vector (of at most 16 bytes).
+inline bool rows_aligned(const void* p, int64_t rows, int64_t stride, int64_t size, int vec) {
+  const int64_t bytes = size * vec > 16 ? 16 : size * vec;
+  return aligned_to(p, bytes) && (rows <= 1 || (stride * size) % bytes == 0);
+}
+
 // Whether the bytes of two matrices' spans overlap.
 inline bool spans_overlap(const void* p, int64_t p_rows, int64_t p_cols, int64_t p_stride,
                           int64_t p_size, const void* q, int64_t q_rows, int64_t q_cols,

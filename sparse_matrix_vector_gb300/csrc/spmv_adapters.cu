@@ -46,8 +46,9 @@ struct AdapterArgs {
   int4* tiles;       // {slot or -1, first sorted position, tokens, unused}
   int32_t* n_tiles;
   int32_t* perm;     // token at each sorted position
-  float* parts;      // k_split x n_tokens (sorted) x rank partial sums of h
-  int max_tiles, k_split, o_split;
+  void* terms;       // 16-bit terms of h: [sorted position][term][term_pitch]
+  float* downs;      // what undoes their scaling, per sorted position
+  int term_pitch, max_tiles, k_split, o_split;
 };
 
 template <typename T>
@@ -110,9 +111,13 @@ __device__ __forceinline__ int rank_of(const AdapterArgs& p, int slot) {
 // range [k0, k1), in steps of 32 that start at k0 + 32 * first and are
 // 32 * step apart. Rows past the rank repeat its last row (their h is not
 // used); x[nt] is the row of this lane's token, any row where there is none.
+// `ahead`: row of the token whose lines this lane asks from L2 kAhead elements
+// before they are loaded (null: none).
+constexpr int kAhead = 512;
+
 template <typename T, int MT, int NT>
 __device__ __forceinline__ void shrink(const AdapterArgs& p, const T* a, int rank, int j0,
-                                       const T* const (&x)[NT], int k0, int k1,
+                                       const T* const (&x)[NT], const T* ahead, int k0, int k1,
                                        float (&acc)[MT][NT][4]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const T* rows[MT][2];
@@ -123,8 +128,13 @@ __device__ __forceinline__ void shrink(const AdapterArgs& p, const T* a, int ran
       rows[m][h] = a + (int64_t)min(j0 + 16 * m + 8 * h + g, rank - 1) * p.n_in + 8 * t;
   const int whole = p.vec_in ? min(k1, p.n_in / 32 * 32) : k0;
   int k = k0;
+  if (ahead)
+    for (int i = k0; i < min(k0 + kAhead, whole); i += 64)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(ahead + i));
 #pragma unroll 2
   for (; k < whole; k += 32) {
+    if (ahead && k + kAhead < whole && (k & 32) == 0)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(ahead + k + kAhead));
     uint4 v[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -192,69 +202,60 @@ __device__ __forceinline__ float split_terms(const float (&v)[SPMV_ADAPTER_MAX_R
   return down;
 }
 
-// acc[m][n]: columns o + 4 g + 2 m (and + 1) of y, tokens 8 n + 2 t (and + 1):
-// lane rows of the two 16-row tiles are laid out so that a lane ends with 4
-// neighbouring columns of each of its tokens. h: terms of 8 NT tokens,
-// `pitch_t` elements per token and `pitch_k` per term.
-template <typename T, int NT>
-__device__ __forceinline__ void expand(const AdapterArgs& p, const T* b, int rank, int nk, int o,
-                                       const T* h, int pitch_t, int pitch_k,
-                                       float (&acc)[2][NT][4]) {
+// 32 columns of B's rows o + 4 g + i, from column 32 k (zeros past the rank).
+// Lane rows of the two 16-row tiles of a step are laid out so that a lane ends
+// with 4 neighbouring columns of each of its tokens.
+template <typename T>
+__device__ __forceinline__ void load_b(const AdapterArgs& p, const T* b, int rank, int k, int o,
+                                       uint4 (&w)[4]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const T* rows[4];
+  const int left = rank - 32 * k - 8 * t;
+  const T* at = b + 32 * k + 8 * t;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    rows[i] = b + (int64_t)min(o + 4 * g + i, p.n_out - 1) * p.rank + 8 * t;
-#pragma unroll 2
-  for (int k = 0; k < nk; ++k) {
-    uint4 w[4];
-    const int left = rank - 32 * k - 8 * t;
+    w[i] = load8(at + (int64_t)min(o + 4 * g + i, p.n_out - 1) * p.rank, left, p.vec_b);
+  if (left < 8) {  // columns past the slot's rank
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = load8(rows[i] + 32 * k, left, p.vec_b);
-    if (left < 8) {  // columns past the slot's rank
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = keep8(w[i], left);
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const T* hp = h + (8 * n + g) * pitch_t + 32 * k + 8 * t;
-#pragma unroll
-      for (int q = 0; q < Terms<T>::n; ++q) {
-        const uint4 v = *reinterpret_cast<const uint4*>(hp + q * pitch_k);
-        mma32<T>(acc[0][n], w[0], w[1], v);
-        mma32<T>(acc[1][n], w[2], w[3], v);
-      }
-    }
+    for (int i = 0; i < 4; ++i) w[i] = keep8(w[i], left);
   }
 }
 
-// 4 neighbouring columns of y, `left` of which exist.
+// acc[m][n][e + 2 i]: column o + 4 g + 2 m + i of y, token 8 n + 2 t + e, over
+// the 32 inner elements of w. h: terms of 8 NT tokens at inner element 32 k,
+// `pitch_t` elements per token and `pitch_k` per term.
+template <typename T, int NT>
+__device__ __forceinline__ void expand(const uint4 (&w)[4], const T* h, int pitch_t, int pitch_k,
+                                       float (&acc)[2][NT][4]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int q = 0; q < Terms<T>::n; ++q) {
+      const uint4 v =
+          *reinterpret_cast<const uint4*>(h + (8 * n + g) * pitch_t + q * pitch_k + 8 * t);
+      mma32<T>(acc[0][n], w[0], w[1], v);
+      mma32<T>(acc[1][n], w[2], w[3], v);
+    }
+}
+
+// 4 neighbouring columns of y, `left` of which exist (the others are zero).
 template <typename YT>
-__device__ __forceinline__ float4 load_y(const YT* p, int left, bool vec) {
-  if (vec) {
-    if (left <= 0) return make_float4(0, 0, 0, 0);
-    const Pack<YT, 4> r = load_pack<YT, 4>(p, true);
-    return make_float4(to_f32(r.v[0]), to_f32(r.v[1]), to_f32(r.v[2]), to_f32(r.v[3]));
-  }
-  return make_float4(left > 0 ? to_f32(p[0]) : 0.f, left > 1 ? to_f32(p[1]) : 0.f,
-                     left > 2 ? to_f32(p[2]) : 0.f, left > 3 ? to_f32(p[3]) : 0.f);
+__device__ __forceinline__ Pack<YT, 4> load_y(const YT* p, int left, bool vec) {
+  if (vec && left > 0) return load_pack<YT, 4>(p, true);
+  Pack<YT, 4> r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = !vec && i < left ? p[i] : from_f32<YT>(0.f);
+  return r;
 }
 template <typename YT>
-__device__ __forceinline__ void store_y(YT* p, float4 v, int left, bool vec) {
+__device__ __forceinline__ void store_y(YT* p, const Pack<YT, 4>& r, int left, bool vec) {
   if (vec) {
-    if (left <= 0) return;
-    Pack<YT, 4> r;
-    r.v[0] = from_f32<YT>(v.x);
-    r.v[1] = from_f32<YT>(v.y);
-    r.v[2] = from_f32<YT>(v.z);
-    r.v[3] = from_f32<YT>(v.w);
-    store_pack<YT, 4>(p, r);
+    if (left > 0) store_pack<YT, 4>(p, r);
     return;
   }
-  if (left > 0) p[0] = from_f32<YT>(v.x);
-  if (left > 1) p[1] = from_f32<YT>(v.y);
-  if (left > 2) p[2] = from_f32<YT>(v.z);
-  if (left > 3) p[3] = from_f32<YT>(v.w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < left) p[i] = r.v[i];
 }
 
 // y = base (or 0) for columns [o0, o1) of a token, by the whole CTA.
@@ -264,40 +265,52 @@ __device__ __forceinline__ void copy_base(const AdapterArgs& p, int token, int o
   const YT* base = static_cast<const YT*>(p.base) + (p.base ? token * p.bs : 0);
   YT* y = static_cast<YT*>(p.y) + token * p.ys;
   for (int o = o0 + 4 * threadIdx.x; o < o1; o += 4 * blockDim.x)
-    store_y(y + o, p.base ? load_y(base + o, o1 - o, p.vec_y) : make_float4(0, 0, 0, 0), o1 - o,
-            p.vec_y);
+    store_y(y + o, load_y(base + o, p.base ? o1 - o : 0, p.vec_y), o1 - o, p.vec_y);
 }
 
-// Add the product to base for one step of 32 columns x 8 NT tokens and store.
+// base and y are read and written by lanes in another order than the matrix
+// instruction leaves them (lane 4 g + t -> 8 t + g): eight neighbouring lanes
+// then cover one 128-byte line of one token, not 32 bytes of each of four
+// (measured: 14 L1 wavefronts per 512-byte request before).
+// The base of one step: columns o + 4 g .. of tokens 8 n + 2 t + e.
+template <typename YT, int NT>
+__device__ __forceinline__ void load_base(const AdapterArgs& p, const int* s_token, int n_tokens,
+                                          int o, Pack<YT, 4> (&v)[NT][2]) {
+  const int lane = threadIdx.x & 31, g = lane & 7, t = lane >> 3, c = o + 4 * g;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = 8 * n + 2 * t + e;
+      const bool on = p.base && i < n_tokens;
+      v[n][e] = load_y(static_cast<const YT*>(p.base) + (on ? s_token[i] * p.bs + c : 0),
+                       on ? p.n_out - c : 0, p.vec_y);
+    }
+}
+
+// Add the product to the base and store (whole warps).
 template <typename YT, int NT>
 __device__ __forceinline__ void finish(const AdapterArgs& p, const int* s_token, int n_tokens,
                                        const float* s_down, float scale, int o,
+                                       const Pack<YT, 4> (&v)[NT][2],
                                        const float (&acc)[2][NT][4]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int c = o + 4 * g, left = p.n_out - c;
-  float4 v[NT][2];
+  const int lane = threadIdx.x & 31, g = lane & 7, t = lane >> 3, c = o + 4 * g;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int i = 8 * n + 2 * t + e;
-      v[n][e] = make_float4(0, 0, 0, 0);
-      if (p.base && i < n_tokens)
-        v[n][e] = load_y(static_cast<const YT*>(p.base) + s_token[i] * p.bs + c, left, p.vec_y);
-    }
+      float m[4];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
+      for (int k = 0; k < 4; ++k)
+        m[k] = __shfl_sync(0xffffffffu, acc[k >> 1][n][e + 2 * (k & 1)], 4 * g + t);
       const int i = 8 * n + 2 * t + e;
       if (i >= n_tokens) continue;
       const float d = s_down[i];
-      float4 r = v[n][e];
-      r.x += scale * (acc[0][n][e] * d);
-      r.y += scale * (acc[0][n][2 + e] * d);
-      r.z += scale * (acc[1][n][e] * d);
-      r.w += scale * (acc[1][n][2 + e] * d);
-      store_y(static_cast<YT*>(p.y) + s_token[i] * p.ys + c, r, left, p.vec_y);
+      Pack<YT, 4> r;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        r.v[k] = from_f32<YT>(to_f32(v[n][e].v[k]) + scale * (m[k] * d));
+      store_y(static_cast<YT*>(p.y) + s_token[i] * p.ys + c, r, p.n_out - c, p.vec_y);
     }
 }
 
@@ -305,26 +318,35 @@ constexpr int kMaxRank = SPMV_ADAPTER_MAX_RANK;
 constexpr int kPitch = kMaxRank + 8;  // 16-bit elements per token: rows on other banks
 
 // ------------------------------------------------------- few tokens (decode)
-// A cluster of CTAs per token, of which the cluster of the first of every
-// eight tokens of a slot works for all eight (a matrix instruction has eight
-// columns) and the others leave at once. Each CTA takes a share of the inner
+// Clusters of CTAs take groups of up to eight tokens of one slot (a matrix
+// instruction has eight columns) in turn; which tokens form the groups every
+// CTA finds for itself. Each CTA takes a share of the inner
 // range of A x; the shares meet in distributed shared memory; then each CTA
-// takes a share of y's columns. One launch, no workspace; what B's share will
-// need is asked from L2 at the start.
+// takes a share of y's columns. One launch, no workspace. What the second
+// product needs does not depend on the first: B's share is asked from L2 at
+// the start, and the first step's B and base are in registers before the
+// shares meet.
 constexpr int kFewTokens = 256;
 constexpr int kGroup = 8;
 
-template <typename T, int MT>
+// Shared memory of a CTA: the warps' sums of A x, later the 16-bit terms.
+template <typename T, int WARPS>
+union FewShared {
+  float warps[WARPS * kGroup * 64];
+  T h[Terms<T>::n * kGroup * kPitch];
+};
+
+template <typename T, int MT, int WARPS>
 __device__ __forceinline__ void few_shrink(const AdapterArgs& p, const T* a, int rank, int j0,
                                            const T* x, int k0, int k1, float* s_warp,
                                            float* s_part) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   // the warps' shares: neighbouring steps of 32
-  const int steps = (k1 - k0 + 31) / 32, per = (steps + kWarps - 1) / kWarps;
+  const int steps = (k1 - k0 + 31) / 32, per = (steps + WARPS - 1) / WARPS;
   const int w0 = min(k0 + warp * per * 32, k1), w1 = min(w0 + per * 32, k1);
   float acc[MT][1][4] = {};
   const T* const xs[1] = {x};
-  shrink<T, MT, 1>(p, a, rank, j0, xs, w0, w1, acc);
+  shrink<T, MT, 1>(p, a, rank, j0, xs, nullptr, w0, w1, acc);
   // [warp][token][16 MT]
   float* mine = s_warp + warp * kGroup * 16 * MT;
 #pragma unroll
@@ -333,119 +355,186 @@ __device__ __forceinline__ void few_shrink(const AdapterArgs& p, const T* a, int
     for (int e = 0; e < 4; ++e)
       mine[(2 * t + (e & 1)) * 16 * MT + 16 * m + g + 8 * (e >> 1)] = acc[m][0][e];
   __syncthreads();
-  for (int i = threadIdx.x; i < kGroup * 16 * MT; i += kThreads) {
+  for (int i = threadIdx.x; i < kGroup * 16 * MT; i += 32 * WARPS) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += s_warp[w * kGroup * 16 * MT + i];
+    for (int w = 0; w < WARPS; ++w) v += s_warp[w * kGroup * 16 * MT + i];
     const int token = i / (16 * MT), j = j0 + i % (16 * MT);
     if (j < kMaxRank) s_part[token * kMaxRank + j] = v;
   }
   __syncthreads();
 }
 
-template <typename T, typename YT>
-__global__ void __launch_bounds__(kThreads) adapters_few(AdapterArgs p) {
-  __shared__ uint32_t s_same[kFewTokens / 32];
+// The call's groups: first token of each, and how many tokens of its slot
+// stand before it. Returns their number. (Whole CTA.)
+template <int WARPS>
+__device__ __forceinline__ int few_groups(const AdapterArgs& p, int* s_ids, int2* s_group) {
+  __shared__ uint32_t s_first[kFewTokens / 32];
+  static_assert(kFewTokens <= 32 * WARPS, "a thread per token");
+  const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
+  if (i < kFewTokens) {
+    const int id = i < p.n_tokens ? p.ids[i] : 0;
+    s_ids[i] = id >= 0 && id < p.n_slots ? id : -1;
+  }
+  __syncthreads();
+  int before = 0;
+  bool first = false;
+  if (i < p.n_tokens) {
+    const int id = s_ids[i];
+    for (int j = 0; j < i; j += 4) {
+      const int4 v = *reinterpret_cast<const int4*>(s_ids + j);
+      before += (v.x == id) + (j + 1 < i && v.y == id) + (j + 2 < i && v.z == id) +
+                (j + 3 < i && v.w == id);
+    }
+    first = before % kGroup == 0;
+  }
+  const uint32_t m = __ballot_sync(0xffffffffu, first);
+  if (lane == 0 && warp < kFewTokens / 32) s_first[warp] = m;
+  __syncthreads();
+  int at = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kFewTokens / 32; ++w) {
+    const int n = __popc(s_first[w]);
+    at += w < warp ? n : w == warp ? __popc(s_first[w] & ((1u << lane) - 1)) : 0;
+    all += n;
+  }
+  if (first) s_group[at] = make_int2(i, before);
+  __syncthreads();
+  return all;
+}
+
+template <typename T, typename YT, int CTAS, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) adapters_few(AdapterArgs p) {
+  __shared__ __align__(16) int s_ids[kFewTokens];
+  __shared__ int2 s_group[kFewTokens];
   __shared__ int s_token[kGroup];
   __shared__ float s_down[kGroup];
-  __shared__ float s_warp[kWarps * kGroup * 64];
+  __shared__ __align__(16) FewShared<T, WARPS> s_mem;
   __shared__ float s_part[kGroup * kMaxRank];
-  __shared__ __align__(16) T s_h[Terms<T>::n * kGroup * kPitch];
   cg::cluster_group cluster = cg::this_cluster();
-  const int ctas = cluster.num_blocks(), cta = cluster.block_rank();
-  const int token = blockIdx.x / ctas, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int slot = p.ids[token];
-  const int o_per = (p.n_out + 32 * ctas - 1) / (32 * ctas) * 32;
+  const int cta = cluster.block_rank();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int o_per = (p.n_out + 32 * CTAS - 1) / (32 * CTAS) * 32;
   const int o0 = min(cta * o_per, p.n_out), o1 = min(o0 + o_per, p.n_out);
-  const int rank = slot >= 0 && slot < p.n_slots ? rank_of(p, slot) : 0;
-  if (rank == 0) {
-    copy_base<YT>(p, token, o0, o1);
-    return;
-  }
-  // tokens of the same slot
-  for (int i = warp; i < (p.n_tokens + 31) / 32; i += kWarps) {
-    const int at = i * 32 + lane;
-    const uint32_t m = __ballot_sync(0xffffffffu, at < p.n_tokens && p.ids[at] == slot);
-    if (lane == 0) s_same[i] = m;
-  }
-  __syncthreads();
-  int before = 0, all = 0;
-  for (int i = 0; i < (p.n_tokens + 31) / 32; ++i) {
-    const uint32_t m = s_same[i];
-    all += __popc(m);
-    before += i < token / 32 ? __popc(m)
-              : i == token / 32 ? __popc(m & ((1u << (token % 32)) - 1)) : 0;
-  }
-  if (before % kGroup) return;  // (the whole cluster)
-  const int n_tokens = min(all - before, kGroup);
-  if ((int)threadIdx.x < n_tokens) {
-    int skip = before + threadIdx.x, i = 0;
-    while (skip >= __popc(s_same[i])) skip -= __popc(s_same[i++]);
-    uint32_t m = s_same[i];
-    while (skip--) m &= m - 1;
-    s_token[threadIdx.x] = i * 32 + __ffs(m) - 1;
-  }
-  __syncthreads();
-
-  const T* b = static_cast<const T*>(p.b) + (int64_t)slot * p.n_out * p.rank;
-  if (o1 > o0) {
-    const char* from = reinterpret_cast<const char*>(b + (int64_t)o0 * p.rank);
-    const int64_t bytes = (int64_t)(o1 - o0) * p.rank * (int)sizeof(T);
-    for (int64_t i = 128ll * threadIdx.x; i < bytes; i += 128ll * kThreads)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
-  }
-  const int k_per = (p.n_in + 32 * ctas - 1) / (32 * ctas) * 32;
+  const int k_per = (p.n_in + 32 * CTAS - 1) / (32 * CTAS) * 32;
   const int k0 = min(cta * k_per, p.n_in), k1 = min(k0 + k_per, p.n_in);
-  const T* a = static_cast<const T*>(p.a) + (int64_t)slot * p.rank * p.n_in;
-  const T* x = static_cast<const T*>(p.x) + s_token[min(lane >> 2, n_tokens - 1)] * p.xs;
-  if (rank <= 16)
-    few_shrink<T, 1>(p, a, rank, 0, x, k0, k1, s_warp, s_part);
-  else if (rank <= 32)
-    few_shrink<T, 2>(p, a, rank, 0, x, k0, k1, s_warp, s_part);
-  else
-    for (int j0 = 0; j0 < rank; j0 += 64)
-      few_shrink<T, 4>(p, a, rank, j0, x, k0, k1, s_warp, s_part);
-  cluster.sync();
-  const int nk = (rank + 31) / 32;
-  if (warp < n_tokens) {  // a warp per token: its h over the cluster's shares
-    float v[kMaxRank / 32];
-#pragma unroll
-    for (int i = 0; i < kMaxRank / 32; ++i) {
-      v[i] = 0.f;
-      if (i < nk && i * 32 + lane < rank)
-        for (int c = 0; c < ctas; ++c)
-          v[i] += cluster.map_shared_rank(s_part, c)[warp * kMaxRank + i * 32 + lane];
+  const int groups = few_groups<WARPS>(p, s_ids, s_group);
+  // every CTA of a cluster goes through the same groups
+  for (int q = blockIdx.x / CTAS; q < groups; q += gridDim.x / CTAS) {
+    const int2 group = s_group[q];
+    const int slot = s_ids[group.x];
+    const int rank = slot >= 0 ? rank_of(p, slot) : 0;
+    // the group's tokens: the first of them and the next seven of its slot
+    int n_tokens = 0;
+    for (int i = group.x / 32 * 32; i < p.n_tokens && n_tokens < kGroup; i += 32) {
+      const int at = i + lane;
+      const uint32_t m =
+          __ballot_sync(0xffffffffu, at >= group.x && at < p.n_tokens && s_ids[at] == slot);
+      const int place = n_tokens + __popc(m & ((1u << lane) - 1));
+      if (warp == 0 && (m >> lane & 1) && place < kGroup) s_token[place] = at;
+      n_tokens += __popc(m);
     }
-    const float down = split_terms<T>(v, nk, s_h + warp * kPitch, kGroup * kPitch);
-    if (lane == 0) s_down[warp] = down;
-  } else {  // columns of the matrix instruction that no token has
-    for (int k = 0; k < Terms<T>::n; ++k)
-      for (int j = lane; j < kPitch; j += 32)
-        s_h[(k * kGroup + warp) * kPitch + j] = from_f32<T>(0.f);
+    n_tokens = min(n_tokens, kGroup);
+    if (rank == 0) {
+      __syncthreads();
+      for (int k = 0; k < n_tokens; ++k) copy_base<YT>(p, s_token[k], o0, o1);
+      __syncthreads();
+      continue;
+    }
+    const T* b = static_cast<const T*>(p.b) + (int64_t)slot * p.n_out * p.rank;
+    if (o1 > o0) {
+      const char* from = reinterpret_cast<const char*>(b + (int64_t)o0 * p.rank);
+      const int64_t bytes = (int64_t)(o1 - o0) * p.rank * (int)sizeof(T);
+      for (int64_t i = 128ll * threadIdx.x; i < bytes; i += 128ll * 32 * WARPS)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
+    }
+    __syncthreads();
+    const T* a = static_cast<const T*>(p.a) + (int64_t)slot * p.rank * p.n_in;
+    const T* x = static_cast<const T*>(p.x) + s_token[min(lane >> 2, n_tokens - 1)] * p.xs;
+    if (rank <= 16)
+      few_shrink<T, 1, WARPS>(p, a, rank, 0, x, k0, k1, s_mem.warps, s_part);
+    else if (rank <= 32)
+      few_shrink<T, 2, WARPS>(p, a, rank, 0, x, k0, k1, s_mem.warps, s_part);
+    else
+      for (int j0 = 0; j0 < rank; j0 += 64)
+        few_shrink<T, 4, WARPS>(p, a, rank, j0, x, k0, k1, s_mem.warps, s_part);
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    const int nk = (rank + 31) / 32;
+    int o = o0 + 32 * warp;
+    uint4 w0[4], w1[4];
+    Pack<YT, 4> v[1][2];
+    if (o < o1) {
+      load_b(p, b, rank, 0, o, w0);
+      if (nk > 1) load_b(p, b, rank, 1, o, w1);
+      load_base<YT, 1>(p, s_token, n_tokens, o, v);
+    }
+    const float scale = p.scales ? p.scales[slot] : 1.f;
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (warp < n_tokens) {  // a warp per token: its h over the cluster's shares
+      float h[kMaxRank / 32];
+#pragma unroll
+      for (int i = 0; i < kMaxRank / 32; ++i) {
+        h[i] = 0.f;
+        if (i < nk && i * 32 + lane < rank) {
+          float part[CTAS];
+#pragma unroll
+          for (int c = 0; c < CTAS; ++c)
+            part[c] = cluster.map_shared_rank(s_part, c)[warp * kMaxRank + i * 32 + lane];
+#pragma unroll
+          for (int c = 0; c < CTAS; ++c) h[i] += part[c];
+        }
+      }
+      const float down = split_terms<T>(h, nk, s_mem.h + warp * kPitch, kGroup * kPitch);
+      if (lane == 0) s_down[warp] = down;
+    } else if (warp < kGroup) {  // columns of the matrix instruction that no token has
+      for (int k = 0; k < Terms<T>::n; ++k)
+        for (int j = lane; j < kPitch; j += 32)
+          s_mem.h[(k * kGroup + warp) * kPitch + j] = from_f32<T>(0.f);
+    }
+    __syncthreads();
+    // the others may still read this CTA's share: its memory changes after them
+    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+    while (o < o1) {
+      float acc[2][1][4] = {};
+      expand<T, 1>(w0, s_mem.h, kPitch, kGroup * kPitch, acc);
+      if (nk > 1) expand<T, 1>(w1, s_mem.h + 32, kPitch, kGroup * kPitch, acc);
+      for (int k = 2; k < nk; ++k) {
+        load_b(p, b, rank, k, o, w0);
+        expand<T, 1>(w0, s_mem.h + 32 * k, kPitch, kGroup * kPitch, acc);
+      }
+      finish<YT, 1>(p, s_token, n_tokens, s_down, scale, o, v, acc);
+      o += 32 * WARPS;
+      if (o < o1) {
+        load_b(p, b, rank, 0, o, w0);
+        if (nk > 1) load_b(p, b, rank, 1, o, w1);
+        load_base<YT, 1>(p, s_token, n_tokens, o, v);
+      }
+    }
+    __syncthreads();
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   }
-  __syncthreads();
-  // the others may still read this CTA's share: its memory goes after them
-  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-  const float scale = p.scales ? p.scales[slot] : 1.f;
-  for (int o = o0 + 32 * warp; o < o1; o += 32 * kWarps) {
-    float acc[2][1][4] = {};
-    expand<T, 1>(p, b, rank, nk, o, s_h, kPitch, kGroup * kPitch, acc);
-    finish<YT, 1>(p, s_token, n_tokens, s_down, scale, o, acc);
-  }
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// Nothing to add: a CTA per token.
+template <typename YT>
+__global__ void __launch_bounds__(kThreads) adapters_copy(AdapterArgs p) {
+  copy_base<YT>(p, blockIdx.x, 0, p.n_out);
 }
 
 // --------------------------------------------------- many tokens (prompts)
 // Tokens are first sorted by slot and cut into tiles of one slot's tokens;
-// then A x per tile and share of the inner range, and y per tile and share of
-// the columns.
+// then A x per tile, by a cluster whose CTAs take shares of the inner range
+// and meet in distributed shared memory; then y per tile and share of the
+// columns.
 constexpr int kTile = 64;
 constexpr int kSortThreads = 1024;
+constexpr int kMaxSplit = 8;  // shares of the inner range: a portable cluster
 
 __global__ void __launch_bounds__(kSortThreads) adapters_sort(AdapterArgs p) {
   extern __shared__ int s_count[];  // per slot, the tokens without one last
   __shared__ int2 s_warp[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = p.n_slots + 1;
+  pdl_launch_dependents();
   for (int i = threadIdx.x; i < n; i += kSortThreads) s_count[i] = 0;
   __syncthreads();
   const auto slot_at = [&](int i) {
@@ -454,6 +543,7 @@ __global__ void __launch_bounds__(kSortThreads) adapters_sort(AdapterArgs p) {
   };
   // one atomic for the lanes of a warp that share a slot
   const int rounds = (p.n_tokens + kSortThreads - 1) / kSortThreads;
+#pragma unroll 4
   for (int q = 0; q < rounds; ++q) {
     const int i = q * kSortThreads + threadIdx.x;
     const int s = i < p.n_tokens ? slot_at(i) : -1;
@@ -501,19 +591,19 @@ __global__ void __launch_bounds__(kSortThreads) adapters_sort(AdapterArgs p) {
 }
 
 // Warps of a CTA: two halves of the tile's tokens times four shares of the
-// CTA's inner range.
+// CTA's inner range, or eight shares where the tile has half its tokens at
+// most. The sums go to s_sum, [token][sum_pitch].
 template <typename T, int MT>
 __device__ __forceinline__ void tile_shrink(const AdapterArgs& p, const T* a, int rank, int j0,
-                                            const T* const (&x)[4], int n_tokens, int start,
-                                            int split, int k0, int k1, float* s_sum) {
+                                            const T* const (&x)[4], const T* ahead, int halves,
+                                            int k0, int k1, float* s_sum, int sum_pitch) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int half = warp & 1, share = warp >> 1;
-  const int steps = (k1 - k0 + 31) / 32, per = (steps + 3) / 4;
+  const int half = warp % halves, share = warp / halves, shares = kWarps / halves;
+  const int steps = (k1 - k0 + 31) / 32, per = (steps + shares - 1) / shares;
   const int w0 = min(k0 + share * per * 32, k1), w1 = min(w0 + per * 32, k1);
   float acc[MT][4][4] = {};
-  if (half * 32 < n_tokens) shrink<T, MT, 4>(p, a, rank, j0, x, w0, w1, acc);
-  // s_sum: [token][16 MT], added up share by share
-  for (int s = 0; s < 4; ++s) {
+  shrink<T, MT, 4>(p, a, rank, j0, x, ahead, w0, w1, acc);
+  for (int s = 0; s < shares; ++s) {
     if (share == s) {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
@@ -521,28 +611,27 @@ __device__ __forceinline__ void tile_shrink(const AdapterArgs& p, const T* a, in
         for (int n = 0; n < 4; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float* at = s_sum + (32 * half + 8 * n + 2 * t + (e & 1)) * (16 * MT + 1) + 16 * m +
+            float* at = s_sum + (32 * half + 8 * n + 2 * t + (e & 1)) * sum_pitch + j0 + 16 * m +
                         g + 8 * (e >> 1);
             *at = s ? *at + acc[m][n][e] : acc[m][n][e];
           }
     }
     __syncthreads();
   }
-  const int width = min(16 * MT, rank - j0);
-  for (int i = threadIdx.x; i < n_tokens * width; i += kThreads) {
-    const int token = i / width, j = i % width;
-    p.parts[((int64_t)split * p.n_tokens + start + token) * p.rank + j0 + j] =
-        s_sum[token * (16 * MT + 1) + j];
-  }
-  __syncthreads();
 }
 
-template <typename T>
+// Columns of a token's sums: whole blocks of 16 MT, on other banks.
+constexpr int sum_pitch_of(int rank) {
+  return (rank <= 16 ? 16 : rank <= 32 ? 32 : (rank + 63) / 64 * 64) + 4;
+}
+
+template <typename T, bool WIDE>  // WIDE: ranks above 32
 __global__ void __launch_bounds__(kThreads, 2) adapters_shrink(AdapterArgs p) {
-  __shared__ float s_sum[kTile * 65];
+  extern __shared__ float s_sum[];  // kTile x sum_pitch_of(p.rank)
+  pdl_launch_dependents();
   pdl_wait();
   const int split = blockIdx.x % p.k_split, i = blockIdx.x / p.k_split;
-  if (i >= *p.n_tiles) return;
+  if (i >= *p.n_tiles) return;  // (the whole cluster, here and below)
   const int4 tile = p.tiles[i];
   if (tile.x < 0) return;
   const int rank = rank_of(p, tile.x);
@@ -550,30 +639,65 @@ __global__ void __launch_bounds__(kThreads, 2) adapters_shrink(AdapterArgs p) {
   const int k_per = (p.n_in + 32 * p.k_split - 1) / (32 * p.k_split) * 32;
   const int k0 = min(split * k_per, p.n_in), k1 = min(k0 + k_per, p.n_in);
   const T* a = static_cast<const T*>(p.a) + (int64_t)tile.x * p.rank * p.n_in;
-  const int g = (threadIdx.x & 31) >> 2, half = (threadIdx.x >> 5) & 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
+  const int pitch = sum_pitch_of(p.rank), halves = tile.z > 32 ? 2 : 1;
+  const auto row = [&](int k) {
+    return static_cast<const T*>(p.x) + p.perm[tile.y + min(k, tile.z - 1)] * p.xs;
+  };
+  const int first = 32 * (warp % halves);
   const T* x[4];
 #pragma unroll
-  for (int n = 0; n < 4; ++n)
-    x[n] = static_cast<const T*>(p.x) +
-           p.perm[tile.y + min(32 * half + 8 * n + g, tile.z - 1)] * p.xs;
+  for (int n = 0; n < 4; ++n) x[n] = row(first + 8 * n + g);
+  const T* ahead = first + lane < tile.z ? row(first + lane) : nullptr;
   if (rank <= 16)
-    tile_shrink<T, 1>(p, a, rank, 0, x, tile.z, tile.y, split, k0, k1, s_sum);
+    tile_shrink<T, 1>(p, a, rank, 0, x, ahead, halves, k0, k1, s_sum, pitch);
   else if (rank <= 32)
-    tile_shrink<T, 2>(p, a, rank, 0, x, tile.z, tile.y, split, k0, k1, s_sum);
-  else
-    for (int j0 = 0; j0 < rank; j0 += 64)
-      tile_shrink<T, 4>(p, a, rank, j0, x, tile.z, tile.y, split, k0, k1, s_sum);
-  pdl_launch_dependents();
+    tile_shrink<T, 2>(p, a, rank, 0, x, ahead, halves, k0, k1, s_sum, pitch);
+  if constexpr (WIDE)
+    if (rank > 32)
+      for (int j0 = 0; j0 < rank; j0 += 64)
+        tile_shrink<T, 4>(p, a, rank, j0, x, j0 ? nullptr : ahead, halves, k0, k1, s_sum, pitch);
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  // a warp per token: its h over the cluster's shares, as 16-bit terms
+  const int nk = (rank + 31) / 32;
+  for (int k = split * kWarps + warp; k < tile.z; k += p.k_split * kWarps) {
+    float h[kMaxRank / 32];
+#pragma unroll
+    for (int q = 0; q < kMaxRank / 32; ++q) {
+      h[q] = 0.f;
+      if (q < nk && q * 32 + lane < rank) {
+        float part[kMaxSplit];
+#pragma unroll
+        for (int c = 0; c < kMaxSplit; ++c)
+          part[c] = c < p.k_split ? cluster.map_shared_rank(s_sum, c)[k * pitch + q * 32 + lane]
+                                  : 0.f;
+#pragma unroll
+        for (int c = 0; c < kMaxSplit; ++c) h[q] += part[c];
+      }
+    }
+    T* out = static_cast<T*>(p.terms) + (int64_t)(tile.y + k) * Terms<T>::n * p.term_pitch;
+    const float down = split_terms<T>(h, nk, out, p.term_pitch);
+    if (lane == 0) p.downs[tile.y + k] = down;
+  }
+  cluster.sync();  // no CTA leaves while another reads its sums
+}
+
+// Elements from token to token in shared memory: 64 bytes past a multiple of
+// 128, so that the two rows of a quarter-warp's 16-byte loads do not meet.
+template <typename T>
+__host__ __device__ constexpr int pitch_of(int row) {
+  return row * (int)sizeof(T) % 128 == 64 ? row : row + 64 / (int)sizeof(T);
 }
 
 template <typename T, typename YT>
 __global__ void __launch_bounds__(kThreads, 2) adapters_expand(AdapterArgs p) {
   extern __shared__ __align__(16) unsigned char s_dyn[];
-  T* s_h = reinterpret_cast<T*>(s_dyn);  // [term][token][pitch]
+  T* s_h = reinterpret_cast<T*>(s_dyn);  // [token][term][term_pitch]
   __shared__ int s_token[kTile];
   __shared__ float s_down[kTile];
   const int split = blockIdx.x % p.o_split, i = blockIdx.x / p.o_split;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   pdl_wait();
   if (i >= *p.n_tiles) return;
   const int4 tile = p.tiles[i];
@@ -584,30 +708,42 @@ __global__ void __launch_bounds__(kThreads, 2) adapters_expand(AdapterArgs p) {
     for (int k = 0; k < tile.z; ++k) copy_base<YT>(p, p.perm[tile.y + k], o0, o1);
     return;
   }
-  const int nk = (rank + 31) / 32, pitch = 32 * ((p.rank + 31) / 32) + 8;
-  if (threadIdx.x < kTile)
-    s_token[threadIdx.x] = p.perm[tile.y + min((int)threadIdx.x, tile.z - 1)];
-  for (int k = warp; k < kTile; k += kWarps) {
-    float v[kMaxRank / 32];
-#pragma unroll
-    for (int q = 0; q < kMaxRank / 32; ++q) {
-      v[q] = 0.f;
-      if (q < nk && q * 32 + lane < rank && k < tile.z)
-        for (int s = 0; s < p.k_split; ++s)
-          v[q] += p.parts[((int64_t)s * p.n_tokens + tile.y + k) * p.rank + q * 32 + lane];
-    }
-    const float down = split_terms<T>(v, nk, s_h + k * pitch, kTile * pitch);
-    if (lane == 0) s_down[k] = down;
+  const int nk = (rank + 31) / 32, row = Terms<T>::n * p.term_pitch, pitch = pitch_of<T>(row);
+  if ((int)threadIdx.x < kTile) {
+    const int k = tile.y + min((int)threadIdx.x, tile.z - 1);
+    s_token[threadIdx.x] = p.perm[k];
+    s_down[threadIdx.x] = p.downs[k];
+  }
+  // terms of the tile's tokens (places past them repeat the last token's)
+  const T* terms = static_cast<const T*>(p.terms) + (int64_t)tile.y * row;
+  for (int k = threadIdx.x; k < kTile * row / 8; k += kThreads) {
+    const int token = k / (row / 8), c = k % (row / 8) * 8;
+    *reinterpret_cast<uint4*>(s_h + token * pitch + c) =
+        *reinterpret_cast<const uint4*>(terms + (int64_t)min(token, tile.z - 1) * row + c);
   }
   __syncthreads();
   const T* b = static_cast<const T*>(p.b) + (int64_t)tile.x * p.n_out * p.rank;
   const float scale = p.scales ? p.scales[tile.x] : 1.f;
-  const int half = warp & 1;
-  if (32 * half >= tile.z) return;
-  for (int o = o0 + 32 * (warp >> 1); o < o1; o += 32 * kWarps / 2) {
+  // two halves of the tile's tokens times four blocks of 32 columns, or eight
+  // blocks where the tile has half its tokens at most
+  const int halves = tile.z > 32 ? 2 : 1, half = warp % halves, n_tokens = tile.z - 32 * half;
+  const T* h = s_h + 32 * half * pitch;
+  const int step = 32 * kWarps / halves, lane = threadIdx.x & 31;
+  const YT* ahead = p.base && lane < n_tokens
+                        ? static_cast<const YT*>(p.base) + s_token[32 * half + lane] * p.bs
+                        : nullptr;
+  for (int o = o0 + 32 * (warp / halves); o < o1; o += step) {
+    Pack<YT, 4> v[4][2];
+    load_base<YT, 4>(p, s_token + 32 * half, n_tokens, o, v);
+    if (ahead && o + step < o1)  // this warp's next columns, from L2
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(ahead + o + step));
     float acc[2][4][4] = {};
-    expand<T, 4>(p, b, rank, nk, o, s_h + 32 * half * pitch, pitch, kTile * pitch, acc);
-    finish<YT, 4>(p, s_token + 32 * half, tile.z - 32 * half, s_down + 32 * half, scale, o, acc);
+    for (int k = 0; k < nk; ++k) {
+      uint4 w[4];
+      load_b(p, b, rank, k, o, w);
+      expand<T, 4>(w, h + 32 * k, pitch, p.term_pitch, acc);
+    }
+    finish<YT, 4>(p, s_token + 32 * half, n_tokens, s_down + 32 * half, scale, o, v, acc);
   }
 }
 
@@ -615,44 +751,71 @@ constexpr int kMaxTokens = 1 << 27, kMaxWidth = 1 << 30;  // (32-bit grids and c
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
-// Workspace of the sorted path: tile count, tiles, sorted tokens, partial h.
+// Workspace of the sorted path: tile count, tiles, sorted tokens, h.
 struct Workspace {
-  int64_t tiles, perm, parts, bytes;
-  int max_tiles, k_split;
+  int64_t tiles, perm, downs, terms, bytes;
+  int max_tiles, k_split, term_pitch;
 };
 
 Workspace workspace_of(int n_tokens, int n_slots, int rank) {
   Workspace w{};
   if (n_tokens <= kFewTokens || n_slots == 0 || rank == 0) return w;
   w.max_tiles = n_tokens / kTile + (n_slots + 1 < n_tokens ? n_slots + 1 : n_tokens);
+  // CTAs for two waves of the device's SMs, with tiles as full as can be
   const int tiles = (n_tokens + kTile - 1) / kTile;
-  w.k_split = tiles >= 304 ? 1 : (304 + tiles - 1) / tiles;
-  if (w.k_split > 8) w.k_split = 8;
+  w.k_split = 1;
+  while (w.k_split < kMaxSplit && tiles * w.k_split < 2 * 152) w.k_split *= 2;
+  w.term_pitch = (rank + 31) / 32 * 32;
   w.tiles = 16;
   w.perm = round_up(w.tiles + 16ll * w.max_tiles, 128);
-  w.parts = round_up(w.perm + 4ll * n_tokens, 128);
-  w.bytes = w.parts + 4ll * w.k_split * n_tokens * rank;
+  w.downs = round_up(w.perm + 4ll * n_tokens, 128);
+  w.terms = round_up(w.downs + 4ll * n_tokens, 128);
+  w.bytes = w.terms + 2ll * Terms<__nv_bfloat16>::n * w.term_pitch * n_tokens;
   return w;
+}
+
+int launch_cluster(const void* fn, int grid, int block, size_t smem, int cluster, bool pdl,
+                   cudaStream_t st, void** args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelExC(&cfg, fn, args) == cudaSuccess ? 0 : -1;
+}
+
+bool allow_smem(const void* fn, size_t bytes) {
+  return bytes <= 40 * 1024 ||  // 48 KB less the static part need no opt-in
+         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
+             cudaSuccess;
 }
 
 template <typename T, typename YT>
 spmv_status run_few(AdapterArgs& p, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  const int ctas = 8;
-  cfg.gridDim = dim3((unsigned)(p.n_tokens * ctas));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   void* args[] = {&p};
-  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&adapters_few<T, YT>), args) ==
-                 cudaSuccess
-             ? SPMV_OK
-             : SPMV_ERR_CUDA;
+  // groups, at most: each slot's tokens in eights, and so those without one
+  const int most = p.n_tokens / kGroup + p.n_slots + 1;
+  const int groups = p.n_tokens < most ? p.n_tokens : most;
+  int e;
+  if (groups <= 9) {  // clusters of 16 while there are SMs for all of them
+    const void* fn = reinterpret_cast<const void*>(&adapters_few<T, YT, 16, 16>);
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      return SPMV_ERR_CUDA;
+    e = launch_cluster(fn, groups * 16, 512, 0, 16, false, st, args);
+  } else {  // at most two waves of two CTAs per SM
+    const int clusters = groups < 76 ? groups : 76;
+    e = launch_cluster(reinterpret_cast<const void*>(&adapters_few<T, YT, 8, 8>), clusters * 8,
+                       256, 0, 8, false, st, args);
+  }
+  return e == 0 ? SPMV_OK : SPMV_ERR_CUDA;
 }
 
 template <typename T, typename YT>
@@ -662,32 +825,32 @@ spmv_status run_many(AdapterArgs& p, cudaStream_t st) {
   p.o_split = (912 + tiles - 1) / tiles;
   p.o_split = p.o_split < 1 ? 1 : p.o_split > most ? most : p.o_split;
   const size_t sort_smem = (size_t)(p.n_slots + 1) * 4;
-  const size_t expand_smem =
-      (size_t)Terms<T>::n * kTile * (32 * ((p.rank + 31) / 32) + 8) * sizeof(T);
+  const size_t shrink_smem = (size_t)kTile * sum_pitch_of(p.rank) * 4;
+  const size_t expand_smem = (size_t)kTile * pitch_of<T>(Terms<T>::n * p.term_pitch) * sizeof(T);
+  const void* shrink_fn = p.rank > 32 ? reinterpret_cast<const void*>(&adapters_shrink<T, true>)
+                                      : reinterpret_cast<const void*>(&adapters_shrink<T, false>);
+  const void* expand_fn = reinterpret_cast<const void*>(&adapters_expand<T, YT>);
   if ((int64_t)p.max_tiles * p.o_split > INT_MAX) return SPMV_ERR_TOO_LARGE;
-  if ((sort_smem > 40 * 1024 &&
-       cudaFuncSetAttribute(reinterpret_cast<const void*>(&adapters_sort),
-                            cudaFuncAttributeMaxDynamicSharedMemorySize,
-                            (int)sort_smem) != cudaSuccess) ||
-      (expand_smem > 40 * 1024 &&
-       cudaFuncSetAttribute(reinterpret_cast<const void*>(&adapters_expand<T, YT>),
-                            cudaFuncAttributeMaxDynamicSharedMemorySize,
-                            (int)expand_smem) != cudaSuccess))
+  if (!allow_smem(reinterpret_cast<const void*>(&adapters_sort), sort_smem) ||
+      !allow_smem(shrink_fn, shrink_smem) || !allow_smem(expand_fn, expand_smem))
     return SPMV_ERR_CUDA;
   adapters_sort<<<1, kSortThreads, sort_smem, st>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SPMV_ERR_CUDA;
   void* args[] = {&p};
-  if (launch_pdl(reinterpret_cast<const void*>(&adapters_shrink<T>), p.max_tiles * p.k_split,
-                 kThreads, 0, st, args) != 0 ||
-      launch_pdl(reinterpret_cast<const void*>(&adapters_expand<T, YT>), p.max_tiles * p.o_split,
-                 kThreads, expand_smem, st, args) != 0)
+  if (launch_cluster(shrink_fn, p.max_tiles * p.k_split, kThreads, shrink_smem, p.k_split, true,
+                     st, args) != 0 ||
+      launch_pdl(expand_fn, p.max_tiles * p.o_split, kThreads, expand_smem, st, args) != 0)
     return SPMV_ERR_CUDA;
   return SPMV_OK;
 }
 
 template <typename T, typename YT>
 spmv_status run(AdapterArgs& p, cudaStream_t st) {
-  return p.n_tokens <= kFewTokens || !p.parts ? run_few<T, YT>(p, st) : run_many<T, YT>(p, st);
+  if (p.n_slots == 0) {
+    if (p.base != p.y) adapters_copy<YT><<<p.n_tokens, kThreads, 0, st>>>(p);
+    return cudaGetLastError() == cudaSuccess ? SPMV_OK : SPMV_ERR_CUDA;
+  }
+  return p.n_tokens <= kFewTokens ? run_few<T, YT>(p, st) : run_many<T, YT>(p, st);
 }
 
 }  // namespace
@@ -749,8 +912,9 @@ extern "C" spmv_status spmv_adapters_run(int32_t n_tokens, int32_t n_in, int32_t
     p.n_tiles = reinterpret_cast<int32_t*>(at);
     p.tiles = reinterpret_cast<int4*>(at + w.tiles);
     p.perm = reinterpret_cast<int32_t*>(at + w.perm);
-    p.parts = reinterpret_cast<float*>(at + w.parts);
-    p.max_tiles = w.max_tiles, p.k_split = w.k_split;
+    p.downs = reinterpret_cast<float*>(at + w.downs);
+    p.terms = at + w.terms;
+    p.max_tiles = w.max_tiles, p.k_split = w.k_split, p.term_pitch = w.term_pitch;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == SPMV_F16)

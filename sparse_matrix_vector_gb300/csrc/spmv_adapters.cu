@@ -39,7 +39,7 @@ struct AdapterArgs {
   int64_t bs;
   void* y;
   int64_t ys;
-  bool vec_in;   // rows of x and A: 16-byte aligned, n_in a multiple of 8
+  int vec_in;    // rows of x and A, and n_in: 0 any, 1 whole 16 bytes, 2 whole 32 bytes
   bool vec_b;    // rows of B: the same, with rank
   bool vec_y;    // rows of base and y: 4 elements aligned, n_out a multiple of 4
   // grouped tokens (workspace)
@@ -48,7 +48,7 @@ struct AdapterArgs {
   int32_t* perm;     // token at each sorted position
   void* terms;       // 16-bit terms of h: [sorted position][term][term_pitch]
   float* downs;      // what undoes their scaling, per sorted position
-  int term_pitch, max_tiles, k_split, o_split;
+  int term_pitch, max_tiles, k_split;
 };
 
 template <typename T>
@@ -95,6 +95,39 @@ __device__ __forceinline__ uint4 load8(const T* p, int left, bool vec) {
   return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
 }
 
+// 16 elements (32 bytes, aligned to it) in one load: a quarter-warp then
+// covers two whole 128-byte lines.
+struct Vec16 {
+  uint32_t w[8];
+};
+__device__ __forceinline__ Vec16 load16(const void* p) {
+  Vec16 r;
+  asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]),
+                 "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7])
+               : "l"(p));
+  return r;
+}
+// c += rows x columns over 64 inner elements.
+template <typename T>
+__device__ __forceinline__ void mma64(float (&c)[4], const Vec16& lo, const Vec16& hi,
+                                      const Vec16& v) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    mma(static_cast<const T*>(nullptr), c, lo.w[i], hi.w[i], lo.w[i + 1], hi.w[i + 1], v.w[i],
+        v.w[i + 1]);
+}
+
+// Ask L2 for `rows` rows of `bytes` bytes, `pitch` bytes apart, by the whole
+// CTA: memory is at work on all of them before the first load waits.
+__device__ __forceinline__ void prefetch_rows(const void* p, int rows, int64_t pitch,
+                                              int64_t bytes) {
+  const int lines = (int)((bytes + 127) / 128);
+  for (int i = threadIdx.x; i < rows * lines; i += blockDim.x)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p) +
+                                                  (i / lines) * pitch + (i % lines) * 128));
+}
+
 // The first `left` of 8 elements, zeros in place of the others.
 __device__ __forceinline__ uint4 keep8(uint4 v, int left) {
   const auto word = [&](uint32_t w, int i) {
@@ -108,11 +141,10 @@ __device__ __forceinline__ int rank_of(const AdapterArgs& p, int slot) {
 }
 
 // acc[mt][nt] += rows j0 + 16 mt .. of A times tokens 8 nt .. over the inner
-// range [k0, k1), in steps of 32 that start at k0 + 32 * first and are
-// 32 * step apart. Rows past the rank repeat its last row (their h is not
-// used); x[nt] is the row of this lane's token, any row where there is none.
-// `ahead`: row of the token whose lines this lane asks from L2 kAhead elements
-// before they are loaded (null: none).
+// range [k0, k1), k0 a multiple of 64. Rows past the rank repeat its last row
+// (their h is not used); x[nt] is the row of this lane's token, any row where
+// there is none. `ahead`: row of the token whose lines this lane asks from L2
+// kAhead elements before they are loaded (null: none).
 constexpr int kAhead = 512;
 
 template <typename T, int MT, int NT>
@@ -125,43 +157,70 @@ __device__ __forceinline__ void shrink(const AdapterArgs& p, const T* a, int ran
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      rows[m][h] = a + (int64_t)min(j0 + 16 * m + 8 * h + g, rank - 1) * p.n_in + 8 * t;
-  const int whole = p.vec_in ? min(k1, p.n_in / 32 * 32) : k0;
+      rows[m][h] = a + (int64_t)min(j0 + 16 * m + 8 * h + g, rank - 1) * p.n_in;
   int k = k0;
   if (ahead)
-    for (int i = k0; i < min(k0 + kAhead, whole); i += 64)
+    for (int i = k0; i < min(k0 + kAhead, k1); i += 64)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(ahead + i));
+  const auto ask = [&] {
+    if (ahead && k + kAhead < k1)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(ahead + k + kAhead));
+  };
+  if constexpr (MT * NT < 16) {  // (more would not fit the registers)
+    const int whole = p.vec_in == 2 ? k0 + max(min(k1, p.n_in) - k0, 0) / 64 * 64 : k0;
+    for (; k < whole; k += 64) {
+      ask();
+      Vec16 v[NT], w[MT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) v[n] = load16(x[n] + k + 16 * t);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) w[m][h] = load16(rows[m][h] + k + 16 * t);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma64<T>(acc[m][n], w[m][0], w[m][1], v[n]);
+    }
+  }
+  const int whole = p.vec_in ? k0 + max(min(k1, p.n_in) - k0, 0) / 32 * 32 : k0;
 #pragma unroll 2
   for (; k < whole; k += 32) {
-    if (ahead && k + kAhead < whole && (k & 32) == 0)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(ahead + k + kAhead));
-    uint4 v[NT];
+    if ((k & 32) == 0) ask();
+    uint4 v[NT], w[MT][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-      v[n] = __ldg(reinterpret_cast<const uint4*>(x[n] + k + 8 * t));
-    uint4 w[MT][2];
+    for (int n = 0; n < NT; ++n) v[n] = __ldg(reinterpret_cast<const uint4*>(x[n] + k + 8 * t));
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) w[m][h] = __ldg(reinterpret_cast<const uint4*>(rows[m][h] + k));
+      for (int h = 0; h < 2; ++h)
+        w[m][h] = __ldg(reinterpret_cast<const uint4*>(rows[m][h] + k + 8 * t));
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int n = 0; n < NT; ++n) mma32<T>(acc[m][n], w[m][0], w[m][1], v[n]);
   }
   for (; k < k1; k += 32) {  // the last, partial step; all steps of unaligned rows
+    if ((k & 32) == 0) ask();
     const int left = p.n_in - k - 8 * t;
     uint4 v[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) v[n] = load8(x[n] + k + 8 * t, left, p.vec_in);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const uint4 lo = load8(rows[m][0] + k, left, p.vec_in);
-      const uint4 hi = load8(rows[m][1] + k, left, p.vec_in);
+      const uint4 lo = load8(rows[m][0] + k + 8 * t, left, p.vec_in);
+      const uint4 hi = load8(rows[m][1] + k + 8 * t, left, p.vec_in);
 #pragma unroll
       for (int n = 0; n < NT; ++n) mma32<T>(acc[m][n], lo, hi, v[n]);
     }
   }
+}
+
+// Share i of n of the inner range, in whole steps of 64.
+__device__ __forceinline__ int2 inner_share(int k0, int k1, int i, int n) {
+  const int per = ((k1 - k0 + 63) / 64 + n - 1) / n * 64;
+  const int lo = min(k0 + i * per, k1);
+  return make_int2(lo, min(lo + per, k1));
 }
 
 // Write a token's h as 16-bit terms, by one warp: element j of lane j % 32 in
@@ -341,12 +400,10 @@ __device__ __forceinline__ void few_shrink(const AdapterArgs& p, const T* a, int
                                            const T* x, int k0, int k1, float* s_warp,
                                            float* s_part) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  // the warps' shares: neighbouring steps of 32
-  const int steps = (k1 - k0 + 31) / 32, per = (steps + WARPS - 1) / WARPS;
-  const int w0 = min(k0 + warp * per * 32, k1), w1 = min(w0 + per * 32, k1);
+  const int2 mine_k = inner_share(k0, k1, warp, WARPS);
   float acc[MT][1][4] = {};
   const T* const xs[1] = {x};
-  shrink<T, MT, 1>(p, a, rank, j0, xs, nullptr, w0, w1, acc);
+  shrink<T, MT, 1>(p, a, rank, j0, xs, nullptr, mine_k.x, mine_k.y, acc);
   // [warp][token][16 MT]
   float* mine = s_warp + warp * kGroup * 16 * MT;
 #pragma unroll
@@ -416,8 +473,8 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) adapters_few(AdapterAr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int o_per = (p.n_out + 32 * CTAS - 1) / (32 * CTAS) * 32;
   const int o0 = min(cta * o_per, p.n_out), o1 = min(o0 + o_per, p.n_out);
-  const int k_per = (p.n_in + 32 * CTAS - 1) / (32 * CTAS) * 32;
-  const int k0 = min(cta * k_per, p.n_in), k1 = min(k0 + k_per, p.n_in);
+  const int2 inner = inner_share(0, p.n_in, cta, CTAS);
+  const int k0 = inner.x, k1 = inner.y;
   const int groups = few_groups<WARPS>(p, s_ids, s_group);
   // every CTA of a cluster goes through the same groups
   for (int q = blockIdx.x / CTAS; q < groups; q += gridDim.x / CTAS) {
@@ -441,15 +498,18 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) adapters_few(AdapterAr
       __syncthreads();
       continue;
     }
-    const T* b = static_cast<const T*>(p.b) + (int64_t)slot * p.n_out * p.rank;
-    if (o1 > o0) {
-      const char* from = reinterpret_cast<const char*>(b + (int64_t)o0 * p.rank);
-      const int64_t bytes = (int64_t)(o1 - o0) * p.rank * (int)sizeof(T);
-      for (int64_t i = 128ll * threadIdx.x; i < bytes; i += 128ll * 32 * WARPS)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
-    }
-    __syncthreads();
     const T* a = static_cast<const T*>(p.a) + (int64_t)slot * p.rank * p.n_in;
+    const T* b = static_cast<const T*>(p.b) + (int64_t)slot * p.n_out * p.rank;
+    __syncthreads();
+    prefetch_rows(a + k0, rank, (int64_t)p.n_in * (int)sizeof(T), (k1 - k0) * (int64_t)sizeof(T));
+    prefetch_rows(b + (int64_t)o0 * p.rank, 1, 0, (int64_t)(o1 - o0) * p.rank * (int)sizeof(T));
+    if (p.base) {
+      const int lines = ((o1 - o0) * (int)sizeof(YT) + 127) / 128;
+      for (int i = threadIdx.x; i < n_tokens * lines; i += 32 * WARPS)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+            reinterpret_cast<const char*>(static_cast<const YT*>(p.base) +
+                                          s_token[i / lines] * p.bs + o0) + (i % lines) * 128));
+    }
     const T* x = static_cast<const T*>(p.x) + s_token[min(lane >> 2, n_tokens - 1)] * p.xs;
     if (rank <= 16)
       few_shrink<T, 1, WARPS>(p, a, rank, 0, x, k0, k1, s_mem.warps, s_part);
@@ -599,10 +659,9 @@ __device__ __forceinline__ void tile_shrink(const AdapterArgs& p, const T* a, in
                                             int k0, int k1, float* s_sum, int sum_pitch) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int half = warp % halves, share = warp / halves, shares = kWarps / halves;
-  const int steps = (k1 - k0 + 31) / 32, per = (steps + shares - 1) / shares;
-  const int w0 = min(k0 + share * per * 32, k1), w1 = min(w0 + per * 32, k1);
+  const int2 mine = inner_share(k0, k1, share, shares);
   float acc[MT][4][4] = {};
-  shrink<T, MT, 4>(p, a, rank, j0, x, ahead, w0, w1, acc);
+  shrink<T, MT, 4>(p, a, rank, j0, x, ahead, mine.x, mine.y, acc);
   for (int s = 0; s < shares; ++s) {
     if (share == s) {
 #pragma unroll
@@ -629,58 +688,59 @@ template <typename T, bool WIDE>  // WIDE: ranks above 32
 __global__ void __launch_bounds__(kThreads, 2) adapters_shrink(AdapterArgs p) {
   extern __shared__ float s_sum[];  // kTile x sum_pitch_of(p.rank)
   pdl_launch_dependents();
-  pdl_wait();
-  const int split = blockIdx.x % p.k_split, i = blockIdx.x / p.k_split;
-  if (i >= *p.n_tiles) return;  // (the whole cluster, here and below)
-  const int4 tile = p.tiles[i];
-  if (tile.x < 0) return;
-  const int rank = rank_of(p, tile.x);
-  if (rank == 0) return;
-  const int k_per = (p.n_in + 32 * p.k_split - 1) / (32 * p.k_split) * 32;
-  const int k0 = min(split * k_per, p.n_in), k1 = min(k0 + k_per, p.n_in);
-  const T* a = static_cast<const T*>(p.a) + (int64_t)tile.x * p.rank * p.n_in;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
-  const int pitch = sum_pitch_of(p.rank), halves = tile.z > 32 ? 2 : 1;
-  const auto row = [&](int k) {
-    return static_cast<const T*>(p.x) + p.perm[tile.y + min(k, tile.z - 1)] * p.xs;
-  };
-  const int first = 32 * (warp % halves);
-  const T* x[4];
-#pragma unroll
-  for (int n = 0; n < 4; ++n) x[n] = row(first + 8 * n + g);
-  const T* ahead = first + lane < tile.z ? row(first + lane) : nullptr;
-  if (rank <= 16)
-    tile_shrink<T, 1>(p, a, rank, 0, x, ahead, halves, k0, k1, s_sum, pitch);
-  else if (rank <= 32)
-    tile_shrink<T, 2>(p, a, rank, 0, x, ahead, halves, k0, k1, s_sum, pitch);
-  if constexpr (WIDE)
-    if (rank > 32)
-      for (int j0 = 0; j0 < rank; j0 += 64)
-        tile_shrink<T, 4>(p, a, rank, j0, x, j0 ? nullptr : ahead, halves, k0, k1, s_sum, pitch);
   cg::cluster_group cluster = cg::this_cluster();
-  cluster.sync();
-  // a warp per token: its h over the cluster's shares, as 16-bit terms
-  const int nk = (rank + 31) / 32;
-  for (int k = split * kWarps + warp; k < tile.z; k += p.k_split * kWarps) {
-    float h[kMaxRank / 32];
+  const int split = blockIdx.x % p.k_split;
+  const int2 inner = inner_share(0, p.n_in, split, p.k_split);
+  const int k0 = inner.x, k1 = inner.y, pitch = sum_pitch_of(p.rank);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
+  pdl_wait();
+  const int n_tiles = *p.n_tiles;
+  // every CTA of a cluster goes through the same tiles
+  for (int i = blockIdx.x / p.k_split; i < n_tiles; i += gridDim.x / p.k_split) {
+    const int4 tile = p.tiles[i];
+    const int rank = tile.x < 0 ? 0 : rank_of(p, tile.x);
+    if (rank == 0) continue;
+    const T* a = static_cast<const T*>(p.a) + (int64_t)tile.x * p.rank * p.n_in;
+    const int halves = tile.z > 32 ? 2 : 1, first = 32 * (warp % halves);
+    const auto row = [&](int k) {
+      return static_cast<const T*>(p.x) + p.perm[tile.y + min(k, tile.z - 1)] * p.xs;
+    };
+    const T* x[4];
 #pragma unroll
-    for (int q = 0; q < kMaxRank / 32; ++q) {
-      h[q] = 0.f;
-      if (q < nk && q * 32 + lane < rank) {
-        float part[kMaxSplit];
+    for (int n = 0; n < 4; ++n) x[n] = row(first + 8 * n + g);
+    const T* ahead = first + lane < tile.z ? row(first + lane) : nullptr;
+    if (rank <= 16)
+      tile_shrink<T, 1>(p, a, rank, 0, x, ahead, halves, k0, k1, s_sum, pitch);
+    else if (rank <= 32)
+      tile_shrink<T, 2>(p, a, rank, 0, x, ahead, halves, k0, k1, s_sum, pitch);
+    if constexpr (WIDE)
+      if (rank > 32)
+        for (int j0 = 0; j0 < rank; j0 += 64)
+          tile_shrink<T, 4>(p, a, rank, j0, x, j0 ? nullptr : ahead, halves, k0, k1, s_sum, pitch);
+    cluster.sync();
+    // a warp per token: its h over the cluster's shares, as 16-bit terms
+    const int nk = (rank + 31) / 32;
+    for (int k = split * kWarps + warp; k < tile.z; k += p.k_split * kWarps) {
+      float h[kMaxRank / 32];
 #pragma unroll
-        for (int c = 0; c < kMaxSplit; ++c)
-          part[c] = c < p.k_split ? cluster.map_shared_rank(s_sum, c)[k * pitch + q * 32 + lane]
-                                  : 0.f;
+      for (int q = 0; q < kMaxRank / 32; ++q) {
+        h[q] = 0.f;
+        if (q < nk && q * 32 + lane < rank) {
+          float part[kMaxSplit];
 #pragma unroll
-        for (int c = 0; c < kMaxSplit; ++c) h[q] += part[c];
+          for (int c = 0; c < kMaxSplit; ++c)
+            part[c] = c < p.k_split ? cluster.map_shared_rank(s_sum, c)[k * pitch + q * 32 + lane]
+                                    : 0.f;
+#pragma unroll
+          for (int c = 0; c < kMaxSplit; ++c) h[q] += part[c];
+        }
       }
+      T* out = static_cast<T*>(p.terms) + (int64_t)(tile.y + k) * Terms<T>::n * p.term_pitch;
+      const float down = split_terms<T>(h, nk, out, p.term_pitch);
+      if (lane == 0) p.downs[tile.y + k] = down;
     }
-    T* out = static_cast<T*>(p.terms) + (int64_t)(tile.y + k) * Terms<T>::n * p.term_pitch;
-    const float down = split_terms<T>(h, nk, out, p.term_pitch);
-    if (lane == 0) p.downs[tile.y + k] = down;
+    cluster.sync();  // no CTA changes its sums or leaves while another reads them
   }
-  cluster.sync();  // no CTA leaves while another reads its sums
 }
 
 // Elements from token to token in shared memory: 64 bytes past a multiple of
@@ -696,57 +756,66 @@ __global__ void __launch_bounds__(kThreads, 2) adapters_expand(AdapterArgs p) {
   T* s_h = reinterpret_cast<T*>(s_dyn);  // [token][term][term_pitch]
   __shared__ int s_token[kTile];
   __shared__ float s_down[kTile];
-  const int split = blockIdx.x % p.o_split, i = blockIdx.x / p.o_split;
-  const int warp = threadIdx.x >> 5;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = Terms<T>::n * p.term_pitch, pitch = pitch_of<T>(row);
   pdl_wait();
-  if (i >= *p.n_tiles) return;
-  const int4 tile = p.tiles[i];
-  const int o_per = (p.n_out + 32 * p.o_split - 1) / (32 * p.o_split) * 32;
-  const int o0 = min(split * o_per, p.n_out), o1 = min(o0 + o_per, p.n_out);
-  const int rank = tile.x < 0 ? 0 : rank_of(p, tile.x);
-  if (rank == 0) {
-    for (int k = 0; k < tile.z; ++k) copy_base<YT>(p, p.perm[tile.y + k], o0, o1);
-    return;
-  }
-  const int nk = (rank + 31) / 32, row = Terms<T>::n * p.term_pitch, pitch = pitch_of<T>(row);
-  if ((int)threadIdx.x < kTile) {
-    const int k = tile.y + min((int)threadIdx.x, tile.z - 1);
-    s_token[threadIdx.x] = p.perm[k];
-    s_down[threadIdx.x] = p.downs[k];
-  }
-  // terms of the tile's tokens (places past them repeat the last token's)
-  const T* terms = static_cast<const T*>(p.terms) + (int64_t)tile.y * row;
-  for (int k = threadIdx.x; k < kTile * row / 8; k += kThreads) {
-    const int token = k / (row / 8), c = k % (row / 8) * 8;
-    *reinterpret_cast<uint4*>(s_h + token * pitch + c) =
-        *reinterpret_cast<const uint4*>(terms + (int64_t)min(token, tile.z - 1) * row + c);
-  }
-  __syncthreads();
-  const T* b = static_cast<const T*>(p.b) + (int64_t)tile.x * p.n_out * p.rank;
-  const float scale = p.scales ? p.scales[tile.x] : 1.f;
-  // two halves of the tile's tokens times four blocks of 32 columns, or eight
-  // blocks where the tile has half its tokens at most
-  const int halves = tile.z > 32 ? 2 : 1, half = warp % halves, n_tokens = tile.z - 32 * half;
-  const T* h = s_h + 32 * half * pitch;
-  const int step = 32 * kWarps / halves, lane = threadIdx.x & 31;
-  const YT* ahead = p.base && lane < n_tokens
-                        ? static_cast<const YT*>(p.base) + s_token[32 * half + lane] * p.bs
-                        : nullptr;
-  for (int o = o0 + 32 * (warp / halves); o < o1; o += step) {
-    Pack<YT, 4> v[4][2];
-    load_base<YT, 4>(p, s_token + 32 * half, n_tokens, o, v);
-    if (ahead && o + step < o1)  // this warp's next columns, from L2
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(ahead + o + step));
-    float acc[2][4][4] = {};
-    for (int k = 0; k < nk; ++k) {
-      uint4 w[4];
-      load_b(p, b, rank, k, o, w);
-      expand<T, 4>(w, h + 32 * k, pitch, p.term_pitch, acc);
+  // (tile, 128 columns) steps in equal contiguous shares
+  const int per_tile = (p.n_out + 127) / 128;
+  const int64_t steps = (int64_t)*p.n_tiles * per_tile;
+  int64_t step = steps * blockIdx.x / gridDim.x;
+  const int64_t end = steps * (blockIdx.x + 1) / gridDim.x;
+  while (step < end) {
+    const int4 tile = p.tiles[step / per_tile];
+    const int from = (int)(step % per_tile), to = (int)min((int64_t)per_tile, from + end - step);
+    step += to - from;
+    const int o0 = 128 * from, o1 = min(128 * to, p.n_out);
+    const int rank = tile.x < 0 ? 0 : rank_of(p, tile.x);
+    if (rank == 0) {
+      for (int k = 0; k < tile.z; ++k) copy_base<YT>(p, p.perm[tile.y + k], o0, o1);
+      continue;
     }
-    finish<YT, 4>(p, s_token + 32 * half, n_tokens, s_down + 32 * half, scale, o, v, acc);
+    const int nk = (rank + 31) / 32;
+    __syncthreads();  // the last tile's terms are done with
+    if ((int)threadIdx.x < kTile) {
+      const int k = tile.y + min((int)threadIdx.x, tile.z - 1);
+      s_token[threadIdx.x] = p.perm[k];
+      s_down[threadIdx.x] = p.downs[k];
+    }
+    // terms of the tile's tokens (places past them repeat the last token's)
+    const T* terms = static_cast<const T*>(p.terms) + (int64_t)tile.y * row;
+    for (int k = threadIdx.x; k < kTile * row / 8; k += kThreads) {
+      const int token = k / (row / 8), c = k % (row / 8) * 8;
+      *reinterpret_cast<uint4*>(s_h + token * pitch + c) =
+          *reinterpret_cast<const uint4*>(terms + (int64_t)min(token, tile.z - 1) * row + c);
+    }
+    __syncthreads();
+    const T* b = static_cast<const T*>(p.b) + (int64_t)tile.x * p.n_out * p.rank;
+    const float scale = p.scales ? p.scales[tile.x] : 1.f;
+    // two halves of the tile's tokens times four blocks of 32 columns, or
+    // eight blocks where the tile has half its tokens at most
+    const int halves = tile.z > 32 ? 2 : 1, half = warp % halves, n_tokens = tile.z - 32 * half;
+    const T* h = s_h + 32 * half * pitch;
+    const int stride = 32 * kWarps / halves;
+    const YT* ahead = p.base && lane < n_tokens
+                          ? static_cast<const YT*>(p.base) + s_token[32 * half + lane] * p.bs
+                          : nullptr;
+    for (int o = o0 + 32 * (warp / halves); o < o1; o += stride) {
+      Pack<YT, 4> v[4][2];
+      load_base<YT, 4>(p, s_token + 32 * half, n_tokens, o, v);
+      if (ahead && o + stride < o1)  // this warp's next columns, from L2
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(ahead + o + stride));
+      float acc[2][4][4] = {};
+      for (int k = 0; k < nk; ++k) {
+        uint4 w[4];
+        load_b(p, b, rank, k, o, w);
+        expand<T, 4>(w, h + 32 * k, pitch, p.term_pitch, acc);
+      }
+      finish<YT, 4>(p, s_token + 32 * half, n_tokens, s_down + 32 * half, scale, o, v, acc);
+    }
   }
 }
 
+constexpr int kWave = 2 * 152;  // CTAs that the device's SMs hold at a time, two each
 constexpr int kMaxTokens = 1 << 27, kMaxWidth = 1 << 30;  // (32-bit grids and columns)
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -761,10 +830,10 @@ Workspace workspace_of(int n_tokens, int n_slots, int rank) {
   Workspace w{};
   if (n_tokens <= kFewTokens || n_slots == 0 || rank == 0) return w;
   w.max_tiles = n_tokens / kTile + (n_slots + 1 < n_tokens ? n_slots + 1 : n_tokens);
-  // CTAs for two waves of the device's SMs, with tiles as full as can be
+  // one wave of CTAs, with tiles as full as can be
   const int tiles = (n_tokens + kTile - 1) / kTile;
   w.k_split = 1;
-  while (w.k_split < kMaxSplit && tiles * w.k_split < 2 * 152) w.k_split *= 2;
+  while (w.k_split < kMaxSplit && tiles * 2 * w.k_split <= kWave) w.k_split *= 2;
   w.term_pitch = (rank + 31) / 32 * 32;
   w.tiles = 16;
   w.perm = round_up(w.tiles + 16ll * w.max_tiles, 128);
@@ -820,26 +889,25 @@ spmv_status run_few(AdapterArgs& p, cudaStream_t st) {
 
 template <typename T, typename YT>
 spmv_status run_many(AdapterArgs& p, cudaStream_t st) {
-  const int tiles = (p.n_tokens + kTile - 1) / kTile;
-  const int most = (p.n_out + 127) / 128;  // a CTA step is 128 columns
-  p.o_split = (912 + tiles - 1) / tiles;
-  p.o_split = p.o_split < 1 ? 1 : p.o_split > most ? most : p.o_split;
   const size_t sort_smem = (size_t)(p.n_slots + 1) * 4;
   const size_t shrink_smem = (size_t)kTile * sum_pitch_of(p.rank) * 4;
   const size_t expand_smem = (size_t)kTile * pitch_of<T>(Terms<T>::n * p.term_pitch) * sizeof(T);
   const void* shrink_fn = p.rank > 32 ? reinterpret_cast<const void*>(&adapters_shrink<T, true>)
                                       : reinterpret_cast<const void*>(&adapters_shrink<T, false>);
   const void* expand_fn = reinterpret_cast<const void*>(&adapters_expand<T, YT>);
-  if ((int64_t)p.max_tiles * p.o_split > INT_MAX) return SPMV_ERR_TOO_LARGE;
   if (!allow_smem(reinterpret_cast<const void*>(&adapters_sort), sort_smem) ||
       !allow_smem(shrink_fn, shrink_smem) || !allow_smem(expand_fn, expand_smem))
     return SPMV_ERR_CUDA;
   adapters_sort<<<1, kSortThreads, sort_smem, st>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SPMV_ERR_CUDA;
   void* args[] = {&p};
-  if (launch_cluster(shrink_fn, p.max_tiles * p.k_split, kThreads, shrink_smem, p.k_split, true,
-                     st, args) != 0 ||
-      launch_pdl(expand_fn, p.max_tiles * p.o_split, kThreads, expand_smem, st, args) != 0)
+  // two CTAs per SM, or fewer where there is less to do
+  const int64_t steps = (int64_t)p.max_tiles * ((p.n_out + 127) / 128);
+  const int clusters = p.max_tiles < kWave / p.k_split ? p.max_tiles : kWave / p.k_split;
+  if (launch_cluster(shrink_fn, clusters * p.k_split, kThreads, shrink_smem, p.k_split, true, st,
+                     args) != 0 ||
+      launch_pdl(expand_fn, (int)(steps < kWave ? steps : kWave), kThreads, expand_smem, st,
+                 args) != 0)
     return SPMV_ERR_CUDA;
   return SPMV_OK;
 }
@@ -904,6 +972,9 @@ extern "C" spmv_status spmv_adapters_run(int32_t n_tokens, int32_t n_in, int32_t
   p.x = x, p.xs = x_stride, p.a = a, p.b = b, p.ids = slot_ids, p.ranks = ranks, p.scales = scales;
   p.base = base, p.bs = base_stride, p.y = y, p.ys = y_stride;
   p.vec_in = n_in % 8 == 0 && rows_aligned(x, n_tokens, x_stride, 2, 8) && aligned_to(a, 16);
+  if (p.vec_in && n_in % 16 == 0 && aligned_to(x, 32) && aligned_to(a, 32) &&
+      (n_tokens == 1 || x_stride % 16 == 0))
+    p.vec_in = 2;
   p.vec_b = rank % 8 == 0 && aligned_to(b, 16);
   p.vec_y = n_out % 4 == 0 && rows_aligned(y, n_tokens, y_stride, ysz, 4) &&
             (!base || rows_aligned(base, n_tokens, base_stride, ysz, 4));

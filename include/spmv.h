@@ -652,8 +652,7 @@ typedef struct spmv_logits {
  * lists outside [0, vocab) are ignored, so lists may be padded with -1.
  * out may be logits itself (same pointer, type and stride). Errors:
  * INVALID_ARG (sizes, null or misaligned pointers, a list without its
- * offsets, strides, overlaps), UNSUPPORTED (types), TOO_LARGE (more than
- * 2^31 - 1 blocks of work), CUDA. */
+ * offsets, strides, overlaps), UNSUPPORTED (types), CUDA. */
 spmv_status spmv_logits_process(const spmv_logits* args, void* stream);
 
 #ifdef __cplusplus

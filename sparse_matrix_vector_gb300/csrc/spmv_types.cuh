@@ -8,6 +8,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "spmv_internal.h"
 
@@ -193,6 +194,49 @@ __device__ __forceinline__ void set_pair(Pack<__nv_bfloat16, N>& r, int k, float
 }
 
 }  // namespace
+
+// Clusters of `cluster` CTAs that the current device holds at a time: what
+// fits its SMs by registers and shared memory, less what a cluster's being
+// confined to one group of SMs leaves over (36 rather than 38 clusters of 8
+// at two CTAs per SM). Asked once per kernel and launch shape, when the kernel
+// is also given leave to use `smem` bytes. 0 on error.
+inline int resident_clusters(const void* fn, int cluster, int block, size_t smem) {
+  struct Known {
+    const void* fn;
+    int dev, cluster;
+    size_t smem;
+    int n;
+  };
+  static std::mutex mu;
+  static Known known[128];
+  static int count = 0;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  for (int i = 0; i < count; ++i)
+    if (known[i].fn == fn && known[i].dev == dev && known[i].cluster == cluster &&
+        known[i].smem == smem)
+      return known[i].n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)cluster);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+          cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (count < 128) known[count++] = Known{fn, dev, cluster, smem, n};
+  return n;
+}
 
 inline bool op_dtype(int t) { return t == SPMV_F32 || t == SPMV_F16 || t == SPMV_BF16; }
 inline int64_t op_dtype_size(int t) { return t == SPMV_F32 ? 4 : 2; }

@@ -137,8 +137,6 @@ def logits(lib, **kw):
     (dict(repetition=M + 2), INVALID), (dict(mask=DB + 2), INVALID), (dict(mask_stride=-4), INVALID),
     (dict(mask_rows=DX + 1), INVALID),
     (dict(dtype=F16, out_dtype=BF16), UNSUPPORTED), (dict(dtype=F32, out_dtype=F16), UNSUPPORTED),
-    (dict(n_requests=2**28, vocab=2**28, stride=2**28, out_stride=2**28, out=1 << 62, mask=None),
-     TOO_LARGE),
     (dict(n_requests=0), OK), (dict(vocab=0), OK),
 ])
 def test_logits_refuses(spmv_lib, kw, status):

@@ -2,14 +2,12 @@
 //
 // Bound by reading the logits and writing them: 8 bytes per token of the
 // vocabulary in fp32, against a few thousand list entries per request. Which
-// tokens a request's lists hold, and how often, has to be known before its
-// logits pass through: a table of one word per token in shared memory, for a
-// share of the vocabulary per CTA. Every CTA reads the whole lists for its
-// share, from L2: an eighth to a sixth more traffic there at a few thousand
-// entries, and none in memory. (Sharing the reading among a cluster, with
-// counts in distributed shared memory, measured slower: 95 against 289 us
-// where this takes XX on 256 requests of 128000 tokens.) Requests whose
-// parameters change nothing skip the tables.
+// tokens a request's lists hold, and how often, takes a table in shared
+// memory, for a share of the vocabulary per CTA; every CTA reads the whole
+// lists for its share, from L2. The few tokens that are listed are finished
+// one by one before the share passes through and are put in place after it, so
+// that the pass itself is a copy with a mask. Requests whose parameters change
+// nothing skip the tables.
 #include <climits>
 #include <type_traits>
 
@@ -19,14 +17,17 @@
 namespace spmv {
 namespace {
 
-constexpr int kLogitThreads = 512, kLogitWarps = kLogitThreads / 32;
-constexpr int kShare = 16384;      // tokens of a CTA's table, at most (64 KB)
+constexpr int kLogitThreads = 384, kLogitWarps = kLogitThreads / 32;
+constexpr int kLogitPerSm = 3;  // CTAs: one passes logits through while others are at their lists
+// A token's 16 bits of the table: count among the output tokens (exact below
+// kHeavy, which it passes by no more than a CTA's threads), and marks.
+constexpr uint32_t kSeen = 0x8000u, kBiased = 0x4000u, kCount = 0x3fffu, kHeavy = 0x2000u;
+constexpr int kShare = 20480;      // tokens of a CTA's share, at most (a table of 40 KB)
 constexpr int kLeastShare = 1024;  // and at least
-constexpr int kListed = 512;       // biases of a CTA's share kept in shared memory
-// table word: output tokens in the low 30 bits, and
-constexpr uint32_t kSeen = 0x80000000u, kBiased = 0x40000000u, kCount = 0x3fffffffu;
+constexpr int kMet = 2048;         // listed tokens of a share kept as a list, with their results
+constexpr int kListed = 384;       // biases of a share kept in shared memory
 
-constexpr int kWave = 2 * 152;  // CTAs that the device's SMs hold at a time, two each
+constexpr int kWave = kLogitPerSm * 152;  // CTAs that the device's SMs hold at a time
 
 struct LogitArgs {
   spmv_logits l;
@@ -38,9 +39,9 @@ struct Penalty {
   float rep, freq, pres;
 };
 
-__device__ __forceinline__ float penalised(float l, uint32_t w, const Penalty& c) {
-  if (w & (kSeen | kCount)) l = l > 0.f ? l / c.rep : l * c.rep;
-  if (w & kCount) l = l - c.freq * (float)(w & kCount) - c.pres;
+__device__ __forceinline__ float penalised(float l, bool seen, int64_t count, const Penalty& c) {
+  if (seen || count > 0) l = l > 0.f ? l / c.rep : l * c.rep;
+  if (count > 0) l = l - c.freq * (float)count - c.pres;
   return l;
 }
 
@@ -49,6 +50,7 @@ struct Request {
   Penalty c;
   int64_t p0, p1, o0, o1, b0, b1;
   int mask_row;  // -1: none
+  // (settle() waits for what load() has only asked for)
   __device__ __forceinline__ void load(const spmv_logits& p, int64_t i) {
     c.rep = p.repetition ? p.repetition[i] : 1.f;
     c.freq = p.frequency ? p.frequency[i] : 0.f;
@@ -58,6 +60,8 @@ struct Request {
     if (p.output_tokens) o0 = p.output_offsets[i], o1 = p.output_offsets[i + 1];
     if (p.bias_tokens) b0 = p.bias_offsets[i], b1 = p.bias_offsets[i + 1];
     mask_row = p.mask ? (p.mask_rows ? p.mask_rows[i] : (int)i) : -1;
+  }
+  __device__ __forceinline__ void settle(const spmv_logits& p) {
     if (mask_row >= p.n_masks) mask_row = -1;
     if (c.rep == 1.f) {
       p1 = p0;
@@ -66,18 +70,94 @@ struct Request {
   }
 };
 
+// Put the lanes' tokens k that are `met` for the first time on the list: one
+// atomic per warp (one per token queued up on the counter's address).
+__device__ __forceinline__ void list_met(bool met, int k, int* s_n, uint16_t* s_met) {
+  const uint32_t m = __ballot_sync(0xffffffffu, met);
+  if (m == 0) return;
+  const int lane = threadIdx.x & 31;
+  int at = 0;
+  if (lane == 0) at = atomicAdd(s_n, __popc(m));
+  at = __shfl_sync(0xffffffffu, at, 0);
+  at += __popc(m & ((1u << lane) - 1));
+  if (met && at < kMet) s_met[at] = (uint16_t)k;
+}
+
+// f(entry - v0) for every entry of list[lo, hi) inside [v0, v0 + n), by the
+// whole CTA, 16 bytes of the list at a time where it allows that; f says
+// whether it meets the token for the first time. Most entries belong to other
+// shares: a warp first queues its own ones, so that f runs with all lanes at
+// work.
+constexpr int kQueue = 256;
+
+template <typename F>
+__device__ __forceinline__ void for_entries(const int32_t* list, int64_t lo, int64_t hi, int v0,
+                                            int n, uint16_t* queue, int* s_n,
+                                            uint16_t* s_met, F&& f) {
+  if (lo >= hi) return;
+  const int me = threadIdx.x, lane = me & 31;
+  const uint32_t below = (1u << lane) - 1;
+  int queued = 0;  // (the same in all lanes)
+  const auto flush = [&] {
+    __syncwarp();
+    for (int e = 0; e < queued; e += 32) {
+      const bool on = e + lane < queued;
+      const int k = on ? queue[e + lane] : 0;
+      list_met(on && f(k), k, s_n, s_met);
+    }
+    __syncwarp();
+    queued = 0;
+  };
+  const auto offer = [&](int v) {
+    const unsigned at = (unsigned)v - (unsigned)v0;
+    const uint32_t m = __ballot_sync(0xffffffffu, at < (unsigned)n);
+    if (at < (unsigned)n) queue[queued + __popc(m & below)] = (uint16_t)at;
+    queued += __popc(m);
+  };
+  const int to_line = (int)((0u - (unsigned)(reinterpret_cast<uintptr_t>(list + lo) >> 2)) & 3u);
+  const int head = (int)min((int64_t)to_line, hi - lo);
+  const int64_t vecs = (hi - lo - head) / 4;
+  const int4* body = reinterpret_cast<const int4*>(list + lo + head);
+  int edge = -1;  // an entry before or after the vectors
+  const int tail = (int)(hi - lo - head - 4 * vecs);
+  if (me < head) edge = list[lo + me];
+  if (me >= 4 && me - 4 < tail) edge = list[hi - tail + me - 4];
+  constexpr int kAtOnce = 4;
+  for (int64_t k = me - lane; k < vecs; k += kAtOnce * kLogitThreads) {  // (whole warps)
+    int4 v[kAtOnce];
+#pragma unroll
+    for (int h = 0; h < kAtOnce; ++h)
+      v[h] = k + lane + h * kLogitThreads < vecs ? __ldg(body + k + lane + h * kLogitThreads)
+                                                 : make_int4(-1, -1, -1, -1);
+#pragma unroll
+    for (int h = 0; h < kAtOnce; ++h) {
+      if (queued > kQueue - 128) flush();
+      offer(v[h].x);
+      offer(v[h].y);
+      offer(v[h].z);
+      offer(v[h].w);
+    }
+  }
+  if (queued > kQueue - 32) flush();
+  offer(edge);
+  flush();
+}
+
 // CTAs take (request, share of the vocabulary) pairs in turn. While one passes
-// through, the next one's parameters and first list entries come into
-// registers and its logits into L2. A table is cleared as it is read, so it is
-// empty again for the next pair.
+// through, the next one's parameters come into registers, its lists and its
+// logits into L2. A token's bits of the table are cleared as it is put in
+// place.
 template <typename T, typename OT, int VEC>
-__global__ void __launch_bounds__(kLogitThreads, 2) logits_rows(LogitArgs a) {
-  extern __shared__ __align__(16) uint32_t s_word[];  // a.share words
+__global__ void __launch_bounds__(kLogitThreads, kLogitPerSm) logits_rows(LogitArgs a) {
+  extern __shared__ __align__(16) uint32_t s_word[];  // a.share / 2 words, two tokens each
+  __shared__ uint16_t s_met[kMet];
+  __shared__ float s_result[kMet];
   __shared__ int s_token[kListed];
   __shared__ float s_value[kListed];
   __shared__ int s_warp[kLogitWarps];
+  __shared__ uint16_t s_queue[kLogitWarps][kQueue];
+  __shared__ int s_n, s_exact;  // met tokens; an exact count
   constexpr int kBatch = VEC == 1 ? 8 : 4;  // vectors under way per thread
-  constexpr int kFirst = 4;                 // prompt entries loaded ahead per thread
   const spmv_logits& p = a.l;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, me = threadIdx.x;
   const int64_t jobs = (int64_t)p.n_requests * a.shares;
@@ -88,92 +168,67 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_rows(LogitArgs a) {
     for (int64_t k = 128ll * me; k < n * (int64_t)sizeof(T); k += 128 * kLogitThreads)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(at + k));
   };
-  struct First {
-    int prompt[kFirst], output, bias;
-    float value;
+  const auto ask_list = [&](const int32_t* list, int64_t lo, int64_t hi) {
+    if (lo + 32 * me < hi) asm volatile("prefetch.global.L2 [%0];" ::"l"(list + lo + 32 * me));
   };
-  const auto load_first = [&](const Request& q, First& f) {
-#pragma unroll
-    for (int h = 0; h < kFirst; ++h) {
-      const int64_t k = q.p0 + me + h * kLogitThreads;
-      f.prompt[h] = k < q.p1 ? p.prompt_tokens[k] : -1;
-    }
-    f.output = q.o0 + me < q.o1 ? p.output_tokens[q.o0 + me] : -1;
-    const bool on = q.b0 + me < q.b1;
-    f.bias = on ? p.bias_tokens[q.b0 + me] : -1;
-    f.value = on ? p.bias_values[q.b0 + me] : 0.f;
-  };
+  const auto bits_of = [&](int k) { return s_word[k >> 1] >> (16 * (k & 1)) & 0xffffu; };
   int64_t i = blockIdx.x / (unsigned)a.shares;
   int v0 = (int)(blockIdx.x % (unsigned)a.shares) * a.share;
   const int64_t step_i = gridDim.x / (unsigned)a.shares;
   const int step_v = (int)(gridDim.x % (unsigned)a.shares) * a.share, wrap = a.shares * a.share;
   ask_logits(i, v0);
   Request next;
-  First first_next;
   next.load(p, i);
-  for (int k = 4 * me; k < a.share; k += 4 * kLogitThreads)
-    *reinterpret_cast<uint4*>(s_word + k) = make_uint4(0, 0, 0, 0);
-  load_first(next, first_next);
+  const auto clear_table = [&] {
+    for (int k = 4 * me; k < a.share / 2; k += 4 * kLogitThreads)
+      *reinterpret_cast<uint4*>(s_word + k) = make_uint4(0, 0, 0, 0);
+  };
+  clear_table();
+  if (me == 0) s_n = 0;
   __syncthreads();
 
   for (int64_t id = blockIdx.x; id < jobs; id += gridDim.x) {
     const int n = min(a.share, p.vocab - v0);
     const T* in = static_cast<const T*>(p.logits) + i * p.stride + v0;
     OT* out = static_cast<OT*>(p.out) + i * p.out_stride + v0;
-    const Request q = next;
-    const First f = first_next;
+    Request q = next;
+    q.settle(p);
     int64_t next_i = i + step_i;
     int next_v = v0 + step_v;
     if (next_v >= wrap) next_v -= wrap, ++next_i;
     const bool more = id + gridDim.x < jobs;
     if (more) next.load(p, next_i);
     const uint32_t* mask = q.mask_row >= 0 ? p.mask + q.mask_row * p.mask_stride + v0 / 32 : nullptr;
-    const bool counted = q.p1 > q.p0 || q.o1 > q.o0;
-    if (counted) {
-      const auto seen = [&](int v) {
-        if (v >= v0 && v < v0 + n) atomicOr(s_word + (v - v0), kSeen);
-      };
-      const auto told = [&](int v) {
-        if (v >= v0 && v < v0 + n) atomicAdd(s_word + (v - v0), 1u);
-      };
-      constexpr int kAtOnce = 4;
-      for (int64_t k = q.p0 + me + kFirst * kLogitThreads; k < q.p1; k += kAtOnce * kLogitThreads) {
-        int v[kAtOnce];
-#pragma unroll
-        for (int h = 0; h < kAtOnce; ++h)
-          v[h] = k + h * kLogitThreads < q.p1 ? p.prompt_tokens[k + h * kLogitThreads] : -1;
-#pragma unroll
-        for (int h = 0; h < kAtOnce; ++h) seen(v[h]);
-      }
-      for (int64_t k = q.o0 + me + kLogitThreads; k < q.o1; k += kAtOnce * kLogitThreads) {
-        int v[kAtOnce];
-#pragma unroll
-        for (int h = 0; h < kAtOnce; ++h)
-          v[h] = k + h * kLogitThreads < q.o1 ? p.output_tokens[k + h * kLogitThreads] : -1;
-#pragma unroll
-        for (int h = 0; h < kAtOnce; ++h) told(v[h]);
-      }
-#pragma unroll
-      for (int h = 0; h < kFirst; ++h) seen(f.prompt[h]);
-      told(f.output);
-    }
+
+    // count the lists; who first meets a token puts it on the list of met ones
+    // (in whatever order: each is finished by itself)
+    const auto mark = [&](int k, uint32_t how) {
+      return (atomicOr(s_word + (k >> 1), how << (16 * (k & 1))) >> (16 * (k & 1)) & 0xffffu) == 0;
+    };
+    const auto seen = [&](int k) {  // (frequent tokens once: atomics of one address queue up)
+      return !(bits_of(k) & kSeen) && mark(k, kSeen);
+    };
+    const auto told = [&](int k) {
+      return (bits_of(k) & kCount) < kHeavy &&
+             (atomicAdd(s_word + (k >> 1), 1u << (16 * (k & 1))) >> (16 * (k & 1)) & 0xffffu) == 0;
+    };
+    for_entries(p.prompt_tokens, q.p0, q.p1, v0, n, s_queue[warp], &s_n, s_met, seen);
+    for_entries(p.output_tokens, q.o0, q.o1, v0, n, s_queue[warp], &s_n, s_met, told);
     if (more) {
       ask_logits(next_i, next_v);
-      load_first(next, first_next);
+      ask_list(p.prompt_tokens, next.p0, next.p1);
+      ask_list(p.output_tokens, next.o0, next.o1);
     }
     // biases of this CTA's tokens, compacted in list order
     int listed = 0;
     for (int64_t k = q.b0; k < q.b1; k += kLogitThreads) {
-      int v = f.bias;
-      float value = f.value;
-      if (k > q.b0) {
-        const bool on = k + me < q.b1;
-        v = on ? p.bias_tokens[k + me] : -1;
-        value = on ? p.bias_values[k + me] : 0.f;
-      }
+      const bool on = k + me < q.b1;
+      const int v = on ? p.bias_tokens[k + me] : -1;
+      const float value = on ? p.bias_values[k + me] : 0.f;
       const bool mine = v >= v0 && v < v0 + n;
       const uint32_t m = __ballot_sync(0xffffffffu, mine);
       if (lane == 0) s_warp[warp] = __popc(m);
+      list_met(mine && mark(v - v0, kBiased), v - v0, &s_n, s_met);
       __syncthreads();
       int before = listed, total = 0;
 #pragma unroll
@@ -187,48 +242,67 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_rows(LogitArgs a) {
         s_value[before] = value;
       }
       listed += total;
-      __syncthreads();
+      if (k + kLogitThreads < q.b1) __syncthreads();
     }
-    if (counted) __syncthreads();
-    const auto allowed = [&](int k) { return !mask || (mask[k / 32] >> (k % 32) & 1u); };
-    if (listed > 0) {
-      // A token with biases is finished by the thread of its first entry and
-      // marked, so that the pass below leaves it alone.
-      const auto finish = [&](int v, float sum) {
-        const int k = v - v0;
-        const uint32_t w = atomicOr(s_word + k, kBiased);
-        out[k] = from_f32<OT>(allowed(k) ? penalised(to_f32(in[k]), w, q.c) + sum : -INFINITY);
-      };
-      if (listed <= kListed) {
-        if ((int)threadIdx.x < listed) {
-          const int v = s_token[threadIdx.x];
-          float sum = 0.f;
-          bool first = true;
-          for (int k = 0; k < listed; ++k) {
-            if (s_token[k] != v) continue;
-            first = first && k >= (int)threadIdx.x;
-            sum += s_value[k];
-          }
-          if (first) finish(v, sum);
+    __syncthreads();
+    const int met = s_n;
+    const bool kept = met <= kMet;  // on the list, all of them
+    // a met token's result
+    const auto result = [&](int k, uint32_t w, int64_t count) {
+      float l = penalised(to_f32(in[k]), w & kSeen, count, q.c);
+      if (w & kBiased) {
+        float sum = 0.f;
+        if (listed <= kListed) {
+          for (int j = 0; j < listed; ++j)
+            if (s_token[j] == v0 + k) sum += s_value[j];
+        } else {  // more than the compacted list holds: from the list itself
+          for (int64_t j = q.b0; j < q.b1; ++j)
+            if (p.bias_tokens[j] == v0 + k) sum += p.bias_values[j];
         }
-      } else {  // more than the compacted list holds: from the list itself
-        for (int64_t at = q.b0 + threadIdx.x; at < q.b1; at += kLogitThreads) {
-          const int v = p.bias_tokens[at];
-          if (v < v0 || v >= v0 + n) continue;
-          float sum = 0.f;
-          bool first = true;
-          for (int64_t k = q.b0; k < q.b1 && first; ++k) {
-            if (p.bias_tokens[k] != v) continue;
-            first = k >= at;
-            sum += p.bias_values[k];
+        l += sum;
+      }
+      return mask && !(mask[k / 32] >> (k % 32) & 1u) ? -INFINITY : l;
+    };
+    if (met > 0) {
+      // Results of the met tokens: into the list's places or, where there are
+      // more than it holds, straight into out, which the pass then leaves
+      // alone there. (out may be the logits themselves: they are read first.)
+      for (int e = me; e < (kept ? met : n); e += kLogitThreads) {
+        const int k = kept ? s_met[e] : e;
+        const uint32_t w = bits_of(k);
+        if (w == 0 || (w & kCount) >= kHeavy) continue;
+        const float l = result(k, w, w & kCount);
+        if (kept)
+          s_result[e] = l;
+        else
+          out[k] = from_f32<OT>(l);
+      }
+      if (q.o1 - q.o0 >= (int64_t)kHeavy) {  // counts past the table's: by the whole CTA
+        for (int e = 0; e < (kept ? met : n); ++e) {
+          const int k = kept ? s_met[e] : e;
+          const uint32_t w = bits_of(k);
+          if ((w & kCount) < kHeavy) continue;
+          __syncthreads();
+          if (me == 0) s_exact = 0;
+          __syncthreads();
+          int count = 0;
+          for (int64_t j = q.o0 + me; j < q.o1; j += kLogitThreads)
+            count += p.output_tokens[j] == v0 + k;
+          count = __reduce_add_sync(0xffffffffu, count);
+          if (lane == 0) atomicAdd(&s_exact, count);
+          __syncthreads();
+          if (me == 0) {
+            const float l = result(k, w, s_exact);
+            if (kept)
+              s_result[e] = l;
+            else
+              out[k] = from_f32<OT>(l);
           }
-          if (first) finish(v, sum);
         }
       }
       __syncthreads();
     }
-    const bool table = counted || listed > 0;
-    for (int base = VEC * threadIdx.x; base < n; base += kBatch * VEC * kLogitThreads) {
+    for (int base = VEC * me; base < n; base += kBatch * VEC * kLogitThreads) {
       Pack<T, VEC> v[kBatch];
       uint32_t bits[kBatch];  // of the tokens from k on (VEC of them, within one word)
 #pragma unroll
@@ -244,31 +318,33 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_rows(LogitArgs a) {
 #pragma unroll
       for (int h = 0; h < kBatch; ++h) {
         const int k = base + h * VEC * kLogitThreads;
-        if (k >= n) break;
-        Pack<uint32_t, VEC> w = {};
-        if (table) {
-          w = load_pack<uint32_t, VEC>(s_word + k);
-          store_pack<uint32_t, VEC>(s_word + k, Pack<uint32_t, VEC>{});
-        }
         Pack<OT, VEC> r;
-        uint32_t any = 0;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          float l = to_f32(v[h].v[e]);
-          if (w.v[e]) l = penalised(l, w.v[e], q.c);  // (few tokens of a vocabulary)
-          r.v[e] = from_f32<OT>(bits[h] >> e & 1 ? l : -INFINITY);
-          any |= w.v[e];
-        }
-        if (!(any & kBiased)) {
+        for (int e = 0; e < VEC; ++e)
+          r.v[e] = from_f32<OT>(bits[h] >> e & 1 ? to_f32(v[h].v[e]) : -INFINITY);
+        if (k >= n) break;
+        if (kept) {
           store_pack<OT, VEC>(out + k, r);
         } else {
 #pragma unroll
           for (int e = 0; e < VEC; ++e)
-            if (!(w.v[e] & kBiased)) out[k + e] = r.v[e];
+            if (bits_of(k + e) == 0) out[k + e] = r.v[e];
         }
       }
     }
-    __syncthreads();  // the table is empty, the list of biases done with
+    if (met > 0) {
+      __syncthreads();
+      if (kept) {
+        for (int e = me; e < met; e += kLogitThreads) {
+          out[s_met[e]] = from_f32<OT>(s_result[e]);
+          reinterpret_cast<uint16_t*>(s_word)[s_met[e]] = 0;
+        }
+      } else {
+        clear_table();
+      }
+      if (me == 0) s_n = 0;
+      __syncthreads();
+    }
     i = next_i;
     v0 = next_v;
   }
@@ -278,11 +354,20 @@ template <typename T, typename OT>
 spmv_status launch_logits(const spmv_logits& p, cudaStream_t st) {
   LogitArgs a{};
   a.l = p;
-  // As large a share as a table holds, every list being read once for each
-  // share; smaller ones where the requests would not give every SM two CTAs.
-  const int64_t tokens = (int64_t)p.vocab * p.n_requests / kWave;
-  const int64_t per = tokens < kLeastShare ? kLeastShare : tokens > kShare ? kShare : tokens;
-  a.shares = (int)((p.vocab + per - 1) / per);
+  // Every list is read once for each share, so shares are large; but CTAs
+  // should be done together. Of the counts that a table allows, up to twice the
+  // least: the one with the least of rounds x (a round's lists, some 15,000
+  // tokens' time, and its tokens).
+  const int least = (int)((p.vocab + (int64_t)kShare - 1) / kShare);
+  int64_t best = INT64_MAX;
+  for (int s = least; s <= 2 * least; ++s) {
+    const int64_t rounds = ((int64_t)p.n_requests * s + kWave - 1) / kWave;
+    const int64_t cost = rounds * (15000 + p.vocab / s);
+    if (cost < best) best = cost, a.shares = s;
+  }
+  // few requests: shares for every SM
+  const int64_t spread = kWave / p.n_requests, most = (p.vocab + kLeastShare - 1) / kLeastShare;
+  if (a.shares < spread && a.shares < most) a.shares = (int)(spread < most ? spread : most);
   a.share = (int)(((int64_t)p.vocab + a.shares - 1) / a.shares + 31) / 32 * 32;
   a.shares = (int)(((int64_t)p.vocab + a.share - 1) / a.share);
   constexpr int kVec = 16 / (int)sizeof(T);
@@ -291,8 +376,8 @@ spmv_status launch_logits(const spmv_logits& p, cudaStream_t st) {
                    rows_aligned(p.out, p.n_requests, p.out_stride, sizeof(OT), kVec);
   const void* fn = vec ? reinterpret_cast<const void*>(&logits_rows<T, OT, kVec>)
                        : reinterpret_cast<const void*>(&logits_rows<T, OT, 1>);
-  const size_t smem = (size_t)a.share * 4;
-  if (smem > 40 * 1024 &&  // 48 KB less the static part need no opt-in
+  const size_t smem = (size_t)a.share * 2;
+  if (smem > 16 * 1024 &&  // 48 KB less the static part need no opt-in
       cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
           cudaSuccess)
     return SPMV_ERR_CUDA;

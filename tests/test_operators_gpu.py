@@ -670,6 +670,40 @@ def test_logits_in_place_repeatable_and_counts(spmv_lib, v):
     assert float(o[0, v - 1]) == -70000.0 and not o[0, :v - 1].any()
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("types", [("f32", "f32"), ("bf16", "bf16")], ids=lambda p: "-".join(p))
+def test_logits_many_requests_long_lists(spmv_lib, types, in_place):
+    """Enough requests that a block has a large share of the vocabulary, with
+    more tokens and biases in it than it keeps as lists, and a token whose
+    count passes 16 bits among them."""
+    g = gen(57)
+    n, v = 460, 7003
+    x = randn(g, n, v, dtype=types[0], std=3.0)
+    lengths = torch.zeros(n, dtype=torch.int64)
+    lengths[3], lengths[4], lengths[200], lengths[459] = 30000, 2500, 100000, 9000
+    off = torch.cat([torch.zeros(1, dtype=torch.int64), lengths.cumsum(0)])
+    tok = torch.randint(0, v, (int(off[-1]),), generator=g).int()
+    tok[off[200] + 5000:off[200] + 95000] = 6999          # 90000 times one token
+    tok[off[459]:off[460]] = 17                           # one token only
+    blen = torch.zeros(n, dtype=torch.int64)
+    blen[3], blen[7], blen[200] = 1500, 700, 900
+    boff = torch.cat([torch.zeros(1, dtype=torch.int64), blen.cumsum(0)])
+    btok = torch.randint(0, v, (int(boff[-1]),), generator=g).int()
+    kw = dict(prompt=(tok.flip(0).contiguous(), off), output=(tok, off), repetition=torch.rand(n, generator=g) + 0.7,
+              frequency=torch.rand(n, generator=g) * 0.01, presence=torch.rand(n, generator=g),
+              bias=(btok, torch.randn(btok.numel(), generator=g), boff),
+              mask=torch.randint(-2 ** 31, 2 ** 31, (2, (v + 31) // 32), generator=g).int(),
+              mask_rows=(torch.arange(n) % 3 - 1).int())
+    dev = {k: tuple(t.to(DEV) for t in a) if isinstance(a, tuple) else a.to(DEV) for k, a in kw.items()}
+    xd = x.to(DEV)
+    out = xd if in_place else torch.full((n, v), float("nan"), dtype=TYPES[types[1]], device=DEV)
+    S.spmv_logits_process(xd, out, **dev)
+    ref, slack = logits_ref(x, kw["prompt"], kw["output"], kw["repetition"], kw["frequency"], kw["presence"],
+                            kw["bias"], kw["mask"], kw["mask_rows"])
+    t = TYPES[types[1]]
+    close(out, ref, ROUND[t] * ref.abs() + slack + TINY[t], "logits")
+
+
 # -------------------------------------------------------- streams and graphs
 
 def _calls(g, big):

@@ -60,12 +60,14 @@ struct ForwardArgs {
 // Forward, one pass over x: a group of threads (a warp, or the CTA) takes
 // rows in turn, each thread the same CPT columns of every row, whose weight
 // and bias it keeps in registers. STAGES - 1 rows are on their way into
-// shared memory while one is worked on (STAGES 0: rows that are not 16-byte
-// aligned, loaded directly, the next one asked from L2 a row ahead). Mean and
+// shared memory while one is worked on. STAGES 0: rows that are not 16-byte
+// aligned, loaded directly, the next one asked from L2 a row ahead; weight and
+// bias are in shared memory then, which leaves registers for more CTAs. Mean and
 // variance are taken one after the other, the variance from the centred
 // values: no cancellation. The arithmetic is on pairs (fp32x2 instructions).
 template <typename XT, typename YT, int VEC, int CPT, int STAGES, bool WARP>
-__global__ void __launch_bounds__(WARP ? kThreads : most_threads(CPT, STAGES > 0))
+__global__ void __launch_bounds__(WARP ? kThreads : most_threads(CPT, STAGES > 0),
+                                  STAGES == 0 && CPT <= 16 ? 2 : 1)
 layernorm_fused(ForwardArgs<XT, YT> p) {
   constexpr int NV = CPT / VEC;
   constexpr bool kAligned = STAGES > 0;
@@ -95,9 +97,20 @@ layernorm_fused(ForwardArgs<XT, YT> p) {
 #pragma unroll
     for (int k = 0; k < STAGES - 1; ++k) fetch(first + k * step, k);
   }
+  // unaligned rows: pair j of thread t at [weight, bias][j][t]
+  float2* s_param = reinterpret_cast<float2*>(s_dyn) + threadIdx.x;
   float2 g[NV][VEC / 2], o[NV][VEC / 2];
   cols.load_param(p.w, p.pt, 1.f, g);
+  if constexpr (STAGES == 0) {
+#pragma unroll
+    for (int j = 0; j < CPT / 2; ++j) s_param[j * blockDim.x] = g[j / (VEC / 2)][j % (VEC / 2)];
+  }
   cols.load_param(p.b, p.pt, 0.f, o);
+  if constexpr (STAGES == 0) {
+#pragma unroll
+    for (int j = 0; j < CPT / 2; ++j)
+      s_param[(CPT / 2 + j) * blockDim.x] = o[j / (VEC / 2)][j % (VEC / 2)];
+  }
   int stage = 0;
   for (int64_t r = first; r < p.n_rows; r += step) {
     PX in[NV];
@@ -150,7 +163,10 @@ layernorm_fused(ForwardArgs<XT, YT> p) {
 #pragma unroll
         for (int k = 0; k < VEC / 2; ++k) {
           const float2 c = __fadd2_rn(pair_f32(in[i], k), off);
-          set_pair(out, k, __ffma2_rn(__fmul2_rn(c, scale), g[i][k], o[i][k]));
+          const int j = i * (VEC / 2) + k;
+          const float2 gk = STAGES == 0 ? s_param[j * blockDim.x] : g[i][k];
+          const float2 ok = STAGES == 0 ? s_param[(CPT / 2 + j) * blockDim.x] : o[i][k];
+          set_pair(out, k, __ffma2_rn(__fmul2_rn(c, scale), gk, ok));
         }
         cols.store(p.y + r * p.ys, i, out);
       }
@@ -192,18 +208,6 @@ layernorm_rows(ForwardArgs<XT, YT> p) {
   }
 }
 
-// Sum of two values over the CTA, in every thread, in a fixed order. One
-// barrier; s_red (32 pairs) must not be in use by an earlier call.
-__device__ __forceinline__ float2 cta_sum2_all(float a, float b, float2* s_red) {
-  a = warp_sum(a);
-  b = warp_sum(b);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) s_red[warp] = make_float2(a, b);
-  __syncthreads();
-  const float2 v = lane < (int)(blockDim.x >> 5) ? s_red[lane] : make_float2(0.f, 0.f);
-  return make_float2(warp_sum(v.x), warp_sum(v.y));
-}
-
 template <typename XT, typename YT>
 struct BackwardArgs {
   int64_t n_rows;
@@ -220,13 +224,33 @@ struct BackwardArgs {
   float* part;   // gridDim.x x {dweight, dbias} x n_cols partial sums, or null
 };
 
+// Sums of N values over the CTA, in every thread, in a fixed order. One
+// barrier; s_red must not be in use by an earlier call.
+template <int N>
+__device__ __forceinline__ void cta_sums_all(float (&v)[N], float (*s_red)[N]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = warp_sum(v[k]);
+  if (lane == 0) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) s_red[warp][k] = v[k];
+  }
+  __syncthreads();
+  const bool on = lane < (int)(blockDim.x >> 5);
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = warp_sum(on ? s_red[lane][k] : 0.f);
+}
+
 // Backward, one pass over x and dy: a group of threads (a warp, or the CTA)
-// takes rows in turn, each thread the same CPT columns of every row, whose
-// dweight and dbias it sums in registers. STAGES - 1 rows are on their way
-// into shared memory while one is worked on (STAGES 0: as in the forward
-// kernel). With c = x - mean, the row needs the sums of g and of g * c:
+// takes ROWS rows at a time, each thread the same CPT columns of every row,
+// whose weight it keeps and whose dweight and dbias it sums in registers.
+// With c = x - mean, a row needs the sums of g and of g * c:
 //   dx = rstd * g - rstd * mean(g) - c * rstd^3 * mean(g * c).
-template <typename XT, typename YT, int VEC, int CPT, int STAGES, bool WARP, bool W_SMEM>
+// STAGES - 1 sets of rows are on their way into shared memory while one is
+// worked on, twice, from there. STAGES 0: rows that are not 16-byte aligned,
+// held in registers, the next one asked from L2 ahead; the weight is in
+// shared memory then.
+template <typename XT, typename YT, int VEC, int CPT, int STAGES, int ROWS, bool WARP>
 __global__ void __launch_bounds__(WARP ? kThreads : most_threads(CPT, STAGES > 0))
 layernorm_backward_fused(BackwardArgs<XT, YT> p) {
   constexpr int NV = CPT / VEC;
@@ -234,55 +258,49 @@ layernorm_backward_fused(BackwardArgs<XT, YT> p) {
   using PX = Pack<XT, VEC>;
   using PY = Pack<YT, VEC>;
   extern __shared__ __align__(16) unsigned char s_dyn[];
-  __shared__ float2 s_red[2][32];
+  __shared__ float s_red[2][32][2 * ROWS];
   const Cols<VEC, kAligned> cols{WARP ? (int)threadIdx.x & 31 : (int)threadIdx.x,
                                  WARP ? 32 : (int)blockDim.x, p.n_cols};
   const int n = p.n_cols;
   const int64_t step = (int64_t)gridDim.x * (WARP ? kWarps : 1);
   const int64_t first = (int64_t)blockIdx.x * (WARP ? kWarps : 1) + (WARP ? threadIdx.x >> 5 : 0);
   const float inv = 1.f / (float)n;
-  // ring of stages, vector i of thread t at [stage][i][t]
+  // ring of row slots, vector i of thread t at [slot][i][t]
   PX* ring_x = reinterpret_cast<PX*>(s_dyn);
-  PY* ring_y = reinterpret_cast<PY*>(s_dyn + (size_t)STAGES * NV * blockDim.x * sizeof(PX));
-  const auto slot = [&](int stage, int i) {
-    return (stage * NV + i) * (int)blockDim.x + (int)threadIdx.x;
+  PY* ring_y = reinterpret_cast<PY*>(s_dyn + (size_t)STAGES * ROWS * NV * blockDim.x * sizeof(PX));
+  const auto place = [&](int slot, int i) {
+    return (slot * NV + i) * (int)blockDim.x + (int)threadIdx.x;
   };
   const auto fetch = [&](int64_t r, int stage) {
-    if (r < p.n_rows) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (cols.has(i)) {
-          copy_async<sizeof(PX)>(&ring_x[slot(stage, i)], p.x + r * p.xs + cols.col(i, 0));
-          copy_async<sizeof(PY)>(&ring_y[slot(stage, i)], p.dy + r * p.dys + cols.col(i, 0));
-        }
-    }
+    for (int h = 0; h < ROWS; ++h)
+      if (r + h * step < p.n_rows) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (cols.has(i)) {
+            const int64_t at = r + h * step;
+            copy_async<sizeof(PX)>(&ring_x[place(stage * ROWS + h, i)],
+                                   p.x + at * p.xs + cols.col(i, 0));
+            copy_async<sizeof(PY)>(&ring_y[place(stage * ROWS + h, i)],
+                                   p.dy + at * p.dys + cols.col(i, 0));
+          }
+      }
     copy_commit();
   };
-  // the weight of this thread's columns: in shared memory for the whole call
-  // where it fits (vector i of thread t at [i][t]; a warp's lanes hold the
-  // same columns in every warp), else read again for every row
-  Pack<float, VEC>* s_w = reinterpret_cast<Pack<float, VEC>*>(
-      s_dyn + (size_t)STAGES * NV * blockDim.x * (sizeof(PX) + sizeof(PY)));
-  if constexpr (W_SMEM) {
-    float2 g[NV][VEC / 2];
-    cols.load_param(p.w, p.pt, 1.f, g);
-    // (warps that share columns write the same values: no barrier needed)
+  if constexpr (STAGES > 0) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int k = 0; k < VEC / 2; ++k) set_pair(s_w[i * cols.group + cols.me], k, g[i][k]);
+    for (int k = 0; k < STAGES - 1; ++k) fetch(first + k * ROWS * step, k);
   }
-  const auto weight = [&](float2 (&g)[NV][VEC / 2]) {
-    if constexpr (W_SMEM) {
+  // unaligned rows: pair j of thread t's weight at [j][t]
+  float2* s_w = reinterpret_cast<float2*>(s_dyn) + threadIdx.x;
+  float2 w[NV][VEC / 2];
+  cols.load_param(p.w, p.pt, 1.f, w);
+  if constexpr (STAGES == 0) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const Pack<float, VEC> v = load_pack<float, VEC>(s_w[i * cols.group + cols.me].v);
-#pragma unroll
-        for (int k = 0; k < VEC / 2; ++k) g[i][k] = pair_f32(v, k);
-      }
-    } else {
-      cols.load_param(p.w, p.pt, 1.f, g);
-    }
+    for (int j = 0; j < CPT / 2; ++j) s_w[j * blockDim.x] = w[j / (VEC / 2)][j % (VEC / 2)];
+  }
+  const auto weight = [&](int i, int k) {
+    return STAGES == 0 ? s_w[(i * (VEC / 2) + k) * blockDim.x] : w[i][k];
   };
 
   float2 dw[NV][VEC / 2], db[NV][VEC / 2];
@@ -290,86 +308,102 @@ layernorm_backward_fused(BackwardArgs<XT, YT> p) {
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int k = 0; k < VEC / 2; ++k) dw[i][k] = db[i][k] = make_float2(0.f, 0.f);
-  if constexpr (STAGES > 0) {
+  float m[ROWS], rs[ROWS], m_next[ROWS] = {}, rs_next[ROWS] = {};
 #pragma unroll
-    for (int k = 0; k < STAGES - 1; ++k) fetch(first + k * step, k);
-  }
-  float m_next = 0.f, rs_next = 0.f;
-  if (first < p.n_rows) m_next = p.mean[first], rs_next = p.rstd[first];
+  for (int h = 0; h < ROWS; ++h)
+    if (first + h * step < p.n_rows)
+      m_next[h] = p.mean[first + h * step], rs_next[h] = p.rstd[first + h * step];
   int stage = 0, turn = 0;
-  for (int64_t r = first; r < p.n_rows; r += step) {
-    const float m = m_next, rs = rs_next;
-    if (r + step < p.n_rows) m_next = p.mean[r + step], rs_next = p.rstd[r + step];
-    PX x[NV];
-    PY dy[NV];
-    if constexpr (STAGES > 0) {
-      // the stage before this one is free: this thread read it a row ago
-      fetch(r + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
-      copy_wait<STAGES - 1>();
+  PX x[STAGES > 0 ? 1 : NV] = {};  // unaligned rows
+  PY dy[STAGES > 0 ? 1 : NV] = {};
+  const auto x_of = [&](int h, int i) {  // vector i of row h of the set
+    if constexpr (STAGES > 0)
+      return ring_x[place(stage * ROWS + h, i)];
+    else
+      return x[i];
+  };
+  const auto dy_of = [&](int h, int i) {
+    if constexpr (STAGES > 0)
+      return ring_y[place(stage * ROWS + h, i)];
+    else
+      return dy[i];
+  };
+  for (int64_t r = first; r < p.n_rows; r += ROWS * step) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (cols.has(i)) {
-          x[i] = ring_x[slot(stage, i)];
-          dy[i] = ring_y[slot(stage, i)];
-        }
-      stage = stage + 1 == STAGES ? 0 : stage + 1;
+    for (int h = 0; h < ROWS; ++h) {
+      m[h] = m_next[h], rs[h] = rs_next[h];
+      const int64_t at = r + (ROWS + h) * step;
+      if (at < p.n_rows) m_next[h] = p.mean[at], rs_next[h] = p.rstd[at];
+    }
+    if constexpr (STAGES > 0) {
+      // the stage before this one is free: this thread is done with it
+      fetch(r + (STAGES - 1) * ROWS * step, stage == 0 ? STAGES - 1 : stage - 1);
+      copy_wait<STAGES - 1>();
     } else {
       cols.load(p.x + r * p.xs, x, true);
-      cols.load(p.dy + r * p.dys, dy, true);
-      // columns past the end count nothing
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int k = 0; k < VEC; ++k)
-          if (!cols.has(i, k)) x[i].v[k] = from_f32<XT>(0.f), dy[i].v[k] = from_f32<YT>(0.f);
+      cols.load(p.dy + r * p.dys, dy, true);  // (past the end: zeros, which count nothing)
       if (r + step < p.n_rows) {
         cols.prefetch(p.x + (r + step) * p.xs);
         cols.prefetch(p.dy + (r + step) * p.dys);
       }
     }
-    const float2 off = make_float2(-m, -m), scale = make_float2(rs, rs);
-    float2 sg = make_float2(0.f, 0.f), sgc = sg, g[NV][VEC / 2];
-    weight(g);
+    float sums[2 * ROWS];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (cols.has(i)) {
+    for (int h = 0; h < ROWS; ++h) {
+      float2 sg = make_float2(0.f, 0.f), sgc = sg;
+      if (h == 0 || r + h * step < p.n_rows) {
+        const float2 off = make_float2(-m[h], -m[h]), scale = make_float2(rs[h], rs[h]);
 #pragma unroll
-        for (int k = 0; k < VEC / 2; ++k) {
-          const float2 d = pair_f32(dy[i], k), c = __fadd2_rn(pair_f32(x[i], k), off);
-          const float2 gk = __fmul2_rn(d, g[i][k]);
-          sg = __fadd2_rn(sg, gk);
-          sgc = __ffma2_rn(gk, c, sgc);
-          dw[i][k] = __ffma2_rn(__fmul2_rn(d, scale), c, dw[i][k]);
-          db[i][k] = __fadd2_rn(db[i][k], d);
-        }
+        for (int i = 0; i < NV; ++i)
+          if (cols.has(i)) {
+            const PX xi = x_of(h, i);
+            const PY di = dy_of(h, i);
+#pragma unroll
+            for (int k = 0; k < VEC / 2; ++k) {
+              const float2 d = pair_f32(di, k), c = __fadd2_rn(pair_f32(xi, k), off);
+              const float2 gk = __fmul2_rn(d, weight(i, k));
+              sg = __fadd2_rn(sg, gk);
+              sgc = __ffma2_rn(gk, c, sgc);
+              dw[i][k] = __ffma2_rn(__fmul2_rn(d, scale), c, dw[i][k]);
+              db[i][k] = __fadd2_rn(db[i][k], d);
+            }
+          }
       }
-    if (!p.dx) continue;
-    float a = sg.x + sg.y, b = sgc.x + sgc.y;
-    if constexpr (WARP) {
-      a = warp_sum(a);
-      b = warp_sum(b);
-    } else {
-      const float2 t = cta_sum2_all(a, b, s_red[turn]);
-      turn ^= 1;
-      a = t.x;
-      b = t.y;
+      sums[2 * h] = sg.x + sg.y;
+      sums[2 * h + 1] = sgc.x + sgc.y;
     }
-    a = -rs * (a * inv);
-    b = -rs * (rs * (rs * (b * inv)));
-    const float2 fa = make_float2(a, a), fb = make_float2(b, b);
-    weight(g);
+    if (p.dx) {
+      if constexpr (WARP) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (cols.has(i)) {
-        PX out;
-#pragma unroll
-        for (int k = 0; k < VEC / 2; ++k) {
-          const float2 c = __fadd2_rn(pair_f32(x[i], k), off);
-          const float2 gk = __fmul2_rn(pair_f32(dy[i], k), g[i][k]);
-          set_pair(out, k, __ffma2_rn(c, fb, __ffma2_rn(gk, scale, fa)));
-        }
-        cols.store(p.dx + r * p.dxs, i, out);
+        for (int k = 0; k < 2 * ROWS; ++k) sums[k] = warp_sum(sums[k]);
+      } else {
+        cta_sums_all<2 * ROWS>(sums, s_red[turn]);
+        turn ^= 1;
       }
+#pragma unroll
+      for (int h = 0; h < ROWS; ++h) {
+        if (h > 0 && r + h * step >= p.n_rows) break;
+        const float2 off = make_float2(-m[h], -m[h]), scale = make_float2(rs[h], rs[h]);
+        const float a = -rs[h] * (sums[2 * h] * inv);
+        const float b = -rs[h] * (rs[h] * (rs[h] * (sums[2 * h + 1] * inv)));
+        const float2 fa = make_float2(a, a), fb = make_float2(b, b);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (cols.has(i)) {
+            const PX xi = x_of(h, i);
+            const PY di = dy_of(h, i);
+            PX out;
+#pragma unroll
+            for (int k = 0; k < VEC / 2; ++k) {
+              const float2 c = __fadd2_rn(pair_f32(xi, k), off);
+              const float2 gk = __fmul2_rn(pair_f32(di, k), weight(i, k));
+              set_pair(out, k, __ffma2_rn(c, fb, __ffma2_rn(gk, scale, fa)));
+            }
+            cols.store(p.dx + (r + h * step) * p.dxs, i, out);
+          }
+      }
+    }
+    if constexpr (STAGES > 0) stage = stage + 1 == STAGES ? 0 : stage + 1;
   }
   pdl_launch_dependents();
   if (!p.part) return;
@@ -400,14 +434,14 @@ layernorm_backward_fused(BackwardArgs<XT, YT> p) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (cols.has(i)) {
-        Pack<float, VEC> w, b;
+        Pack<float, VEC> pw, pb;
 #pragma unroll
         for (int k = 0; k < VEC / 2; ++k) {
-          set_pair(w, k, dw[i][k]);
-          set_pair(b, k, db[i][k]);
+          set_pair(pw, k, dw[i][k]);
+          set_pair(pb, k, db[i][k]);
         }
-        cols.store(part, i, w);
-        cols.store(part + n, i, b);
+        cols.store(part, i, pw);
+        cols.store(part + n, i, pb);
       }
   }
 }
@@ -415,7 +449,7 @@ layernorm_backward_fused(BackwardArgs<XT, YT> p) {
 // Backward, rows too long for registers: dx, one row per CTA step.
 template <typename XT, typename YT>
 __global__ void __launch_bounds__(kThreads) layernorm_dx_rows(BackwardArgs<XT, YT> p) {
-  __shared__ float2 s_red[2][32];
+  __shared__ float s_red[2][32][2];
   int turn = 0;
   for (int64_t r = blockIdx.x; r < p.n_rows; r += gridDim.x) {
     const float m = p.mean[r], rs = p.rstd[r];
@@ -427,10 +461,11 @@ __global__ void __launch_bounds__(kThreads) layernorm_dx_rows(BackwardArgs<XT, Y
       sg += g;
       sgx += g * ((to_f32(x[j]) - m) * rs);
     }
-    const float2 t = cta_sum2_all(sg, sgx, s_red[turn]);
+    float sums[2] = {sg, sgx};
+    cta_sums_all<2>(sums, s_red[turn]);
     turn ^= 1;
-    sg = t.x / (float)p.n_cols;
-    sgx = t.y / (float)p.n_cols;
+    sg = sums[0] / (float)p.n_cols;
+    sgx = sums[1] / (float)p.n_cols;
     for (int j = threadIdx.x; j < p.n_cols; j += kThreads) {
       const float g = to_f32(dy[j]) * (p.w ? load_as_f32(p.w, p.pt, j) : 1.f);
       const float xh = (to_f32(x[j]) - m) * rs;
@@ -497,7 +532,7 @@ struct RowShape {
   int cols, threads, grid;
 };
 
-RowShape row_shape(int64_t n_rows, int n_cols, bool aligned) {
+RowShape row_shape(int64_t n_rows, int n_cols, bool aligned, bool forward) {
   RowShape s{};
   int per_sm = 0;  // CTAs that an SM's registers hold
   int64_t groups = n_rows;
@@ -514,7 +549,7 @@ RowShape row_shape(int64_t n_rows, int n_cols, bool aligned) {
       s.cols = n_cols <= 2048 ? 8 : n_cols <= 16 * 512 ? 16 : n_cols <= 24 * 512 ? 24 : 0;
     if (!s.cols) return s;
     s.threads = ((n_cols + s.cols - 1) / s.cols + 31) / 32 * 32;
-    const int most = (!aligned ? (s.cols == 8 ? 640 : 512)
+    const int most = (!aligned ? (s.cols == 24 ? 512 : forward ? 1024 : s.cols == 8 ? 640 : 512)
                                : s.cols == 8 ? 1024 : s.cols == 16 ? 800 : 512) / s.threads;
     per_sm = most < 1 ? 1 : most > 8 ? 8 : most;
   }
@@ -531,7 +566,7 @@ int64_t backward_workspace(int64_t n_rows, int n_cols, bool want_params) {
   if (!want_params || n_rows == 0) return 0;
   int64_t parts = kLongParts;
   for (const bool aligned : {false, true}) {
-    const RowShape s = row_shape(n_rows, n_cols, aligned);
+    const RowShape s = row_shape(n_rows, n_cols, aligned, false);
     if (s.cols && s.grid > parts) parts = s.grid;
   }
   return parts * 2 * n_cols * 4;
@@ -569,13 +604,14 @@ spmv_status forward_launch(const RowShape& s, const ForwardArgs<XT, YT>& p, cuda
   // four stages of fp32 are at most 192 KB of an SM's shared memory (three of
   // rows with 32 columns per thread)
   constexpr int kStages = !ALIGNED ? 0 : CPT == 32 ? 3 : 4;
-  return launch_rows(layernorm_fused<XT, YT, kVec, CPT, kStages, WARP>, s,
-                     (size_t)kStages * s.threads * CPT * sizeof(XT), p, st);
+  const size_t smem = ALIGNED ? (size_t)kStages * s.threads * CPT * sizeof(XT)
+                              : (size_t)s.threads * CPT * 8;  // weight and bias
+  return launch_rows(layernorm_fused<XT, YT, kVec, CPT, kStages, WARP>, s, smem, p, st);
 }
 
 template <typename XT, typename YT, bool ALIGNED>
 spmv_status forward(const ForwardArgs<XT, YT>& p, cudaStream_t st) {
-  RowShape s = row_shape(p.n_rows, p.n_cols, ALIGNED);
+  RowShape s = row_shape(p.n_rows, p.n_cols, ALIGNED, true);
   if constexpr (ALIGNED) {
     if (s.cols == 32) return forward_launch<XT, YT, 32, false, true>(s, p, st);
     if (s.warp)
@@ -594,31 +630,30 @@ spmv_status forward(const ForwardArgs<XT, YT>& p, cudaStream_t st) {
 template <typename XT, typename YT, int CPT, bool WARP, bool ALIGNED>
 spmv_status backward_launch(const RowShape& s, const BackwardArgs<XT, YT>& p, cudaStream_t st) {
   constexpr int kVec = 16 / (int)sizeof(XT);
-  const size_t w = (size_t)(WARP ? 32 : s.threads) * CPT * 4;  // weights
   if constexpr (!ALIGNED) {
-    return launch_rows(layernorm_backward_fused<XT, YT, kVec, CPT, 0, WARP, true>, s, w, p, st);
+    return launch_rows(layernorm_backward_fused<XT, YT, kVec, CPT, 0, 1, WARP>, s,
+                       (size_t)s.threads * CPT * 4, p, st);
   } else {
-    const size_t stage = (size_t)s.threads * CPT * (sizeof(XT) + sizeof(YT));
-    // (a warp group's ring is larger than the two sums per column that the
-    // warps leave in its place at the end)
+    // Two rows at a time halve the barriers; where two sets of them do not
+    // fit, single rows. (A warp group's ring is larger than the two sums per
+    // column that the warps leave in its place at the end.)
+    const size_t row = (size_t)s.threads * CPT * (sizeof(XT) + sizeof(YT));
     const size_t room = kSmemBudget / (size_t)((s.grid + kSms - 1) / kSms);
-    if constexpr (CPT < 32)
-      if (3 * stage + w <= room)
-        return launch_rows(layernorm_backward_fused<XT, YT, kVec, CPT, 3, WARP, true>, s,
-                           3 * stage + w, p, st);
-    if (2 * stage + w <= room || CPT == 8 || WARP)
-      return launch_rows(layernorm_backward_fused<XT, YT, kVec, CPT, 2, WARP, true>, s,
-                         2 * stage + w, p, st);
-    if constexpr (CPT > 8 && !WARP)
-      return launch_rows(layernorm_backward_fused<XT, YT, kVec, CPT, 2, WARP, false>, s,
-                         2 * stage, p, st);
-    return SPMV_ERR_UNSUPPORTED;
+    if constexpr (CPT < 32) {
+      if (4 * row <= room)
+        return launch_rows(layernorm_backward_fused<XT, YT, kVec, CPT, 2, 2, WARP>, s, 4 * row, p,
+                           st);
+      if (3 * row <= room)
+        return launch_rows(layernorm_backward_fused<XT, YT, kVec, CPT, 3, 1, WARP>, s, 3 * row, p,
+                           st);
+    }
+    return launch_rows(layernorm_backward_fused<XT, YT, kVec, CPT, 2, 1, WARP>, s, 2 * row, p, st);
   }
 }
 
 template <typename XT, typename YT, bool ALIGNED>
 spmv_status backward(const BackwardArgs<XT, YT>& p, void* dweight, void* dbias, cudaStream_t st) {
-  const RowShape s = row_shape(p.n_rows, p.n_cols, ALIGNED);
+  const RowShape s = row_shape(p.n_rows, p.n_cols, ALIGNED, false);
   int parts = s.grid;
   spmv_status status = SPMV_OK;
   if (s.warp) {

@@ -103,18 +103,21 @@ struct Cols {
   // whether vector i (ALIGNED) is inside the row
   __device__ __forceinline__ bool has(int i) const { return !ALIGNED || col(i, 0) < n; }
   __device__ __forceinline__ bool has(int i, int k) const { return ALIGNED || col(i, k) < n; }
-  // Loads of all vectors, under way together: places past the end repeat the
-  // row's last vector or element.
+  // Loads of all vectors, under way together: places past the end hold the
+  // row's last vector (ALIGNED) or zeros.
   template <typename T, int NV>
   __device__ __forceinline__ void load(const T* row, Pack<T, VEC> (&r)[NV], bool stream) const {
+    if constexpr (ALIGNED) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if constexpr (ALIGNED) {
-        r[i] = load_pack<T, VEC>(row + min(col(i, 0), n - VEC), stream);
-      } else {
+      for (int i = 0; i < NV; ++i) r[i] = load_pack<T, VEC>(row + min(col(i, 0), n - VEC), stream);
+    } else {
+      const T* at = row + me;
 #pragma unroll
-        for (int k = 0; k < VEC; ++k)
-          r[i].v[k] = load_pack<T, 1>(row + min(col(i, k), n - 1), stream).v[0];
+      for (int j = 0; j < NV * VEC; ++j) {
+        T v = from_f32<T>(0.f);
+        if (me + j * group < n) v = load_pack<T, 1>(at, stream).v[0];
+        r[j / VEC].v[j % VEC] = v;
+        at += group;
       }
     }
   }
@@ -123,9 +126,12 @@ struct Cols {
     if constexpr (ALIGNED) {
       store_pack<T, VEC>(row + col(i, 0), r);
     } else {
+      T* at = row + col(i, 0);
 #pragma unroll
-      for (int k = 0; k < VEC; ++k)
-        if (col(i, k) < n) row[col(i, k)] = r.v[k];
+      for (int k = 0; k < VEC; ++k) {
+        if (col(i, k) < n) *at = r.v[k];
+        at += group;
+      }
     }
   }
   // The same columns of a vector of runtime type (a layer's parameter), in

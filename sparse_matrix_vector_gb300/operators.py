@@ -20,6 +20,17 @@ from ._lib import SPMV_BF16, SPMV_F16, SPMV_F32
 from .api import SpmvError
 
 _CODES = {torch.float32: SPMV_F32, torch.float16: SPMV_F16, torch.bfloat16: SPMV_BF16}
+_F32, _I32, _I64 = torch.float32, torch.int32, torch.int64
+_current_device = torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (absent in CPU builds)
+_library = None
+
+
+def _lib_handle():
+    global _library
+    if _library is None:
+        _library = _lib.load()
+    return _library
 
 
 def _check(status: int, where: str) -> None:
@@ -62,38 +73,37 @@ def _vector(t, n: int, dtype, what: str) -> int:
     return t.data_ptr()
 
 
-def _same_device(*tensors) -> int:
+def _same_device(first, *others) -> int:
     """The tensors' common CUDA device, which must be the current one."""
-    dev = torch.cuda.current_device() if tensors[0].is_cuda else -1
-    for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != dev):
+    dev = _current_device() if first.is_cuda else -1
+    if dev < 0 or first.get_device() != dev:
+        raise ValueError(f"tensors must be on the current CUDA device, got {first.device}")
+    for t in others:
+        if t is not None and t.get_device() != dev:  # (-1: not a CUDA tensor)
             raise ValueError(f"tensors must be on the current CUDA device, got {t.device}")
     return dev
 
 
 def _on(stream, dev: int) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _raw_stream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _workspace(given, n_bytes: int, stream, handle: int, dev: int):
-    """A workspace tensor (None when none is needed), safe to drop as soon as
-    the call returns, on whatever stream it ran."""
+    """(address, bytes, owner) of a workspace; one that the caller does not
+    give is safe to drop as soon as the call returns, on whatever stream it
+    ran."""
     if given is not None:
         if given.data_ptr() % 16 or not given.is_contiguous():
             raise ValueError("workspace must be contiguous and 16-byte aligned")
-        return given
+        return given.data_ptr(), given.numel() * given.element_size(), given
     if n_bytes == 0:
-        return None
-    ws = torch.empty(n_bytes, dtype=torch.uint8, device=f"cuda:{dev}")
-    if stream is not None and handle != torch._C._cuda_getCurrentRawStream(dev):
+        return None, 0, None
+    ws = torch.empty(n_bytes, dtype=torch.uint8, device=dev)
+    if stream is not None and handle != _raw_stream(dev):
         ws.record_stream(torch.cuda.ExternalStream(handle, device=dev))
-    return ws
-
-
-def _span(ws):
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+    return ws.data_ptr(), n_bytes, ws
 
 
 def _params(weight, bias, d: int, what: str):
@@ -117,15 +127,15 @@ def spmv_layernorm(x, weight, bias, y, eps: float = 1e-5, mean=None, rstd=None,
         raise ValueError("x and y must have the same shape")
     dev = _same_device(x, y, weight, bias, mean, rstd)
     w, b, p = _params(weight, bias, d, "weight and bias")
-    _check(_lib.load().spmv_layernorm(
+    _check(_lib_handle().spmv_layernorm(
         n, d, x.data_ptr(), _dtype(x, "x"), xs, w, b, p, eps, y.data_ptr(), _dtype(y, "y"), ys,
-        _vector(mean, n, torch.float32, "mean"), _vector(rstd, n, torch.float32, "rstd"),
+        _vector(mean, n, _F32, "mean"), _vector(rstd, n, _F32, "rstd"),
         _on(stream, dev)), "spmv_layernorm")
 
 
 def spmv_layernorm_backward_workspace(n_rows: int, n_cols: int, want_params: bool = True) -> int:
     """Bytes of workspace that spmv_layernorm_backward needs."""
-    return int(_lib.load().spmv_layernorm_backward_workspace(n_rows, n_cols, int(want_params)))
+    return int(_lib_handle().spmv_layernorm_backward_workspace(n_rows, n_cols, int(want_params)))
 
 
 def spmv_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace=None,
@@ -155,20 +165,19 @@ def spmv_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, works
     if mean is None or rstd is None:
         raise ValueError("mean and rstd of the forward call are needed")
     handle = _on(stream, dev)
-    lib = _lib.load()
+    lib = _lib_handle()
     need = lib.spmv_layernorm_backward_workspace(n, d, 1 if dw or db else 0)
-    ws = _workspace(workspace, need, stream, handle, dev)
-    wp, wn = _span(ws)
+    wp, wn, _owner = _workspace(workspace, need, stream, handle, dev)
     _check(lib.spmv_layernorm_backward(
         n, d, dy.data_ptr(), _dtype(dy, "dy"), dys, x.data_ptr(), code, xs, w, p,
-        _vector(mean, n, torch.float32, "mean"), _vector(rstd, n, torch.float32, "rstd"),
+        _vector(mean, n, _F32, "mean"), _vector(rstd, n, _F32, "rstd"),
         0 if dx is None else dx.data_ptr(), dxs, dw, db, wp, wn, handle),
         "spmv_layernorm_backward")
 
 
 def spmv_adapters_workspace(n_tokens: int, n_slots: int, rank: int) -> int:
     """Bytes of workspace that spmv_adapters_run needs."""
-    return int(_lib.load().spmv_adapters_workspace(n_tokens, n_slots, rank))
+    return int(_lib_handle().spmv_adapters_workspace(n_tokens, n_slots, rank))
 
 
 def spmv_adapters_run(x, a, b, slot_ids, y, base=None, ranks=None, scales=None, workspace=None,
@@ -202,14 +211,14 @@ def spmv_adapters_run(x, a, b, slot_ids, y, base=None, ranks=None, scales=None, 
         raise ValueError("slot_ids is needed")
     dev = _same_device(x, y, a, b, slot_ids, base, ranks, scales, workspace)
     handle = _on(stream, dev)
-    lib = _lib.load()
-    ws = _workspace(workspace, lib.spmv_adapters_workspace(t, slots, rank), stream, handle, dev)
-    wp, wn = _span(ws)
+    lib = _lib_handle()
+    wp, wn, _owner = _workspace(workspace, lib.spmv_adapters_workspace(t, slots, rank), stream,
+                                handle, dev)
     _check(lib.spmv_adapters_run(
         t, n_in, n_out, slots, rank, _dtype(x, "x"), x.data_ptr(), xs, a.data_ptr(),
-        b.data_ptr(), _vector(slot_ids, t, torch.int32, "slot_ids"),
-        _vector(ranks, slots, torch.int32, "ranks"),
-        _vector(scales, slots, torch.float32, "scales"),
+        b.data_ptr(), _vector(slot_ids, t, _I32, "slot_ids"),
+        _vector(ranks, slots, _I32, "ranks"),
+        _vector(scales, slots, _F32, "scales"),
         None if base is None else base.data_ptr(), bs, y.data_ptr(), _dtype(y, "y"), ys, wp, wn,
         handle), "spmv_adapters_run")
 
@@ -219,8 +228,8 @@ def _list(pair, n: int, what: str):
     if pair is None:
         return 0, 0
     tokens, offsets = pair
-    return (_vector(tokens, tokens.numel(), torch.int32, what + " tokens"),
-            _vector(offsets, n + 1, torch.int64, what + " offsets"))
+    return (_vector(tokens, tokens.numel(), _I32, what + " tokens"),
+            _vector(offsets, n + 1, _I64, what + " offsets"))
 
 
 def spmv_logits_process(logits, out, prompt=None, output=None, repetition=None, frequency=None,
@@ -245,7 +254,7 @@ def spmv_logits_process(logits, out, prompt=None, output=None, repetition=None, 
     b_tok = b_val = b_off = 0
     if bias is not None:
         b_tok, b_off = _list((bias[0], bias[2]), n, "bias")
-        b_val = _vector(bias[1], bias[0].numel(), torch.float32, "bias values")
+        b_val = _vector(bias[1], bias[0].numel(), _F32, "bias values")
     m_ptr = m_stride = n_masks = 0
     if mask is not None:
         if mask.dtype != torch.int32:
@@ -258,11 +267,10 @@ def spmv_logits_process(logits, out, prompt=None, output=None, repetition=None, 
         m_ptr = mask.data_ptr()
     lists = [t for group in (prompt, output, bias) if group is not None for t in group]
     dev = _same_device(logits, out, repetition, frequency, presence, mask, mask_rows, *lists)
-    f32 = torch.float32
     args = _lib.spmv_logits(
         n, v, logits.data_ptr(), stride, out.data_ptr(), out_stride, _dtype(logits, "logits"),
-        _dtype(out, "out"), p_tok, p_off, o_tok, o_off, _vector(repetition, n, f32, "repetition"),
-        _vector(frequency, n, f32, "frequency"), _vector(presence, n, f32, "presence"), b_tok,
-        b_val, b_off, m_ptr, m_stride, _vector(mask_rows, n, torch.int32, "mask_rows"), n_masks, 0)
-    _check(_lib.load().spmv_logits_process(ctypes.byref(args), _on(stream, dev)),
+        _dtype(out, "out"), p_tok, p_off, o_tok, o_off, _vector(repetition, n, _F32, "repetition"),
+        _vector(frequency, n, _F32, "frequency"), _vector(presence, n, _F32, "presence"), b_tok,
+        b_val, b_off, m_ptr, m_stride, _vector(mask_rows, n, _I32, "mask_rows"), n_masks, 0)
+    _check(_lib_handle().spmv_logits_process(ctypes.byref(args), _on(stream, dev)),
            "spmv_logits_process")

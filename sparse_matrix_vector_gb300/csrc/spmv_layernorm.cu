@@ -41,7 +41,9 @@ __device__ __forceinline__ void copy_wait() {
 // Columns a thread holds of its rows, and the threads a CTA has at most with
 // them: more columns, or the addresses of single elements, take more
 // registers and leave room for fewer threads.
-constexpr int most_threads(int cols, bool aligned) { return cols == 16 && aligned ? 768 : 512; }
+constexpr int most_threads(int cols, bool aligned) {
+  return cols == 8 ? 640 : cols == 16 && aligned ? 768 : 512;
+}
 
 template <typename XT, typename YT>
 struct ForwardArgs {
@@ -221,7 +223,9 @@ struct BackwardArgs {
   const float *mean, *rstd;
   XT* dx;        // or null
   int64_t dxs;
-  float* part;   // gridDim.x x {dweight, dbias} x n_cols partial sums, or null
+  float* part;   // row_ctas x {dweight, dbias} x n_cols partial sums, or null
+  int row_ctas;  // CTAs that take rows; the others take columns (column_sums)
+  void *dweight, *dbias;  // what column_sums writes
 };
 
 // Sums of N values over the CTA, in every thread, in a fixed order. One
@@ -241,6 +245,56 @@ __device__ __forceinline__ void cta_sums_all(float (&v)[N], float (*s_red)[N]) {
   for (int k = 0; k < N; ++k) v[k] = warp_sum(on ? s_red[lane][k] : 0.f);
 }
 
+// dweight and dbias of the 32 columns from c0, by one CTA, straight from x and
+// dy: each warp sums every warps-th row, then the warps' sums in order. For
+// calls so small that their rows are still in L2: one launch and no workspace.
+template <typename XT, typename YT>
+__device__ __forceinline__ void column_sums(const BackwardArgs<XT, YT>& p, int c0) {
+  __shared__ float s_dw[32][32], s_db[32][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int c = c0 + lane, at = min(c, p.n_cols - 1);
+  const int n = (int)p.n_rows;
+  float dw = 0.f, db = 0.f;
+  // 32 of the warp's rows at a time, whose statistics the lanes load
+  const XT* x = p.x + at;
+  const YT* dy = p.dy + at;
+  for (int base = warp; base < n; base += 32 * warps) {
+    const int mine = min(base + lane * warps, n - 1);
+    const float m_lane = p.mean[mine], rs_lane = p.rstd[mine];
+#pragma unroll 1
+    for (int k0 = 0; k0 < 32 && base + k0 * warps < n; k0 += 8) {
+      XT xv[8];
+      YT dv[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t r = min(base + (k0 + k) * warps, n - 1);
+        xv[k] = x[r * p.xs];
+        dv[k] = dy[r * p.dys];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float m = __shfl_sync(0xffffffffu, m_lane, k0 + k);
+        const float rs = __shfl_sync(0xffffffffu, rs_lane, k0 + k);
+        if (base + (k0 + k) * warps < n) {
+          const float d = to_f32(dv[k]);
+          dw += d * ((to_f32(xv[k]) - m) * rs);
+          db += d;
+        }
+      }
+    }
+  }
+  s_dw[warp][lane] = dw;
+  s_db[warp][lane] = db;
+  __syncthreads();
+  if (warp > 0 || c >= p.n_cols) return;
+  for (int k = 1; k < warps; ++k) {
+    dw += s_dw[k][lane];
+    db += s_db[k][lane];
+  }
+  if (p.dweight) store_from_f32(p.dweight, p.pt, c, dw);
+  if (p.dbias) store_from_f32(p.dbias, p.pt, c, db);
+}
+
 // Backward, one pass over x and dy: a group of threads (a warp, or the CTA)
 // takes ROWS rows at a time, each thread the same CPT columns of every row,
 // whose weight it keeps and whose dweight and dbias it sums in registers.
@@ -251,7 +305,8 @@ __device__ __forceinline__ void cta_sums_all(float (&v)[N], float (*s_red)[N]) {
 // held in registers, the next one asked from L2 ahead; the weight is in
 // shared memory then.
 template <typename XT, typename YT, int VEC, int CPT, int STAGES, int ROWS, bool WARP>
-__global__ void __launch_bounds__(WARP ? kThreads : most_threads(CPT, STAGES > 0))
+__global__ void __launch_bounds__(WARP ? kThreads : most_threads(CPT, STAGES > 0),
+                                  !WARP ? 1 : CPT == 8 ? 3 : 2)
 layernorm_backward_fused(BackwardArgs<XT, YT> p) {
   constexpr int NV = CPT / VEC;
   constexpr bool kAligned = STAGES > 0;
@@ -262,8 +317,14 @@ layernorm_backward_fused(BackwardArgs<XT, YT> p) {
   const Cols<VEC, kAligned> cols{WARP ? (int)threadIdx.x & 31 : (int)threadIdx.x,
                                  WARP ? 32 : (int)blockDim.x, p.n_cols};
   const int n = p.n_cols;
-  const int64_t step = (int64_t)gridDim.x * (WARP ? kWarps : 1);
-  const int64_t first = (int64_t)blockIdx.x * (WARP ? kWarps : 1) + (WARP ? threadIdx.x >> 5 : 0);
+  // the CTAs for columns come first: they take longest
+  const int row_cta = (int)blockIdx.x - ((int)gridDim.x - p.row_ctas);
+  if (row_cta < 0) {
+    column_sums(p, 32 * (int)blockIdx.x);
+    return;
+  }
+  const int64_t step = (int64_t)p.row_ctas * (WARP ? kWarps : 1);
+  const int64_t first = (int64_t)row_cta * (WARP ? kWarps : 1) + (WARP ? threadIdx.x >> 5 : 0);
   const float inv = 1.f / (float)n;
   // ring of row slots, vector i of thread t at [slot][i][t]
   PX* ring_x = reinterpret_cast<PX*>(s_dyn);
@@ -407,7 +468,7 @@ layernorm_backward_fused(BackwardArgs<XT, YT> p) {
   }
   pdl_launch_dependents();
   if (!p.part) return;
-  float* part = p.part + (int64_t)blockIdx.x * 2 * n;
+  float* part = p.part + (int64_t)row_cta * 2 * n;
   if constexpr (WARP) {
     // the warps' sums, added up in warp order in shared memory
     copy_wait<0>();
@@ -546,10 +607,13 @@ RowShape row_shape(int64_t n_rows, int n_cols, bool aligned, bool forward) {
     if (aligned)
       s.cols = n_cols <= 2048 ? 8 : n_cols <= 16 * 768 ? 16 : n_cols <= 32 * 512 ? 32 : 0;
     else
-      s.cols = n_cols <= 2048 ? 8 : n_cols <= 16 * 512 ? 16 : n_cols <= 24 * 512 ? 24 : 0;
+      s.cols = n_cols <= (forward ? 2048 : 8 * 640) ? 8
+               : n_cols <= 16 * 512                 ? 16
+               : n_cols <= 24 * 512                 ? 24
+                                                    : 0;
     if (!s.cols) return s;
     s.threads = ((n_cols + s.cols - 1) / s.cols + 31) / 32 * 32;
-    const int most = (!aligned ? (s.cols == 24 ? 512 : forward ? 1024 : s.cols == 8 ? 640 : 512)
+    const int most = (!aligned ? (s.cols == 24 ? 512 : forward || s.cols == 8 ? 1024 : 512)
                                : s.cols == 8 ? 1024 : s.cols == 16 ? 800 : 512) / s.threads;
     per_sm = most < 1 ? 1 : most > 8 ? 8 : most;
   }
@@ -557,13 +621,22 @@ RowShape row_shape(int64_t n_rows, int n_cols, bool aligned, bool forward) {
   return s;
 }
 
+// Whether dweight and dbias are summed by columns in the launch that makes dx,
+// rather than from partial sums of its rows: x and dy are read twice, the
+// second time from L2, but there is one launch and no workspace. (512 x 4096
+// fp32 x: 12.6 us by columns, 14.2 by rows.)
+bool by_columns(int64_t n_rows, int n_cols) {
+  return n_rows <= 1024 && n_rows * n_cols <= (3 << 20) && n_cols <= 16 * 512;
+}
+
 constexpr int kMaxCols = INT32_MAX - 4096;
 constexpr int kRowGrid = kSms * 8;
-constexpr size_t kSmemBudget = 225 * 1024;  // of an SM's shared memory, for rings
+constexpr size_t kSmemPerSm = 228 * 1024;
+constexpr size_t kSmemStatic = 10 * 1024;  // of a backward CTA, with what the system reserves
 
 // Partial sums of dweight and dbias, at most (whichever kernel runs).
 int64_t backward_workspace(int64_t n_rows, int n_cols, bool want_params) {
-  if (!want_params || n_rows == 0) return 0;
+  if (!want_params || n_rows == 0 || by_columns(n_rows, n_cols)) return 0;
   int64_t parts = kLongParts;
   for (const bool aligned : {false, true}) {
     const RowShape s = row_shape(n_rows, n_cols, aligned, false);
@@ -587,12 +660,12 @@ spmv_status by_types(spmv_dtype x, spmv_dtype y, F&& f) {
 
 template <typename Args>
 spmv_status launch_rows(void (*fn)(Args), const RowShape& s, size_t smem, const Args& p,
-                        cudaStream_t st) {
+                        cudaStream_t st, int more_ctas = 0) {
   if (smem > 40 * 1024 &&  // 48 KB less the static part need no opt-in
       cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
                            cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return SPMV_ERR_CUDA;
-  fn<<<s.grid, s.threads, smem, st>>>(p);
+  fn<<<s.grid + more_ctas, s.threads, smem, st>>>(p);
   return launched();
 }
 
@@ -630,30 +703,61 @@ spmv_status forward(const ForwardArgs<XT, YT>& p, cudaStream_t st) {
 template <typename XT, typename YT, int CPT, bool WARP, bool ALIGNED>
 spmv_status backward_launch(const RowShape& s, const BackwardArgs<XT, YT>& p, cudaStream_t st) {
   constexpr int kVec = 16 / (int)sizeof(XT);
+  const int columns = p.dweight || p.dbias ? (p.n_cols + 31) / 32 : 0;  // CTAs for them
   if constexpr (!ALIGNED) {
     return launch_rows(layernorm_backward_fused<XT, YT, kVec, CPT, 0, 1, WARP>, s,
-                       (size_t)s.threads * CPT * 4, p, st);
+                       (size_t)s.threads * CPT * 4, p, st, columns);
   } else {
-    // Two rows at a time halve the barriers; where two sets of them do not
-    // fit, single rows. (A warp group's ring is larger than the two sums per
+    // Two rows at a time halve the barriers (a warp's rows need none); where
+    // two sets of them do not fit, single rows. (A warp group's ring is larger than the two sums per
     // column that the warps leave in its place at the end.)
     const size_t row = (size_t)s.threads * CPT * (sizeof(XT) + sizeof(YT));
-    const size_t room = kSmemBudget / (size_t)((s.grid + kSms - 1) / kSms);
+    const size_t room =
+        kSmemPerSm / (size_t)((s.grid + columns + kSms - 1) / kSms) - kSmemStatic;
     if constexpr (CPT < 32) {
-      if (4 * row <= room)
-        return launch_rows(layernorm_backward_fused<XT, YT, kVec, CPT, 2, 2, WARP>, s, 4 * row, p,
-                           st);
+      if constexpr (!WARP)
+        if (4 * row <= room)
+          return launch_rows(layernorm_backward_fused<XT, YT, kVec, CPT, 2, 2, false>, s, 4 * row,
+                             p, st, columns);
       if (3 * row <= room)
         return launch_rows(layernorm_backward_fused<XT, YT, kVec, CPT, 3, 1, WARP>, s, 3 * row, p,
-                           st);
+                           st, columns);
     }
-    return launch_rows(layernorm_backward_fused<XT, YT, kVec, CPT, 2, 1, WARP>, s, 2 * row, p, st);
+    return launch_rows(layernorm_backward_fused<XT, YT, kVec, CPT, 2, 1, WARP>, s, 2 * row, p, st,
+                       columns);
   }
 }
 
 template <typename XT, typename YT, bool ALIGNED>
-spmv_status backward(const BackwardArgs<XT, YT>& p, void* dweight, void* dbias, cudaStream_t st) {
-  const RowShape s = row_shape(p.n_rows, p.n_cols, ALIGNED, false);
+spmv_status backward(BackwardArgs<XT, YT> p, void* dweight, void* dbias, cudaStream_t st) {
+  RowShape s = row_shape(p.n_rows, p.n_cols, ALIGNED, false);
+  const bool columns = (dweight || dbias) && by_columns(p.n_rows, p.n_cols);
+  // two sets of 32 columns' rows in fp32 do not fit shared memory
+  if (s.cols == 32 && ALIGNED &&
+      2 * (size_t)s.threads * 32 * (sizeof(XT) + sizeof(YT)) > kSmemPerSm - kSmemStatic)
+    s.cols = 0;
+  if (columns) {
+    p.part = nullptr;
+    // CTAs of 16 warps at least, for the columns' rows
+    if (s.warp || (s.cols == 16 && p.n_cols <= 8 * 640)) {
+      s.warp = false;
+      s.cols = 8;
+      s.threads = ((p.n_cols + 7) / 8 + 31) / 32 * 32;
+    }
+    if (s.threads < 512) s.threads = 512;
+    const int64_t most = s.cols == 8 ? 2 * kSms : kSms;
+    s.grid = (int)(p.n_rows < most ? p.n_rows : most);
+    if (p.dx == static_cast<const void*>(p.dy)) {  // the columns first: dx takes dy's place
+      BackwardArgs<XT, YT> q = p;
+      q.dx = nullptr;
+      const spmv_status status = backward<XT, YT, ALIGNED>(q, dweight, dbias, st);
+      if (status != SPMV_OK) return status;
+    } else {
+      p.dweight = dweight, p.dbias = dbias;
+    }
+    if (!p.dx) s.grid = 0;
+  }
+  p.row_ctas = s.grid;
   int parts = s.grid;
   spmv_status status = SPMV_OK;
   if (s.warp) {
@@ -776,7 +880,8 @@ extern "C" spmv_status spmv_layernorm_backward(
     BackwardArgs<XT, YT> p{n_rows, n_cols, static_cast<const YT*>(dy), dy_stride,
                            static_cast<const XT*>(x), x_stride, weight, param_dtype, mean, rstd,
                            static_cast<XT*>(dx), dx_stride,
-                           params ? static_cast<float*>(workspace) : nullptr};
+                           params ? static_cast<float*>(workspace) : nullptr, 0, nullptr,
+                           nullptr};
     if (n_cols % kVec == 0 && rows_aligned(x, n_rows, x_stride, xs, kVec) &&
         rows_aligned(dy, n_rows, dy_stride, dys, kVec) &&
         (!dx || rows_aligned(dx, n_rows, dx_stride, xs, kVec)) && aligned_to(weight, 16))

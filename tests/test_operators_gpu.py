@@ -254,7 +254,9 @@ def check_grad(dy, x, w, param_type="f32", dy_layout=(None, 0), x_layout=(None, 
 @pytest.mark.parametrize("types", PAIRS, ids=lambda p: "-".join(p))
 @pytest.mark.parametrize("shape", [(1, 1), (3, 2), (5, 7), (64, 31), (7, 64), (33, 255), (400, 257), (9, 1000),
                                    (3, 1024), (700, 64), (2, 4099), (65, 2048), (11, 8192), (310, 12288),
-                                   (2, 20001), (1, 70003)], ids=lambda s: f"{s[0]}x{s[1]}")
+                                   (2, 20001), (1, 70003), (1025, 64), (1500, 300), (2000, 513), (1100, 1027), (1030, 2048),
+                                   (1200, 2051), (900, 5003), (1026, 4096), (600, 8195), (300, 16384)],
+                         ids=lambda s: f"{s[0]}x{s[1]}")
 def test_gradient(spmv_lib, shape, types):
     n, d = shape
     g = gen(n * 7 + d)
@@ -767,8 +769,9 @@ def test_wrong_tensors_are_refused(spmv_lib):
         S.spmv_layernorm(x.half(), None, None, x)
     with pytest.raises(TypeError):
         S.spmv_layernorm(x, None, None, x, mean=torch.zeros(4, dtype=torch.float16, device=DEV))
+    many = torch.zeros(5000, 8, device=DEV)
     with pytest.raises(S.SpmvError):
-        S.spmv_layernorm_backward(x, x, None, x[:, 0].contiguous(), x[:, 0].contiguous(), torch.zeros_like(x),
+        S.spmv_layernorm_backward(many, many, None, many[:, 0].contiguous(), many[:, 0].contiguous(), torch.zeros_like(many),
                                   torch.zeros(8, device=DEV), None, workspace=torch.zeros(0, dtype=torch.uint8, device=DEV))
     with pytest.raises(S.SpmvError):
         S.spmv_adapters_run(x, torch.zeros(2, 4, 8, device=DEV), torch.zeros(2, 8, 4, device=DEV),

@@ -56,7 +56,7 @@ def backward(lib, **kw):
     (dict(m=None), INVALID), (dict(r=None), INVALID), (dict(dyt=9), INVALID),
     (dict(dxs=4), INVALID), (dict(dx=DX + 2), INVALID), (dict(dy=Y + 1), INVALID),
     (dict(w=W + 1), INVALID), (dict(dw=DW + 2), INVALID), (dict(db=DB + 2), INVALID),
-    (dict(ws=WS + 8), INVALID), (dict(ws=None), INVALID), (dict(wn=0), INVALID),
+    (dict(ws=WS + 8), INVALID), (dict(n=5000, ws=None), INVALID), (dict(n=5000, wn=0), INVALID),
     (dict(dx=X), INVALID), (dict(dx=Y), INVALID), (dict(dx=Y + 32, dyt=F32), INVALID),
     (dict(xt=F16, dyt=BF16), UNSUPPORTED), (dict(d=2**31 - 1, xs=2**31, dys=2**31, dxs=2**31),
                                             TOO_LARGE),

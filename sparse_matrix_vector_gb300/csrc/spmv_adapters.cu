@@ -40,7 +40,7 @@ struct AdapterArgs {
   void* y;
   int64_t ys;
   int vec_in;    // rows of x and A, and n_in: 0 any, 1 whole 16 bytes, 2 whole 32 bytes
-  bool vec_b;    // rows of B: the same, with rank
+  int vec_b;     // rows of B, and rank: 0 any, 1 whole 16 bytes, 8 or 4: whole 8 or 4 bytes
   bool vec_y;    // rows of base and y: 4 elements aligned, n_out a multiple of 4
   // grouped tokens (workspace)
   int4* tiles;       // {slot or -1, first sorted position, tokens, unused}
@@ -83,16 +83,37 @@ __device__ __forceinline__ void mma32(float (&c)[4], const uint4& lo, const uint
   mma(static_cast<const T*>(nullptr), c, lo.z, hi.z, lo.w, hi.w, v.z, v.w);
 }
 
-// 8 elements at p of which `left` exist (the others are zero); vec: p is
-// 16-byte aligned and all 8 or none exist.
+// 8 elements at p of which `left` exist (the others are zero), in the largest
+// loads that `vec` allows: 1: 16 bytes, 8 or 4: that many, 0: single elements
+// (rows are a whole number of such loads).
 template <typename T>
-__device__ __forceinline__ uint4 load8(const T* p, int left, bool vec) {
-  if (vec) return left > 0 ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
-  const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
-  uint32_t e[8];
+__device__ __forceinline__ uint4 load8(const T* p, int left, int vec) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (vec == 1) {
+    if (left > 0) v = __ldg(reinterpret_cast<const uint4*>(p));
+  } else if (vec == 8) {
+    const uint2* q = reinterpret_cast<const uint2*>(p);
+    uint2 lo = make_uint2(0, 0), hi = lo;
+    if (left > 0) lo = __ldg(q);
+    if (left > 4) hi = __ldg(q + 1);
+    v = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  } else if (vec == 4) {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
+    if (left > 0) v.x = __ldg(q);
+    if (left > 2) v.y = __ldg(q + 1);
+    if (left > 4) v.z = __ldg(q + 2);
+    if (left > 6) v.w = __ldg(q + 3);
+  } else {
+    const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+    uint32_t e[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) e[k] = k < left ? __ldg(q + k) : 0u;
-  return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+    for (int k = 0; k < 8; ++k) {
+      e[k] = 0;
+      if (k < left) e[k] = __ldg(q + k);
+    }
+    v = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+  }
+  return v;
 }
 
 // 16 elements (32 bytes, aligned to it) in one load: a quarter-warp then
@@ -118,14 +139,15 @@ __device__ __forceinline__ void mma64(float (&c)[4], const Vec16& lo, const Vec1
         v.w[i + 1]);
 }
 
-// Ask L2 for `rows` rows of `bytes` bytes, `pitch` bytes apart, by the whole
-// CTA: memory is at work on all of them before the first load waits.
-__device__ __forceinline__ void prefetch_rows(const void* p, int rows, int64_t pitch,
-                                              int64_t bytes) {
-  const int lines = (int)((bytes + 127) / 128);
-  for (int i = threadIdx.x; i < rows * lines; i += blockDim.x)
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p) +
-                                                  (i / lines) * pitch + (i % lines) * 128));
+// Ask L2 for `rows` rows of `bytes` bytes, at(i) the i-th, a warp per row:
+// memory is at work on all of them before the first load waits.
+template <typename F>
+__device__ __forceinline__ void prefetch_rows(int rows, int bytes, F&& at) {
+  for (int i = threadIdx.x >> 5; i < rows; i += blockDim.x >> 5) {
+    const char* row = reinterpret_cast<const char*>(at(i));
+    for (int k = 128 * (threadIdx.x & 31); k < bytes; k += 128 * 32)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(row + k));
+  }
 }
 
 // The first `left` of 8 elements, zeros in place of the others.
@@ -143,13 +165,11 @@ __device__ __forceinline__ int rank_of(const AdapterArgs& p, int slot) {
 // acc[mt][nt] += rows j0 + 16 mt .. of A times tokens 8 nt .. over the inner
 // range [k0, k1), k0 a multiple of 64. Rows past the rank repeat its last row
 // (their h is not used); x[nt] is the row of this lane's token, any row where
-// there is none. `ahead`: row of the token whose lines this lane asks from L2
-// kAhead elements before they are loaded (null: none).
-constexpr int kAhead = 512;
+// there is none.
 
 template <typename T, int MT, int NT>
 __device__ __forceinline__ void shrink(const AdapterArgs& p, const T* a, int rank, int j0,
-                                       const T* const (&x)[NT], const T* ahead, int k0, int k1,
+                                       const T* const (&x)[NT], int k0, int k1,
                                        float (&acc)[MT][NT][4]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const T* rows[MT][2];
@@ -159,17 +179,9 @@ __device__ __forceinline__ void shrink(const AdapterArgs& p, const T* a, int ran
     for (int h = 0; h < 2; ++h)
       rows[m][h] = a + (int64_t)min(j0 + 16 * m + 8 * h + g, rank - 1) * p.n_in;
   int k = k0;
-  if (ahead)
-    for (int i = k0; i < min(k0 + kAhead, k1); i += 64)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(ahead + i));
-  const auto ask = [&] {
-    if (ahead && k + kAhead < k1)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(ahead + k + kAhead));
-  };
-  if constexpr (MT * NT < 16) {  // (more would not fit the registers)
+  if constexpr (MT * NT <= 16) {  // (more would not fit the registers)
     const int whole = p.vec_in == 2 ? k0 + max(min(k1, p.n_in) - k0, 0) / 64 * 64 : k0;
     for (; k < whole; k += 64) {
-      ask();
       Vec16 v[NT], w[MT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) v[n] = load16(x[n] + k + 16 * t);
@@ -186,7 +198,6 @@ __device__ __forceinline__ void shrink(const AdapterArgs& p, const T* a, int ran
   const int whole = p.vec_in ? k0 + max(min(k1, p.n_in) - k0, 0) / 32 * 32 : k0;
 #pragma unroll 2
   for (; k < whole; k += 32) {
-    if ((k & 32) == 0) ask();
     uint4 v[NT], w[MT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) v[n] = __ldg(reinterpret_cast<const uint4*>(x[n] + k + 8 * t));
@@ -201,15 +212,14 @@ __device__ __forceinline__ void shrink(const AdapterArgs& p, const T* a, int ran
       for (int n = 0; n < NT; ++n) mma32<T>(acc[m][n], w[m][0], w[m][1], v[n]);
   }
   for (; k < k1; k += 32) {  // the last, partial step; all steps of unaligned rows
-    if ((k & 32) == 0) ask();
     const int left = p.n_in - k - 8 * t;
     uint4 v[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) v[n] = load8(x[n] + k + 8 * t, left, p.vec_in);
+    for (int n = 0; n < NT; ++n) v[n] = load8(x[n] + k + 8 * t, left, p.vec_in ? 1 : 0);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const uint4 lo = load8(rows[m][0] + k + 8 * t, left, p.vec_in);
-      const uint4 hi = load8(rows[m][1] + k + 8 * t, left, p.vec_in);
+      const uint4 lo = load8(rows[m][0] + k + 8 * t, left, p.vec_in ? 1 : 0);
+      const uint4 hi = load8(rows[m][1] + k + 8 * t, left, p.vec_in ? 1 : 0);
 #pragma unroll
       for (int n = 0; n < NT; ++n) mma32<T>(acc[m][n], lo, hi, v[n]);
     }
@@ -382,9 +392,8 @@ constexpr int kPitch = kMaxRank + 8;  // 16-bit elements per token: rows on othe
 // CTA finds for itself. Each CTA takes a share of the inner
 // range of A x; the shares meet in distributed shared memory; then each CTA
 // takes a share of y's columns. One launch, no workspace. What the second
-// product needs does not depend on the first: B's share is asked from L2 at
-// the start, and the first step's B and base are in registers before the
-// shares meet.
+// product needs does not depend on the first: B's share is asked from L2, and
+// the first step's B and base are loaded, before the shares meet.
 constexpr int kFewTokens = 256;
 constexpr int kGroup = 8;
 
@@ -403,7 +412,7 @@ __device__ __forceinline__ void few_shrink(const AdapterArgs& p, const T* a, int
   const int2 mine_k = inner_share(k0, k1, warp, WARPS);
   float acc[MT][1][4] = {};
   const T* const xs[1] = {x};
-  shrink<T, MT, 1>(p, a, rank, j0, xs, nullptr, mine_k.x, mine_k.y, acc);
+  shrink<T, MT, 1>(p, a, rank, j0, xs, mine_k.x, mine_k.y, acc);
   // [warp][token][16 MT]
   float* mine = s_warp + warp * kGroup * 16 * MT;
 #pragma unroll
@@ -501,15 +510,7 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) adapters_few(AdapterAr
     const T* a = static_cast<const T*>(p.a) + (int64_t)slot * p.rank * p.n_in;
     const T* b = static_cast<const T*>(p.b) + (int64_t)slot * p.n_out * p.rank;
     __syncthreads();
-    prefetch_rows(a + k0, rank, (int64_t)p.n_in * (int)sizeof(T), (k1 - k0) * (int64_t)sizeof(T));
-    prefetch_rows(b + (int64_t)o0 * p.rank, 1, 0, (int64_t)(o1 - o0) * p.rank * (int)sizeof(T));
-    if (p.base) {
-      const int lines = ((o1 - o0) * (int)sizeof(YT) + 127) / 128;
-      for (int i = threadIdx.x; i < n_tokens * lines; i += 32 * WARPS)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(
-            reinterpret_cast<const char*>(static_cast<const YT*>(p.base) +
-                                          s_token[i / lines] * p.bs + o0) + (i % lines) * 128));
-    }
+    prefetch_rows(rank, (k1 - k0) * (int)sizeof(T), [&](int i) { return a + (int64_t)i * p.n_in + k0; });
     const T* x = static_cast<const T*>(p.x) + s_token[min(lane >> 2, n_tokens - 1)] * p.xs;
     if (rank <= 16)
       few_shrink<T, 1, WARPS>(p, a, rank, 0, x, k0, k1, s_mem.warps, s_part);
@@ -519,15 +520,28 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) adapters_few(AdapterAr
       for (int j0 = 0; j0 < rank; j0 += 64)
         few_shrink<T, 4, WARPS>(p, a, rank, j0, x, k0, k1, s_mem.warps, s_part);
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    // (any earlier, B would take its share of the memory from A)
+    const char* share = reinterpret_cast<const char*>(b + (int64_t)o0 * p.rank);
+    for (int64_t i = 128ll * threadIdx.x; i < (int64_t)(o1 - o0) * p.rank * (int)sizeof(T);
+         i += 128ll * 32 * WARPS)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(share + i));
+    if (p.base)
+      prefetch_rows(n_tokens, (o1 - o0) * (int)sizeof(YT), [&](int i) {
+        return static_cast<const YT*>(p.base) + s_token[i] * p.bs + o0;
+      });
     const int nk = (rank + 31) / 32;
+    // a step's base and first 32 columns of B: two steps are under way at a time
+    struct Step {
+      uint4 w[4];
+      Pack<YT, 4> v[1][2];
+    } now, then;
+    const auto load_step = [&](Step& s, int o) {
+      if (o >= o1) return;
+      load_b(p, b, rank, 0, o, s.w);
+      load_base<YT, 1>(p, s_token, n_tokens, o, s.v);
+    };
     int o = o0 + 32 * warp;
-    uint4 w0[4], w1[4];
-    Pack<YT, 4> v[1][2];
-    if (o < o1) {
-      load_b(p, b, rank, 0, o, w0);
-      if (nk > 1) load_b(p, b, rank, 1, o, w1);
-      load_base<YT, 1>(p, s_token, n_tokens, o, v);
-    }
+    load_step(now, o);
     const float scale = p.scales ? p.scales[slot] : 1.f;
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (warp < n_tokens) {  // a warp per token: its h over the cluster's shares
@@ -554,21 +568,23 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) adapters_few(AdapterAr
     __syncthreads();
     // the others may still read this CTA's share: its memory changes after them
     asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-    while (o < o1) {
+    const auto do_step = [&](Step& s, int o) {
       float acc[2][1][4] = {};
-      expand<T, 1>(w0, s_mem.h, kPitch, kGroup * kPitch, acc);
-      if (nk > 1) expand<T, 1>(w1, s_mem.h + 32, kPitch, kGroup * kPitch, acc);
-      for (int k = 2; k < nk; ++k) {
-        load_b(p, b, rank, k, o, w0);
-        expand<T, 1>(w0, s_mem.h + 32 * k, kPitch, kGroup * kPitch, acc);
+      expand<T, 1>(s.w, s_mem.h, kPitch, kGroup * kPitch, acc);
+      for (int k = 1; k < nk; ++k) {
+        load_b(p, b, rank, k, o, s.w);
+        expand<T, 1>(s.w, s_mem.h + 32 * k, kPitch, kGroup * kPitch, acc);
       }
-      finish<YT, 1>(p, s_token, n_tokens, s_down, scale, o, v, acc);
+      finish<YT, 1>(p, s_token, n_tokens, s_down, scale, o, s.v, acc);
+    };
+    while (o < o1) {
+      load_step(then, o + 32 * WARPS);
+      do_step(now, o);
       o += 32 * WARPS;
-      if (o < o1) {
-        load_b(p, b, rank, 0, o, w0);
-        if (nk > 1) load_b(p, b, rank, 1, o, w1);
-        load_base<YT, 1>(p, s_token, n_tokens, o, v);
-      }
+      if (o >= o1) break;
+      load_step(now, o + 32 * WARPS);
+      do_step(then, o);
+      o += 32 * WARPS;
     }
     __syncthreads();
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
@@ -650,49 +666,76 @@ __global__ void __launch_bounds__(kSortThreads) adapters_sort(AdapterArgs p) {
   }
 }
 
-// Warps of a CTA: two halves of the tile's tokens times four shares of the
-// CTA's inner range, or eight shares where the tile has half its tokens at
-// most. The sums go to s_sum, [token][sum_pitch].
-template <typename T, int MT>
+// The warps take shares of the CTA's inner range, each for all of the tile's
+// tokens (8 NT of them at most): A is read once per tile. Their sums meet in
+// s_warp, [warp][token][16 MT + 1], and go to s_sum, [token][sum_pitch].
+template <typename T, int MT, int NT>
 __device__ __forceinline__ void tile_shrink(const AdapterArgs& p, const T* a, int rank, int j0,
-                                            const T* const (&x)[4], const T* ahead, int halves,
-                                            int k0, int k1, float* s_sum, int sum_pitch) {
+                                            const int32_t* tokens, int n_tokens, int k0, int k1,
+                                            float* s_warp, float* s_sum, int sum_pitch) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int half = warp % halves, share = warp / halves, shares = kWarps / halves;
-  const int2 mine = inner_share(k0, k1, share, shares);
-  float acc[MT][4][4] = {};
-  shrink<T, MT, 4>(p, a, rank, j0, x, ahead, mine.x, mine.y, acc);
-  for (int s = 0; s < shares; ++s) {
-    if (share == s) {
+  const T* x[NT];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+  for (int n = 0; n < NT; ++n)
+    x[n] = static_cast<const T*>(p.x) + tokens[min(8 * n + g, n_tokens - 1)] * p.xs;
+  const int2 mine = inner_share(k0, k1, warp, kWarps);
+  float acc[MT][NT][4] = {};
+  shrink<T, MT, NT>(p, a, rank, j0, x, mine.x, mine.y, acc);
+  constexpr int kWide = 16 * MT + 1;
+  float* out = s_warp + warp * 8 * NT * kWide;
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float* at = s_sum + (32 * half + 8 * n + 2 * t + (e & 1)) * sum_pitch + j0 + 16 * m +
-                        g + 8 * (e >> 1);
-            *at = s ? *at + acc[m][n][e] : acc[m][n][e];
-          }
-    }
-    __syncthreads();
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        out[(8 * n + 2 * t + (e & 1)) * kWide + 16 * m + g + 8 * (e >> 1)] = acc[m][n][e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < n_tokens * 16 * MT; i += kThreads) {
+    const int token = i / (16 * MT), j = i % (16 * MT);
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += s_warp[(w * 8 * NT + token) * kWide + j];
+    s_sum[token * sum_pitch + j0 + j] = v;
   }
+  __syncthreads();
+}
+
+// tile_shrink over a slot's rank, by blocks of 64.
+template <typename T, bool WIDE, int NT>
+__device__ __forceinline__ void tile_shrink_all(const AdapterArgs& p, const T* a, int rank,
+                                                const int32_t* tokens, int n_tokens, int k0,
+                                                int k1, float* s_warp, float* s_sum, int pitch) {
+  if (rank <= 16)
+    tile_shrink<T, 1, NT>(p, a, rank, 0, tokens, n_tokens, k0, k1, s_warp, s_sum, pitch);
+  else if (rank <= 32)
+    tile_shrink<T, 2, NT>(p, a, rank, 0, tokens, n_tokens, k0, k1, s_warp, s_sum, pitch);
+  if constexpr (WIDE)
+    if (rank > 32)
+      for (int j0 = 0; j0 < rank; j0 += 64)
+        tile_shrink<T, 4, NT>(p, a, rank, j0, tokens, n_tokens, k0, k1, s_warp, s_sum, pitch);
 }
 
 // Columns of a token's sums: whole blocks of 16 MT, on other banks.
 constexpr int sum_pitch_of(int rank) {
   return (rank <= 16 ? 16 : rank <= 32 ? 32 : (rank + 63) / 64 * 64) + 4;
 }
+// Floats of the warps' sums, for tiles of kTile tokens.
+constexpr int warp_sums_of(int rank) {
+  return kWarps * kTile * ((rank <= 16 ? 16 : rank <= 32 ? 32 : 64) + 1);
+}
 
 template <typename T, bool WIDE>  // WIDE: ranks above 32
-__global__ void __launch_bounds__(kThreads, 2) adapters_shrink(AdapterArgs p) {
-  extern __shared__ float s_sum[];  // kTile x sum_pitch_of(p.rank)
+__global__ void __launch_bounds__(kThreads, 1) adapters_shrink(AdapterArgs p) {
+  extern __shared__ float s_dyn_sum[];  // kTile x sum_pitch_of(p.rank), then the warps' sums
   pdl_launch_dependents();
   cg::cluster_group cluster = cg::this_cluster();
   const int split = blockIdx.x % p.k_split;
   const int2 inner = inner_share(0, p.n_in, split, p.k_split);
   const int k0 = inner.x, k1 = inner.y, pitch = sum_pitch_of(p.rank);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* s_sum = s_dyn_sum;
+  float* s_warp = s_sum + kTile * pitch;
   pdl_wait();
   const int n_tiles = *p.n_tiles;
   // every CTA of a cluster goes through the same tiles
@@ -701,22 +744,12 @@ __global__ void __launch_bounds__(kThreads, 2) adapters_shrink(AdapterArgs p) {
     const int rank = tile.x < 0 ? 0 : rank_of(p, tile.x);
     if (rank == 0) continue;
     const T* a = static_cast<const T*>(p.a) + (int64_t)tile.x * p.rank * p.n_in;
-    const int halves = tile.z > 32 ? 2 : 1, first = 32 * (warp % halves);
-    const auto row = [&](int k) {
-      return static_cast<const T*>(p.x) + p.perm[tile.y + min(k, tile.z - 1)] * p.xs;
-    };
-    const T* x[4];
-#pragma unroll
-    for (int n = 0; n < 4; ++n) x[n] = row(first + 8 * n + g);
-    const T* ahead = first + lane < tile.z ? row(first + lane) : nullptr;
-    if (rank <= 16)
-      tile_shrink<T, 1>(p, a, rank, 0, x, ahead, halves, k0, k1, s_sum, pitch);
-    else if (rank <= 32)
-      tile_shrink<T, 2>(p, a, rank, 0, x, ahead, halves, k0, k1, s_sum, pitch);
-    if constexpr (WIDE)
-      if (rank > 32)
-        for (int j0 = 0; j0 < rank; j0 += 64)
-          tile_shrink<T, 4>(p, a, rank, j0, x, j0 ? nullptr : ahead, halves, k0, k1, s_sum, pitch);
+    if (tile.z > 32)
+      tile_shrink_all<T, WIDE, 8>(p, a, rank, p.perm + tile.y, tile.z, k0, k1, s_warp, s_sum, pitch);
+    else if (tile.z > 8)
+      tile_shrink_all<T, WIDE, 4>(p, a, rank, p.perm + tile.y, tile.z, k0, k1, s_warp, s_sum, pitch);
+    else
+      tile_shrink_all<T, WIDE, 1>(p, a, rank, p.perm + tile.y, tile.z, k0, k1, s_warp, s_sum, pitch);
     cluster.sync();
     // a warp per token: its h over the cluster's shares, as 16-bit terms
     const int nk = (rank + 31) / 32;
@@ -750,6 +783,10 @@ __host__ __device__ constexpr int pitch_of(int row) {
   return row * (int)sizeof(T) % 128 == 64 ? row : row + 64 / (int)sizeof(T);
 }
 
+// base's steps are on their way into shared memory, each lane's own places,
+// while the step before is multiplied and stored.
+constexpr int kBaseStages = 2;
+
 template <typename T, typename YT>
 __global__ void __launch_bounds__(kThreads, 2) adapters_expand(AdapterArgs p) {
   extern __shared__ __align__(16) unsigned char s_dyn[];
@@ -758,6 +795,10 @@ __global__ void __launch_bounds__(kThreads, 2) adapters_expand(AdapterArgs p) {
   __shared__ float s_down[kTile];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = Terms<T>::n * p.term_pitch, pitch = pitch_of<T>(row);
+  using P = Pack<YT, 4>;
+  // [stage][warp][8 places][lane]
+  P* ring = reinterpret_cast<P*>(s_dyn + (size_t)kTile * pitch * sizeof(T)) + warp * 256 + lane;
+  const bool async = p.base && p.vec_y;
   pdl_wait();
   // (tile, 128 columns) steps in equal contiguous shares
   const int per_tile = (p.n_out + 127) / 128;
@@ -795,27 +836,53 @@ __global__ void __launch_bounds__(kThreads, 2) adapters_expand(AdapterArgs p) {
     // eight blocks where the tile has half its tokens at most
     const int halves = tile.z > 32 ? 2 : 1, half = warp % halves, n_tokens = tile.z - 32 * half;
     const T* h = s_h + 32 * half * pitch;
+    const int* tokens = s_token + 32 * half;
     const int stride = 32 * kWarps / halves;
-    const YT* ahead = p.base && lane < n_tokens
-                          ? static_cast<const YT*>(p.base) + s_token[32 * half + lane] * p.bs
-                          : nullptr;
-    for (int o = o0 + 32 * (warp / halves); o < o1; o += stride) {
-      Pack<YT, 4> v[4][2];
-      load_base<YT, 4>(p, s_token + 32 * half, n_tokens, o, v);
-      if (ahead && o + stride < o1)  // this warp's next columns, from L2
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(ahead + o + stride));
+    const auto fetch = [&](int o, int stage) {
+      if (o < o1) {
+        const int g = lane & 7, t = lane >> 3, c = o + 4 * g;
+        const YT* at = static_cast<const YT*>(p.base) + c;
+        P* to = ring + stage * kWarps * 256;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int i = 8 * (k >> 1) + 2 * t + (k & 1);
+          if (i < n_tokens && c < p.n_out)
+            copy_async<sizeof(P)>(to + 32 * k, at + tokens[i] * p.bs);
+        }
+      }
+      copy_commit();
+    };
+    int o = o0 + 32 * (warp / halves), stage = 0;
+    if (async) {
+#pragma unroll
+      for (int k = 0; k < kBaseStages - 1; ++k) fetch(o + k * stride, k);
+    }
+    uint4 w[4];
+    if (o < o1) load_b(p, b, rank, 0, o, w);
+    for (; o < o1; o += stride) {
+      if (async) fetch(o + (kBaseStages - 1) * stride, (stage + kBaseStages - 1) % kBaseStages);
       float acc[2][4][4] = {};
-      for (int k = 0; k < nk; ++k) {
-        uint4 w[4];
+      expand<T, 4>(w, h, pitch, p.term_pitch, acc);
+      for (int k = 1; k < nk; ++k) {
         load_b(p, b, rank, k, o, w);
         expand<T, 4>(w, h + 32 * k, pitch, p.term_pitch, acc);
       }
-      finish<YT, 4>(p, s_token + 32 * half, n_tokens, s_down + 32 * half, scale, o, v, acc);
+      if (o + stride < o1) load_b(p, b, rank, 0, o + stride, w);
+      P v[4][2];
+      if (async) {
+        copy_wait<kBaseStages - 1>();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k >> 1][k & 1] = ring[stage * kWarps * 256 + 32 * k];
+        stage = (stage + 1) % kBaseStages;
+      } else {
+        load_base<YT, 4>(p, tokens, n_tokens, o, v);
+      }
+      finish<YT, 4>(p, tokens, n_tokens, s_down + 32 * half, scale, o, v, acc);
     }
   }
 }
 
-constexpr int kWave = 2 * 152;  // CTAs that the device's SMs hold at a time, two each
+constexpr int kSms = 152;
 constexpr int kMaxTokens = 1 << 27, kMaxWidth = 1 << 30;  // (32-bit grids and columns)
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -833,7 +900,7 @@ Workspace workspace_of(int n_tokens, int n_slots, int rank) {
   // one wave of CTAs, with tiles as full as can be
   const int tiles = (n_tokens + kTile - 1) / kTile;
   w.k_split = 1;
-  while (w.k_split < kMaxSplit && tiles * 2 * w.k_split <= kWave) w.k_split *= 2;
+  while (w.k_split < kMaxSplit && tiles * 2 * w.k_split <= kSms) w.k_split *= 2;
   w.term_pitch = (rank + 31) / 32 * 32;
   w.tiles = 16;
   w.perm = round_up(w.tiles + 16ll * w.max_tiles, 128);
@@ -890,8 +957,9 @@ spmv_status run_few(AdapterArgs& p, cudaStream_t st) {
 template <typename T, typename YT>
 spmv_status run_many(AdapterArgs& p, cudaStream_t st) {
   const size_t sort_smem = (size_t)(p.n_slots + 1) * 4;
-  const size_t shrink_smem = (size_t)kTile * sum_pitch_of(p.rank) * 4;
-  const size_t expand_smem = (size_t)kTile * pitch_of<T>(Terms<T>::n * p.term_pitch) * sizeof(T);
+  const size_t shrink_smem = ((size_t)kTile * sum_pitch_of(p.rank) + warp_sums_of(p.rank)) * 4;
+  const size_t expand_smem = (size_t)kTile * pitch_of<T>(Terms<T>::n * p.term_pitch) * sizeof(T) +
+                             (size_t)kBaseStages * kThreads * 8 * sizeof(Pack<YT, 4>);
   const void* shrink_fn = p.rank > 32 ? reinterpret_cast<const void*>(&adapters_shrink<T, true>)
                                       : reinterpret_cast<const void*>(&adapters_shrink<T, false>);
   const void* expand_fn = reinterpret_cast<const void*>(&adapters_expand<T, YT>);
@@ -901,13 +969,15 @@ spmv_status run_many(AdapterArgs& p, cudaStream_t st) {
   adapters_sort<<<1, kSortThreads, sort_smem, st>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SPMV_ERR_CUDA;
   void* args[] = {&p};
-  // two CTAs per SM, or fewer where there is less to do
+  const int most = resident_clusters(shrink_fn, p.k_split, kThreads, shrink_smem);
+  if (most == 0) return SPMV_ERR_CUDA;
+  const int clusters = p.max_tiles < most ? p.max_tiles : most;
+  // (two CTAs per SM where the terms of a large rank leave room for them)
+  const int64_t wave = expand_smem <= 112 * 1024 ? 2 * kSms : kSms;
   const int64_t steps = (int64_t)p.max_tiles * ((p.n_out + 127) / 128);
-  const int clusters = p.max_tiles < kWave / p.k_split ? p.max_tiles : kWave / p.k_split;
   if (launch_cluster(shrink_fn, clusters * p.k_split, kThreads, shrink_smem, p.k_split, true, st,
                      args) != 0 ||
-      launch_pdl(expand_fn, (int)(steps < kWave ? steps : kWave), kThreads, expand_smem, st,
-                 args) != 0)
+      launch_pdl(expand_fn, (int)(steps < wave ? steps : wave), kThreads, expand_smem, st, args) != 0)
     return SPMV_ERR_CUDA;
   return SPMV_OK;
 }
@@ -975,7 +1045,10 @@ extern "C" spmv_status spmv_adapters_run(int32_t n_tokens, int32_t n_in, int32_t
   if (p.vec_in && n_in % 16 == 0 && aligned_to(x, 32) && aligned_to(a, 32) &&
       (n_tokens == 1 || x_stride % 16 == 0))
     p.vec_in = 2;
-  p.vec_b = rank % 8 == 0 && aligned_to(b, 16);
+  p.vec_b = rank % 8 == 0 && aligned_to(b, 16)  ? 1
+            : rank % 4 == 0 && aligned_to(b, 8) ? 8
+            : rank % 2 == 0 && aligned_to(b, 4) ? 4
+                                                : 0;
   p.vec_y = n_out % 4 == 0 && rows_aligned(y, n_tokens, y_stride, ysz, 4) &&
             (!base || rows_aligned(base, n_tokens, base_stride, ysz, 4));
   if (w.bytes > 0) {

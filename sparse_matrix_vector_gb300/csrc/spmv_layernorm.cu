@@ -19,25 +19,6 @@ __device__ __forceinline__ float cta_sum_all(float v, float* s_red) {
   return warp_sum(lane < (int)(blockDim.x >> 5) ? s_red[lane] : 0.f);
 }
 
-// This thread's asynchronous copies of 4, 8 or 16 bytes into shared memory,
-// in groups; each thread reads back only what it copied itself, so waiting
-// for its own groups is all the synchronisation there is.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void* dst, const void* src) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src),
-                 "n"(BYTES)
-                 : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
-}
-
 // Columns a thread holds of its rows, and the threads a CTA has at most with
 // them: more columns, or the addresses of single elements, take more
 // registers and leave room for fewer threads.

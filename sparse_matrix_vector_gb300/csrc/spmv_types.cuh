@@ -10,6 +10,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "spmv_device.cuh"
 #include "spmv_internal.h"
 
 namespace spmv {
@@ -85,6 +86,25 @@ __device__ __forceinline__ void store_pack(T* p, const Pack<T, N>& r) {
 #pragma unroll
   for (int i = 0; i < kBytes / kPart; ++i)
     reinterpret_cast<B*>(p)[i] = reinterpret_cast<const B*>(&r)[i];
+}
+
+// This thread's asynchronous copies of 4, 8 or 16 bytes into shared memory,
+// in groups; each thread reads back only what it copied itself, so waiting
+// for its own groups is all the synchronisation there is.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src),
+                 "n"(BYTES)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
 // ------------------------------------------------- a thread's columns of a row

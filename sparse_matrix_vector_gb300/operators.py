@@ -7,11 +7,12 @@ Only argument marshalling lives here. Tensors are CUDA tensors of one device,
 which is the current one; matrices have contiguous columns and any row
 stride. Calls run on ``stream`` (default: the current torch stream) and do
 not synchronize. A workspace that the caller does not give comes from torch's
-caching allocator.
+caching allocator; the default stream's is kept for its next call.
 """
 from __future__ import annotations
 
 import ctypes
+import threading
 
 import torch
 
@@ -24,6 +25,11 @@ _F32, _I32, _I64 = torch.float32, torch.int32, torch.int64
 _current_device = torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (absent in CPU builds)
 _library = None
+# Workspaces of the default stream, one per thread and device, kept for the
+# next call: its calls are in order, and it can be neither captured nor
+# destroyed. (Taking one from the allocator between launches costs 4 us and
+# makes the launches 2 us slower, of some 20 us a call.)
+_kept = threading.local()
 
 
 def _lib_handle():
@@ -100,6 +106,15 @@ def _workspace(given, n_bytes: int, stream, handle: int, dev: int):
         return given.data_ptr(), given.numel() * given.element_size(), given
     if n_bytes == 0:
         return None, 0, None
+    if handle == 0:
+        try:
+            kept = _kept.by_device
+        except AttributeError:
+            kept = _kept.by_device = {}
+        ws = kept.get(dev)
+        if ws is None or ws.numel() < n_bytes:
+            ws = kept[dev] = torch.empty(n_bytes, dtype=torch.uint8, device=dev)
+        return ws.data_ptr(), n_bytes, ws
     ws = torch.empty(n_bytes, dtype=torch.uint8, device=dev)
     if stream is not None and handle != _raw_stream(dev):
         ws.record_stream(torch.cuda.ExternalStream(handle, device=dev))

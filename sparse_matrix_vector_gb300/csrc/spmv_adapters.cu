@@ -116,6 +116,25 @@ __device__ __forceinline__ uint4 load8(const T* p, int left, int vec) {
   return v;
 }
 
+// 8 elements at any p (2-byte aligned) of which the 7 before and the 16 from p
+// on exist too: the two 16-byte granules around them, shifted into place.
+// (Against 8 loads of an element: a third of the L1 accesses.)
+template <typename T>
+__device__ __forceinline__ uint4 load8_shifted(const T* p) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const uint4* q = reinterpret_cast<const uint4*>(at & ~uintptr_t(15));
+  const uint4 a = __ldg(q), b = __ldg(q + 1);
+  const bool by2 = at & 8, by1 = at & 4;
+  const uint32_t half = 8 * (uint32_t)(at & 2);
+  // words from the one that holds p's element on
+  const uint32_t u0 = by2 ? a.z : a.x, u1 = by2 ? a.w : a.y, u2 = by2 ? b.x : a.z,
+                 u3 = by2 ? b.y : a.w, u4 = by2 ? b.z : b.x, u5 = by2 ? b.w : b.y;
+  const uint32_t v0 = by1 ? u1 : u0, v1 = by1 ? u2 : u1, v2 = by1 ? u3 : u2, v3 = by1 ? u4 : u3,
+                 v4 = by1 ? u5 : u4;
+  return make_uint4(__funnelshift_r(v0, v1, half), __funnelshift_r(v1, v2, half),
+                    __funnelshift_r(v2, v3, half), __funnelshift_r(v3, v4, half));
+}
+
 // 16 elements (32 bytes, aligned to it) in one load: a quarter-warp then
 // covers two whole 128-byte lines.
 struct Vec16 {
@@ -165,9 +184,8 @@ __device__ __forceinline__ int rank_of(const AdapterArgs& p, int slot) {
 // acc[mt][nt] += rows j0 + 16 mt .. of A times tokens 8 nt .. over the inner
 // range [k0, k1), k0 a multiple of 64. Rows past the rank repeat its last row
 // (their h is not used); x[nt] is the row of this lane's token, any row where
-// there is none.
-
-template <typename T, int MT, int NT>
+// there is none. ANY: rows of any alignment.
+template <typename T, int MT, int NT, bool ANY>
 __device__ __forceinline__ void shrink(const AdapterArgs& p, const T* a, int rank, int j0,
                                        const T* const (&x)[NT], int k0, int k1,
                                        float (&acc)[MT][NT][4]) {
@@ -179,7 +197,7 @@ __device__ __forceinline__ void shrink(const AdapterArgs& p, const T* a, int ran
     for (int h = 0; h < 2; ++h)
       rows[m][h] = a + (int64_t)min(j0 + 16 * m + 8 * h + g, rank - 1) * p.n_in;
   int k = k0;
-  if constexpr (MT * NT <= 16) {  // (more would not fit the registers)
+  if constexpr (!ANY && MT * NT <= 16) {  // (more would not fit the registers)
     const int whole = p.vec_in == 2 ? k0 + max(min(k1, p.n_in) - k0, 0) / 64 * 64 : k0;
     for (; k < whole; k += 64) {
       Vec16 v[NT], w[MT][2];
@@ -195,35 +213,57 @@ __device__ __forceinline__ void shrink(const AdapterArgs& p, const T* a, int ran
         for (int n = 0; n < NT; ++n) mma64<T>(acc[m][n], w[m][0], w[m][1], v[n]);
     }
   }
-  const int whole = p.vec_in ? k0 + max(min(k1, p.n_in) - k0, 0) / 32 * 32 : k0;
+  if constexpr (!ANY) {
+    const int whole = k0 + max(min(k1, p.n_in) - k0, 0) / 32 * 32;
 #pragma unroll 2
-  for (; k < whole; k += 32) {
-    uint4 v[NT], w[MT][2];
+    for (; k < whole; k += 32) {
+      uint4 v[NT], w[MT][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) v[n] = __ldg(reinterpret_cast<const uint4*>(x[n] + k + 8 * t));
+      for (int n = 0; n < NT; ++n) v[n] = __ldg(reinterpret_cast<const uint4*>(x[n] + k + 8 * t));
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        w[m][h] = __ldg(reinterpret_cast<const uint4*>(rows[m][h] + k + 8 * t));
+        for (int h = 0; h < 2; ++h)
+          w[m][h] = __ldg(reinterpret_cast<const uint4*>(rows[m][h] + k + 8 * t));
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma32<T>(acc[m][n], w[m][0], w[m][1], v[n]);
+        for (int n = 0; n < NT; ++n) mma32<T>(acc[m][n], w[m][0], w[m][1], v[n]);
+    }
   }
-  for (; k < k1; k += 32) {  // the last, partial step; all steps of unaligned rows
+  const auto single = [&] {
     const int left = p.n_in - k - 8 * t;
     uint4 v[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) v[n] = load8(x[n] + k + 8 * t, left, p.vec_in ? 1 : 0);
+    for (int n = 0; n < NT; ++n) v[n] = load8(x[n] + k + 8 * t, left, ANY ? 0 : 1);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const uint4 lo = load8(rows[m][0] + k + 8 * t, left, p.vec_in ? 1 : 0);
-      const uint4 hi = load8(rows[m][1] + k + 8 * t, left, p.vec_in ? 1 : 0);
+      const uint4 lo = load8(rows[m][0] + k + 8 * t, left, ANY ? 0 : 1);
+      const uint4 hi = load8(rows[m][1] + k + 8 * t, left, ANY ? 0 : 1);
 #pragma unroll
       for (int n = 0; n < NT; ++n) mma32<T>(acc[m][n], lo, hi, v[n]);
     }
+  };
+  if constexpr (ANY) {  // all but the first and last steps of a row
+    if (k == 0 && k < k1) {
+      single();
+      k += 32;
+    }
+    for (; k < k1 && k + 40 <= p.n_in; k += 32) {
+      uint4 v[NT], w[MT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) v[n] = load8_shifted(x[n] + k + 8 * t);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) w[m][h] = load8_shifted(rows[m][h] + k + 8 * t);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma32<T>(acc[m][n], w[m][0], w[m][1], v[n]);
+    }
   }
+  for (; k < k1; k += 32) single();
 }
 
 // Share i of n of the inner range, in whole steps of 64.
@@ -404,7 +444,7 @@ union FewShared {
   T h[Terms<T>::n * kGroup * kPitch];
 };
 
-template <typename T, int MT, int WARPS>
+template <typename T, int MT, int WARPS, bool ANY>
 __device__ __forceinline__ void few_shrink(const AdapterArgs& p, const T* a, int rank, int j0,
                                            const T* x, int k0, int k1, float* s_warp,
                                            float* s_part) {
@@ -412,7 +452,7 @@ __device__ __forceinline__ void few_shrink(const AdapterArgs& p, const T* a, int
   const int2 mine_k = inner_share(k0, k1, warp, WARPS);
   float acc[MT][1][4] = {};
   const T* const xs[1] = {x};
-  shrink<T, MT, 1>(p, a, rank, j0, xs, mine_k.x, mine_k.y, acc);
+  shrink<T, MT, 1, ANY>(p, a, rank, j0, xs, mine_k.x, mine_k.y, acc);
   // [warp][token][16 MT]
   float* mine = s_warp + warp * kGroup * 16 * MT;
 #pragma unroll
@@ -469,7 +509,7 @@ __device__ __forceinline__ int few_groups(const AdapterArgs& p, int* s_ids, int2
   return all;
 }
 
-template <typename T, typename YT, int CTAS, int WARPS>
+template <typename T, typename YT, int CTAS, int WARPS, bool ANY>
 __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) adapters_few(AdapterArgs p) {
   __shared__ __align__(16) int s_ids[kFewTokens];
   __shared__ int2 s_group[kFewTokens];
@@ -513,12 +553,12 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) adapters_few(AdapterAr
     prefetch_rows(rank, (k1 - k0) * (int)sizeof(T), [&](int i) { return a + (int64_t)i * p.n_in + k0; });
     const T* x = static_cast<const T*>(p.x) + s_token[min(lane >> 2, n_tokens - 1)] * p.xs;
     if (rank <= 16)
-      few_shrink<T, 1, WARPS>(p, a, rank, 0, x, k0, k1, s_mem.warps, s_part);
+      few_shrink<T, 1, WARPS, ANY>(p, a, rank, 0, x, k0, k1, s_mem.warps, s_part);
     else if (rank <= 32)
-      few_shrink<T, 2, WARPS>(p, a, rank, 0, x, k0, k1, s_mem.warps, s_part);
+      few_shrink<T, 2, WARPS, ANY>(p, a, rank, 0, x, k0, k1, s_mem.warps, s_part);
     else
       for (int j0 = 0; j0 < rank; j0 += 64)
-        few_shrink<T, 4, WARPS>(p, a, rank, j0, x, k0, k1, s_mem.warps, s_part);
+        few_shrink<T, 4, WARPS, ANY>(p, a, rank, j0, x, k0, k1, s_mem.warps, s_part);
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     // (any earlier, B would take its share of the memory from A)
     const char* share = reinterpret_cast<const char*>(b + (int64_t)o0 * p.rank);
@@ -669,7 +709,7 @@ __global__ void __launch_bounds__(kSortThreads) adapters_sort(AdapterArgs p) {
 // The warps take shares of the CTA's inner range, each for all of the tile's
 // tokens (8 NT of them at most): A is read once per tile. Their sums meet in
 // s_warp, [warp][token][16 MT + 1], and go to s_sum, [token][sum_pitch].
-template <typename T, int MT, int NT>
+template <typename T, int MT, int NT, bool ANY>
 __device__ __forceinline__ void tile_shrink(const AdapterArgs& p, const T* a, int rank, int j0,
                                             const int32_t* tokens, int n_tokens, int k0, int k1,
                                             float* s_warp, float* s_sum, int sum_pitch) {
@@ -680,7 +720,7 @@ __device__ __forceinline__ void tile_shrink(const AdapterArgs& p, const T* a, in
     x[n] = static_cast<const T*>(p.x) + tokens[min(8 * n + g, n_tokens - 1)] * p.xs;
   const int2 mine = inner_share(k0, k1, warp, kWarps);
   float acc[MT][NT][4] = {};
-  shrink<T, MT, NT>(p, a, rank, j0, x, mine.x, mine.y, acc);
+  shrink<T, MT, NT, ANY>(p, a, rank, j0, x, mine.x, mine.y, acc);
   constexpr int kWide = 16 * MT + 1;
   float* out = s_warp + warp * 8 * NT * kWide;
 #pragma unroll
@@ -702,18 +742,18 @@ __device__ __forceinline__ void tile_shrink(const AdapterArgs& p, const T* a, in
 }
 
 // tile_shrink over a slot's rank, by blocks of 64.
-template <typename T, bool WIDE, int NT>
+template <typename T, bool WIDE, int NT, bool ANY>
 __device__ __forceinline__ void tile_shrink_all(const AdapterArgs& p, const T* a, int rank,
                                                 const int32_t* tokens, int n_tokens, int k0,
                                                 int k1, float* s_warp, float* s_sum, int pitch) {
   if (rank <= 16)
-    tile_shrink<T, 1, NT>(p, a, rank, 0, tokens, n_tokens, k0, k1, s_warp, s_sum, pitch);
+    tile_shrink<T, 1, NT, ANY>(p, a, rank, 0, tokens, n_tokens, k0, k1, s_warp, s_sum, pitch);
   else if (rank <= 32)
-    tile_shrink<T, 2, NT>(p, a, rank, 0, tokens, n_tokens, k0, k1, s_warp, s_sum, pitch);
+    tile_shrink<T, 2, NT, ANY>(p, a, rank, 0, tokens, n_tokens, k0, k1, s_warp, s_sum, pitch);
   if constexpr (WIDE)
     if (rank > 32)
       for (int j0 = 0; j0 < rank; j0 += 64)
-        tile_shrink<T, 4, NT>(p, a, rank, j0, tokens, n_tokens, k0, k1, s_warp, s_sum, pitch);
+        tile_shrink<T, 4, NT, ANY>(p, a, rank, j0, tokens, n_tokens, k0, k1, s_warp, s_sum, pitch);
 }
 
 // Columns of a token's sums: whole blocks of 16 MT, on other banks.
@@ -725,7 +765,7 @@ constexpr int warp_sums_of(int rank) {
   return kWarps * kTile * ((rank <= 16 ? 16 : rank <= 32 ? 32 : 64) + 1);
 }
 
-template <typename T, bool WIDE>  // WIDE: ranks above 32
+template <typename T, bool WIDE, bool ANY>  // WIDE: ranks above 32
 __global__ void __launch_bounds__(kThreads, 1) adapters_shrink(AdapterArgs p) {
   extern __shared__ float s_dyn_sum[];  // kTile x sum_pitch_of(p.rank), then the warps' sums
   pdl_launch_dependents();
@@ -745,11 +785,11 @@ __global__ void __launch_bounds__(kThreads, 1) adapters_shrink(AdapterArgs p) {
     if (rank == 0) continue;
     const T* a = static_cast<const T*>(p.a) + (int64_t)tile.x * p.rank * p.n_in;
     if (tile.z > 32)
-      tile_shrink_all<T, WIDE, 8>(p, a, rank, p.perm + tile.y, tile.z, k0, k1, s_warp, s_sum, pitch);
+      tile_shrink_all<T, WIDE, 8, ANY>(p, a, rank, p.perm + tile.y, tile.z, k0, k1, s_warp, s_sum, pitch);
     else if (tile.z > 8)
-      tile_shrink_all<T, WIDE, 4>(p, a, rank, p.perm + tile.y, tile.z, k0, k1, s_warp, s_sum, pitch);
+      tile_shrink_all<T, WIDE, 4, ANY>(p, a, rank, p.perm + tile.y, tile.z, k0, k1, s_warp, s_sum, pitch);
     else
-      tile_shrink_all<T, WIDE, 1>(p, a, rank, p.perm + tile.y, tile.z, k0, k1, s_warp, s_sum, pitch);
+      tile_shrink_all<T, WIDE, 1, ANY>(p, a, rank, p.perm + tile.y, tile.z, k0, k1, s_warp, s_sum, pitch);
     cluster.sync();
     // a warp per token: its h over the cluster's shares, as 16-bit terms
     const int nk = (rank + 31) / 32;
@@ -942,14 +982,16 @@ spmv_status run_few(AdapterArgs& p, cudaStream_t st) {
   const int groups = p.n_tokens < most ? p.n_tokens : most;
   int e;
   if (groups <= 9) {  // clusters of 16 while there are SMs for all of them
-    const void* fn = reinterpret_cast<const void*>(&adapters_few<T, YT, 16, 16>);
+    const void* fn = p.vec_in ? reinterpret_cast<const void*>(&adapters_few<T, YT, 16, 16, false>)
+                              : reinterpret_cast<const void*>(&adapters_few<T, YT, 16, 16, true>);
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
       return SPMV_ERR_CUDA;
     e = launch_cluster(fn, groups * 16, 512, 0, 16, false, st, args);
   } else {  // at most two waves of two CTAs per SM
+    const void* fn = p.vec_in ? reinterpret_cast<const void*>(&adapters_few<T, YT, 8, 8, false>)
+                              : reinterpret_cast<const void*>(&adapters_few<T, YT, 8, 8, true>);
     const int clusters = groups < 76 ? groups : 76;
-    e = launch_cluster(reinterpret_cast<const void*>(&adapters_few<T, YT, 8, 8>), clusters * 8,
-                       256, 0, 8, false, st, args);
+    e = launch_cluster(fn, clusters * 8, 256, 0, 8, false, st, args);
   }
   return e == 0 ? SPMV_OK : SPMV_ERR_CUDA;
 }
@@ -960,8 +1002,12 @@ spmv_status run_many(AdapterArgs& p, cudaStream_t st) {
   const size_t shrink_smem = ((size_t)kTile * sum_pitch_of(p.rank) + warp_sums_of(p.rank)) * 4;
   const size_t expand_smem = (size_t)kTile * pitch_of<T>(Terms<T>::n * p.term_pitch) * sizeof(T) +
                              (size_t)kBaseStages * kThreads * 8 * sizeof(Pack<YT, 4>);
-  const void* shrink_fn = p.rank > 32 ? reinterpret_cast<const void*>(&adapters_shrink<T, true>)
-                                      : reinterpret_cast<const void*>(&adapters_shrink<T, false>);
+  const bool wide = p.rank > 32;
+  const void* shrink_fn =
+      p.vec_in ? (wide ? reinterpret_cast<const void*>(&adapters_shrink<T, true, false>)
+                       : reinterpret_cast<const void*>(&adapters_shrink<T, false, false>))
+               : (wide ? reinterpret_cast<const void*>(&adapters_shrink<T, true, true>)
+                       : reinterpret_cast<const void*>(&adapters_shrink<T, false, true>));
   const void* expand_fn = reinterpret_cast<const void*>(&adapters_expand<T, YT>);
   if (!allow_smem(reinterpret_cast<const void*>(&adapters_sort), sort_smem) ||
       !allow_smem(shrink_fn, shrink_smem) || !allow_smem(expand_fn, expand_smem))

@@ -158,17 +158,6 @@ __device__ __forceinline__ void mma64(float (&c)[4], const Vec16& lo, const Vec1
         v.w[i + 1]);
 }
 
-// Ask L2 for `rows` rows of `bytes` bytes, at(i) the i-th, a warp per row:
-// memory is at work on all of them before the first load waits.
-template <typename F>
-__device__ __forceinline__ void prefetch_rows(int rows, int bytes, F&& at) {
-  for (int i = threadIdx.x >> 5; i < rows; i += blockDim.x >> 5) {
-    const char* row = reinterpret_cast<const char*>(at(i));
-    for (int k = 128 * (threadIdx.x & 31); k < bytes; k += 128 * 32)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(row + k));
-  }
-}
-
 // The first `left` of 8 elements, zeros in place of the others.
 __device__ __forceinline__ uint4 keep8(uint4 v, int left) {
   const auto word = [&](uint32_t w, int i) {
@@ -550,7 +539,9 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) adapters_few(AdapterAr
     const T* a = static_cast<const T*>(p.a) + (int64_t)slot * p.rank * p.n_in;
     const T* b = static_cast<const T*>(p.b) + (int64_t)slot * p.n_out * p.rank;
     __syncthreads();
-    prefetch_rows(rank, (k1 - k0) * (int)sizeof(T), [&](int i) { return a + (int64_t)i * p.n_in + k0; });
+    // (memory is at work on all of A's share before the first load waits)
+    for (int i = threadIdx.x; i < rank; i += 32 * WARPS)
+      prefetch_bulk(a + (int64_t)i * p.n_in + k0, (k1 - k0) * (int64_t)sizeof(T));
     const T* x = static_cast<const T*>(p.x) + s_token[min(lane >> 2, n_tokens - 1)] * p.xs;
     if (rank <= 16)
       few_shrink<T, 1, WARPS, ANY>(p, a, rank, 0, x, k0, k1, s_mem.warps, s_part);
@@ -561,14 +552,13 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) adapters_few(AdapterAr
         few_shrink<T, 4, WARPS, ANY>(p, a, rank, j0, x, k0, k1, s_mem.warps, s_part);
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     // (any earlier, B would take its share of the memory from A)
-    const char* share = reinterpret_cast<const char*>(b + (int64_t)o0 * p.rank);
-    for (int64_t i = 128ll * threadIdx.x; i < (int64_t)(o1 - o0) * p.rank * (int)sizeof(T);
-         i += 128ll * 32 * WARPS)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(share + i));
-    if (p.base)
-      prefetch_rows(n_tokens, (o1 - o0) * (int)sizeof(YT), [&](int i) {
-        return static_cast<const YT*>(p.base) + s_token[i] * p.bs + o0;
-      });
+    const int64_t share = (int64_t)(o1 - o0) * p.rank;
+    if (lane == 0)
+      prefetch_bulk(b + (int64_t)o0 * p.rank + share * warp / WARPS,
+                    (share * (warp + 1) / WARPS - share * warp / WARPS) * (int)sizeof(T));
+    if (p.base && (int)threadIdx.x < n_tokens)
+      prefetch_bulk(static_cast<const YT*>(p.base) + s_token[threadIdx.x] * p.bs + o0,
+                    (o1 - o0) * (int64_t)sizeof(YT));
     const int nk = (rank + 31) / 32;
     // a step's base and first 32 columns of B: two steps are under way at a time
     struct Step {

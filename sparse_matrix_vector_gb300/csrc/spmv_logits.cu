@@ -163,13 +163,11 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitPerSm) logits_rows(LogitA
   const int64_t jobs = (int64_t)p.n_requests * a.shares;
   const auto ask_logits = [&](int64_t i, int v0) {
     const int n = min(a.share, p.vocab - v0);
-    const char* at =
-        reinterpret_cast<const char*>(static_cast<const T*>(p.logits) + i * p.stride + v0);
-    for (int64_t k = 128ll * me; k < n * (int64_t)sizeof(T); k += 128 * kLogitThreads)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(at + k));
+    if (me == 0)
+      prefetch_bulk(static_cast<const T*>(p.logits) + i * p.stride + v0, n * (int64_t)sizeof(T));
   };
   const auto ask_list = [&](const int32_t* list, int64_t lo, int64_t hi) {
-    if (lo + 32 * me < hi) asm volatile("prefetch.global.L2 [%0];" ::"l"(list + lo + 32 * me));
+    if (me == 32) prefetch_bulk(list + lo, min(hi - lo, (int64_t)1 << 16) * 4);
   };
   const auto bits_of = [&](int k) { return s_word[k >> 1] >> (16 * (k & 1)) & 0xffffu; };
   int64_t i = blockIdx.x / (unsigned)a.shares;

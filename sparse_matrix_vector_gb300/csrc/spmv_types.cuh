@@ -107,6 +107,18 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
+// Ask L2 for the whole 16-byte granules of [p, p + bytes), by one thread: one
+// request to the copy engine. (The same by prefetches of single lines takes
+// the load/store units a cycle or more per line, which the loads behind them
+// wait for.)
+__device__ __forceinline__ void prefetch_bulk(const void* p, int64_t bytes) {
+  const uintptr_t lo = (reinterpret_cast<uintptr_t>(p) + 15) & ~uintptr_t(15);
+  const uintptr_t hi = (reinterpret_cast<uintptr_t>(p) + (uintptr_t)bytes) & ~uintptr_t(15);
+  if (bytes > 0 && hi > lo)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(lo), "r"((uint32_t)(hi - lo))
+                 : "memory");
+}
+
 // ------------------------------------------------- a thread's columns of a row
 // A group of `group` threads shares a row of n columns, thread `me` holding
 // NV vectors of VEC (even) columns. ALIGNED: rows start on vector boundaries
@@ -185,8 +197,7 @@ struct Cols {
   // Ask L2 for a row (its loads come one row later).
   template <typename T>
   __device__ __forceinline__ void prefetch(const T* row) const {
-    for (int c = me * (int)(128 / sizeof(T)); c < n; c += group * (int)(128 / sizeof(T)))
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
+    if (me == 0) prefetch_bulk(row, (int64_t)n * (int)sizeof(T));
   }
 };
 

@@ -463,10 +463,20 @@ layernorm_backward_fused(BackwardArgs<XT, YT> p) {
         if (cols.has(i)) {
 #pragma unroll
           for (int k = 0; k < VEC / 2; ++k) {
-            float2* pw = reinterpret_cast<float2*>(s_dw + cols.col(i, 2 * k));
-            float2* pb = reinterpret_cast<float2*>(s_db + cols.col(i, 2 * k));
-            *pw = t ? __fadd2_rn(*pw, dw[i][k]) : dw[i][k];
-            *pb = t ? __fadd2_rn(*pb, db[i][k]) : db[i][k];
+            if constexpr (kAligned) {
+              float2* pw = reinterpret_cast<float2*>(s_dw + cols.col(i, 2 * k));
+              float2* pb = reinterpret_cast<float2*>(s_db + cols.col(i, 2 * k));
+              *pw = t ? __fadd2_rn(*pw, dw[i][k]) : dw[i][k];
+              *pb = t ? __fadd2_rn(*pb, db[i][k]) : db[i][k];
+            } else {
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (cols.has(i, 2 * k + e)) {
+                  const int c = cols.col(i, 2 * k + e);
+                  s_dw[c] = (t ? s_dw[c] : 0.f) + (e ? dw[i][k].y : dw[i][k].x);
+                  s_db[c] = (t ? s_db[c] : 0.f) + (e ? db[i][k].y : db[i][k].x);
+                }
+            }
           }
         }
     }
@@ -488,6 +498,28 @@ layernorm_backward_fused(BackwardArgs<XT, YT> p) {
   }
 }
 
+// f(column, x, dy) for this thread's columns of a row, kFew loads of each
+// under way at a time. (Loads past the end repeat the last column; their
+// values are not used.)
+constexpr int kFew = 8;
+
+template <typename XT, typename YT, typename F>
+__device__ __forceinline__ void for_row(const XT* x, const YT* dy, int n, F&& f) {
+  for (int64_t j0 = threadIdx.x; j0 < n; j0 += kFew * kThreads) {
+    XT xv[kFew];
+    YT dv[kFew];
+#pragma unroll
+    for (int k = 0; k < kFew; ++k) {
+      const int64_t j = min(j0 + k * kThreads, (int64_t)n - 1);
+      xv[k] = x[j];
+      dv[k] = dy[j];
+    }
+#pragma unroll
+    for (int k = 0; k < kFew; ++k)
+      if (j0 + k * kThreads < n) f((int)(j0 + k * kThreads), to_f32(xv[k]), to_f32(dv[k]));
+  }
+}
+
 // Backward, rows too long for registers: dx, one row per CTA step.
 template <typename XT, typename YT>
 __global__ void __launch_bounds__(kThreads) layernorm_dx_rows(BackwardArgs<XT, YT> p) {
@@ -498,21 +530,20 @@ __global__ void __launch_bounds__(kThreads) layernorm_dx_rows(BackwardArgs<XT, Y
     const YT* dy = p.dy + r * p.dys;
     const XT* x = p.x + r * p.xs;
     float sg = 0.f, sgx = 0.f;
-    for (int j = threadIdx.x; j < p.n_cols; j += kThreads) {
-      const float g = to_f32(dy[j]) * (p.w ? load_as_f32(p.w, p.pt, j) : 1.f);
+    for_row(x, dy, p.n_cols, [&](int j, float v, float d) {
+      const float g = d * (p.w ? load_as_f32(p.w, p.pt, j) : 1.f);
       sg += g;
-      sgx += g * ((to_f32(x[j]) - m) * rs);
-    }
+      sgx += g * ((v - m) * rs);
+    });
     float sums[2] = {sg, sgx};
     cta_sums_all<2>(sums, s_red[turn]);
     turn ^= 1;
     sg = sums[0] / (float)p.n_cols;
     sgx = sums[1] / (float)p.n_cols;
-    for (int j = threadIdx.x; j < p.n_cols; j += kThreads) {
-      const float g = to_f32(dy[j]) * (p.w ? load_as_f32(p.w, p.pt, j) : 1.f);
-      const float xh = (to_f32(x[j]) - m) * rs;
-      p.dx[r * p.dxs + j] = from_f32<XT>(rs * (g - sg - xh * sgx));
-    }
+    for_row(x, dy, p.n_cols, [&](int j, float v, float d) {
+      const float g = d * (p.w ? load_as_f32(p.w, p.pt, j) : 1.f);
+      p.dx[r * p.dxs + j] = from_f32<XT>(rs * (g - sg - (v - m) * rs * sgx));
+    });
   }
 }
 
@@ -527,6 +558,7 @@ __global__ void __launch_bounds__(kThreads) layernorm_params_part(BackwardArgs<X
   const int64_t per = (p.n_rows + kLongParts - 1) / kLongParts;
   const int64_t lo = blockIdx.y * per, hi = lo + per < p.n_rows ? lo + per : p.n_rows;
   float dw = 0.f, db = 0.f;
+#pragma unroll 8
   for (int64_t r = lo; r < hi; ++r) {
     const float d = to_f32(p.dy[r * p.dys + j]);
     dw += d * ((to_f32(p.x[r * p.xs + j]) - p.mean[r]) * p.rstd[r]);
@@ -566,6 +598,8 @@ layernorm_params_sum(int n_cols, int parts, const float* part, void* dw_out, voi
 }
 
 constexpr int kSms = 152;
+constexpr size_t kSmemPerSm = 228 * 1024;
+constexpr size_t kSmemStatic = 10 * 1024;  // of a backward CTA, with what the system reserves
 
 // How the rows of a call are cut: a warp per row or a CTA per row, columns
 // per thread (0: rows too long for registers), threads, CTAs.
@@ -574,29 +608,43 @@ struct RowShape {
   int cols, threads, grid;
 };
 
-RowShape row_shape(int64_t n_rows, int n_cols, bool aligned, bool forward) {
+// xs, ys: bytes of an element of x and of y (or dy).
+RowShape row_shape(int64_t n_rows, int n_cols, size_t xs, size_t ys, bool aligned, bool forward) {
   RowShape s{};
   int per_sm = 0;  // CTAs that an SM's registers hold
   int64_t groups = n_rows;
-  if (aligned && n_cols <= 512) {
+  if (n_cols <= 512) {
     s.warp = true;
     s.cols = n_cols <= 256 ? 8 : 16;
     s.threads = kThreads;
-    per_sm = s.cols == 8 ? 3 : 2;
+    per_sm = (s.cols == 8 ? 3 : 2) + (forward && (aligned || s.cols == 8) ? 1 : 0);
     groups = (n_rows + kWarps - 1) / kWarps;
   } else {
-    if (aligned)
-      s.cols = n_cols <= 2048 ? 8 : n_cols <= 16 * 768 ? 16 : n_cols <= 32 * 512 ? 32 : 0;
-    else
-      s.cols = n_cols <= (forward ? 2048 : 8 * 640) ? 8
-               : n_cols <= 16 * 512                 ? 16
-               : n_cols <= 24 * 512                 ? 24
-                                                    : 0;
+    int most;  // threads per SM
+    if (!aligned) {
+      s.cols = !forward && n_cols > 16 * 256 && n_cols <= 8 * 640 ? 8
+               : n_cols <= 16 * 512                                ? 16
+               : n_cols <= 24 * 512                                ? 24
+                                                                   : 0;
+      most = s.cols != 24 && (forward || s.cols == 8) ? 1024 : 512;
+    } else if (forward) {
+      s.cols = n_cols < 2048 || xs == 4 ? 16 : n_cols <= 32 * 256 ? 32 : 16;
+      if (n_cols > 16 * 768) s.cols = n_cols <= 32 * 512 ? 32 : 0;
+      most = s.cols == 32 ? 512 : 768;
+    } else {
+      const bool two = n_cols <= 32 * 256 &&  // CTAs of 32 columns per thread
+                       2 * (size_t)n_cols * (xs + ys) <= kSmemPerSm / 2 - kSmemStatic;
+      s.cols = n_cols <= 2048       ? 8
+               : n_cols <= 16 * 384 ? 16
+               : two                ? 32
+               : n_cols <= 16 * 768 ? 16
+               : n_cols <= 32 * 512 ? 32
+                                    : 0;
+      most = s.cols == 32 ? 512 : s.cols == 8 && xs == 4 ? 640 : 768;
+    }
     if (!s.cols) return s;
     s.threads = ((n_cols + s.cols - 1) / s.cols + 31) / 32 * 32;
-    const int most = (!aligned ? (s.cols == 24 ? 512 : forward || s.cols == 8 ? 1024 : 512)
-                               : s.cols == 8 ? 1024 : s.cols == 16 ? 800 : 512) / s.threads;
-    per_sm = most < 1 ? 1 : most > 8 ? 8 : most;
+    per_sm = most / s.threads < 1 ? 1 : most / s.threads;
   }
   s.grid = (int)(groups < (int64_t)per_sm * kSms ? groups : (int64_t)per_sm * kSms);
   return s;
@@ -607,22 +655,22 @@ RowShape row_shape(int64_t n_rows, int n_cols, bool aligned, bool forward) {
 // second time from L2, but there is one launch and no workspace. (512 x 4096
 // fp32 x: 12.6 us by columns, 14.2 by rows.)
 bool by_columns(int64_t n_rows, int n_cols) {
-  return n_rows <= 1024 && n_rows * n_cols <= (3 << 20) && n_cols <= 16 * 512;
+  return n_rows <= 1024 && n_rows * n_cols <= (9 << 18) && n_cols <= 16 * 512;
 }
 
 constexpr int kMaxCols = INT32_MAX - 4096;
 constexpr int kRowGrid = kSms * 8;
-constexpr size_t kSmemPerSm = 228 * 1024;
-constexpr size_t kSmemStatic = 10 * 1024;  // of a backward CTA, with what the system reserves
 
 // Partial sums of dweight and dbias, at most (whichever kernel runs).
 int64_t backward_workspace(int64_t n_rows, int n_cols, bool want_params) {
   if (!want_params || n_rows == 0 || by_columns(n_rows, n_cols)) return 0;
   int64_t parts = kLongParts;
-  for (const bool aligned : {false, true}) {
-    const RowShape s = row_shape(n_rows, n_cols, aligned, false);
-    if (s.cols && s.grid > parts) parts = s.grid;
-  }
+  for (const bool aligned : {false, true})
+    for (const int xs : {2, 4})
+      for (const int ys : {2, 4}) {
+        const RowShape s = row_shape(n_rows, n_cols, xs, ys, aligned, false);
+        if (s.cols && s.grid > parts) parts = s.grid;
+      }
   return parts * 2 * n_cols * 4;
 }
 
@@ -655,24 +703,28 @@ spmv_status launch_rows(void (*fn)(Args), const RowShape& s, size_t smem, const 
 template <typename XT, typename YT, int CPT, bool WARP, bool ALIGNED>
 spmv_status forward_launch(const RowShape& s, const ForwardArgs<XT, YT>& p, cudaStream_t st) {
   constexpr int kVec = 16 / (int)sizeof(XT);
-  // four stages of fp32 are at most 192 KB of an SM's shared memory (three of
-  // rows with 32 columns per thread)
-  constexpr int kStages = !ALIGNED ? 0 : CPT == 32 ? 3 : 4;
-  const size_t smem = ALIGNED ? (size_t)kStages * s.threads * CPT * sizeof(XT)
-                              : (size_t)s.threads * CPT * 8;  // weight and bias
-  return launch_rows(layernorm_fused<XT, YT, kVec, CPT, kStages, WARP>, s, smem, p, st);
+  const size_t vectors = (size_t)s.threads * CPT;
+  if constexpr (!ALIGNED) {  // weight and bias
+    return launch_rows(layernorm_fused<XT, YT, kVec, CPT, 0, WARP>, s, vectors * 8, p, st);
+  } else {
+    if constexpr (CPT == 16 && !WARP)
+      if (2 * s.threads <= most_threads(16, true))
+        return launch_rows(layernorm_fused<XT, YT, kVec, 16, 2, false>, s,
+                           2 * vectors * sizeof(XT), p, st);
+    constexpr int kStages = WARP ? 4 : 3;
+    return launch_rows(layernorm_fused<XT, YT, kVec, CPT, kStages, WARP>, s,
+                       kStages * vectors * sizeof(XT), p, st);
+  }
 }
 
 template <typename XT, typename YT, bool ALIGNED>
 spmv_status forward(const ForwardArgs<XT, YT>& p, cudaStream_t st) {
-  RowShape s = row_shape(p.n_rows, p.n_cols, ALIGNED, true);
-  if constexpr (ALIGNED) {
+  RowShape s = row_shape(p.n_rows, p.n_cols, sizeof(XT), sizeof(YT), ALIGNED, true);
+  if (s.warp)
+    return s.cols == 8 ? forward_launch<XT, YT, 8, true, ALIGNED>(s, p, st)
+                       : forward_launch<XT, YT, 16, true, ALIGNED>(s, p, st);
+  if constexpr (ALIGNED)
     if (s.cols == 32) return forward_launch<XT, YT, 32, false, true>(s, p, st);
-    if (s.warp)
-      return s.cols == 8 ? forward_launch<XT, YT, 8, true, true>(s, p, st)
-                         : forward_launch<XT, YT, 16, true, true>(s, p, st);
-  }
-  if (s.cols == 8) return forward_launch<XT, YT, 8, false, ALIGNED>(s, p, st);
   if (s.cols == 16) return forward_launch<XT, YT, 16, false, ALIGNED>(s, p, st);
   if constexpr (!ALIGNED)
     if (s.cols == 24) return forward_launch<XT, YT, 24, false, false>(s, p, st);
@@ -711,7 +763,7 @@ spmv_status backward_launch(const RowShape& s, const BackwardArgs<XT, YT>& p, cu
 
 template <typename XT, typename YT, bool ALIGNED>
 spmv_status backward(BackwardArgs<XT, YT> p, void* dweight, void* dbias, cudaStream_t st) {
-  RowShape s = row_shape(p.n_rows, p.n_cols, ALIGNED, false);
+  RowShape s = row_shape(p.n_rows, p.n_cols, sizeof(XT), sizeof(YT), ALIGNED, false);
   const bool columns = (dweight || dbias) && by_columns(p.n_rows, p.n_cols);
   // two sets of 32 columns' rows in fp32 do not fit shared memory
   if (s.cols == 32 && ALIGNED &&
@@ -724,6 +776,8 @@ spmv_status backward(BackwardArgs<XT, YT> p, void* dweight, void* dbias, cudaStr
       s.warp = false;
       s.cols = 8;
       s.threads = ((p.n_cols + 7) / 8 + 31) / 32 * 32;
+    } else if (s.cols == 32) {
+      s.cols = 16;
     }
     if (s.threads < 512) s.threads = 512;
     const int64_t most = s.cols == 8 ? 2 * kSms : kSms;
@@ -742,9 +796,8 @@ spmv_status backward(BackwardArgs<XT, YT> p, void* dweight, void* dbias, cudaStr
   int parts = s.grid;
   spmv_status status = SPMV_OK;
   if (s.warp) {
-    if constexpr (ALIGNED)
-      status = s.cols == 8 ? backward_launch<XT, YT, 8, true, true>(s, p, st)
-                           : backward_launch<XT, YT, 16, true, true>(s, p, st);
+    status = s.cols == 8 ? backward_launch<XT, YT, 8, true, ALIGNED>(s, p, st)
+                         : backward_launch<XT, YT, 16, true, ALIGNED>(s, p, st);
   } else if (s.cols == 8) {
     status = backward_launch<XT, YT, 8, false, ALIGNED>(s, p, st);
   } else if (s.cols == 16) {

@@ -552,7 +552,8 @@ spmv_status spmv_layernorm(int64_t n_rows, int32_t n_cols, const void* x, spmv_d
                            int64_t y_stride, float* mean_out, float* rstd_out, void* stream);
 
 /* Bytes of workspace that spmv_layernorm_backward needs for these sizes (0
- * for sizes it refuses, and where neither dweight nor dbias is wanted). */
+ * for sizes it refuses, where neither dweight nor dbias is wanted, and for
+ * calls small enough to need none). */
 int64_t spmv_layernorm_backward_workspace(int64_t n_rows, int32_t n_cols, int32_t want_params);
 
 /* Gradient of spmv_layernorm. With xhat = (x - mean) * rstd and

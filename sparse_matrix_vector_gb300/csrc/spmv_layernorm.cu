@@ -1,5 +1,24 @@
 // Layer norm of rows and its gradient (spmv_layernorm,
 // spmv_layernorm_backward).
+//
+//   mean = sum x / n, rstd = 1 / sqrt(sum (x - mean)^2 / n + eps)
+//   y = (x - mean) rstd w + b
+//   g = dy w, c = x - mean:
+//   dx = rstd g - rstd mean(g) - c rstd^3 mean(g c)
+//   dw = sum over rows of dy c rstd, db = sum over rows of dy
+//
+// Both are bound by moving the rows: some ten operations per element, each
+// read once and written once. All arithmetic is fp32; a value is rounded once,
+// to the type of the tensor it goes to. Measured, in us, and as a share of the
+// 6.79 TB/s of a plain copy:
+//   norm      8192 x 12288 fp32 -> fp16  89 (1.00)   16384 x 4096  62 (0.96)
+//             8192 x 12288 bf16          74 (0.80)   16384 x 4096  45 (0.87)
+//   gradient  8192 x 12288 fp32, fp16   166 (0.89)   16384 x 4096 106 (0.93)
+//             8192 x 12288 bf16         120 (0.74)   16384 x 4096  81 (0.73)
+// In 16 bits the gradient is bound by its instructions, some 14 per element
+// (unpacking x and dy twice, once for the sums and once for dx).
+// Unaligned rows move element by element: 8192 x 5003 bf16 64 us (0.38), its
+// gradient 94 (0.39); 1023 x 5003 12.4 us, of which a launch is 4.3.
 #include <climits>
 #include <type_traits>
 
@@ -602,7 +621,25 @@ constexpr size_t kSmemPerSm = 228 * 1024;
 constexpr size_t kSmemStatic = 10 * 1024;  // of a backward CTA, with what the system reserves
 
 // How the rows of a call are cut: a warp per row or a CTA per row, columns
-// per thread (0: rows too long for registers), threads, CTAs.
+// per thread (0: rows too long for registers), threads, CTAs. In us, with the
+// other choice measured beside it:
+// - A warp takes rows of up to 512 columns, without barriers: 65536 x 256 fp16
+//   18 (CTAs: 35), gradient 28 (36); unaligned 65536 x 301 bf16 39 (64).
+// - Longer rows take the columns per thread with which an SM holds two CTAs at
+//   least: one works while the other waits for its sums. Norm in 16 bits, 32
+//   columns up to 8192: 16384 x 8192 bf16 86 (16 columns: 113), x 4096 45 (50);
+//   below 2048 they leave too few warps. Of fp32 the ring of 32 columns is too
+//   large to gain: 16384 x 8192 134 (16 columns: 128). Gradient, 8 columns up
+//   to 2048: 32768 x 1024 bf16 45 (16: 53); 32 columns from 6144 to 8192:
+//   16384 x 8192 bf16 149 (16: 177).
+// - Above that one CTA fills an SM: 16 columns, whose threads need fewer
+//   registers, while they reach: gradient of 8192 x 12288 bf16 120 (32: 137).
+// - The registers would hold more threads of 8 fp32 columns, but then the
+//   rings' requests get in each other's way: gradient of 32768 x 1024 fp32 60
+//   (1024 threads per SM: 72).
+// - Unaligned rows, whose loads go to registers: 16 columns, gradient of
+//   16384 x 4001 bf16 115 (8: 159), but 8 where 16 leave one CTA per SM: 8192 x
+//   5003 92 (16: 100).
 struct RowShape {
   bool warp;
   int cols, threads, grid;
@@ -652,8 +689,10 @@ RowShape row_shape(int64_t n_rows, int n_cols, size_t xs, size_t ys, bool aligne
 
 // Whether dweight and dbias are summed by columns in the launch that makes dx,
 // rather than from partial sums of its rows: x and dy are read twice, the
-// second time from L2, but there is one launch and no workspace. (512 x 4096
-// fp32 x: 12.6 us by columns, 14.2 by rows.)
+// second time from L2, but there is one launch and no workspace. In us, by
+// columns against by rows, fp32 x: 64 x 2048 4.3 / 6.3, 512 x 4096 12.7 /
+// 13.7, 1024 x 2048 14.4 / 14.5; beyond these bounds 300 x 8192 16.4 / 13.8,
+// 2048 x 1024 18.4 / 15.0.
 bool by_columns(int64_t n_rows, int n_cols) {
   return n_rows <= 1024 && n_rows * n_cols <= (9 << 18) && n_cols <= 16 * 512;
 }
@@ -707,6 +746,9 @@ spmv_status forward_launch(const RowShape& s, const ForwardArgs<XT, YT>& p, cuda
   if constexpr (!ALIGNED) {  // weight and bias
     return launch_rows(layernorm_fused<XT, YT, kVec, CPT, 0, WARP>, s, vectors * 8, p, st);
   } else {
+    // Two rows on their way where two CTAs share an SM, three where there is
+    // one (16384 rows of fp32, 4096 columns: 62 us with two, 65 with three;
+    // 8192: 137 with two, 128 with three).
     if constexpr (CPT == 16 && !WARP)
       if (2 * s.threads <= most_threads(16, true))
         return launch_rows(layernorm_fused<XT, YT, kVec, 16, 2, false>, s,
@@ -741,9 +783,10 @@ spmv_status backward_launch(const RowShape& s, const BackwardArgs<XT, YT>& p, cu
     return launch_rows(layernorm_backward_fused<XT, YT, kVec, CPT, 0, 1, WARP>, s,
                        (size_t)s.threads * CPT * 4, p, st, columns);
   } else {
-    // Two rows at a time halve the barriers (a warp's rows need none); where
-    // two sets of them do not fit, single rows. (A warp group's ring is larger than the two sums per
-    // column that the warps leave in its place at the end.)
+    // Two rows at a time halve the barriers (a warp's rows need none; 8192 x
+    // 12288 bf16: 120 us, single rows 131); where two sets of them do not fit,
+    // single rows. (A warp group's ring is larger than the two sums per column
+    // that the warps leave in its place at the end.)
     const size_t row = (size_t)s.threads * CPT * (sizeof(XT) + sizeof(YT));
     const size_t room =
         kSmemPerSm / (size_t)((s.grid + columns + kSms - 1) / kSms) - kSmemStatic;

@@ -151,9 +151,10 @@ __device__ __forceinline__ void for_entries(const int32_t* list, int64_t lo, int
 }
 
 // CTAs take (request, share of the vocabulary) pairs in turn; the next one's
-// parameters come into registers early. (Asking L2 for its lists and logits as
-// well changes nothing: 256 x 128000 fp32 76 us with, 75 without.) A token's
-// bits of the table are cleared as it is put in place.
+// parameters come into registers early and, where logits are loaded element by
+// element, its logits into L2 (256 x 50257 fp32: 41 us, 47 without; whole
+// vectors have enough under way themselves: 256 x 128000 75 us without, 76
+// with). A token's bits of the table are cleared as it is put in place.
 template <typename T, typename OT, int VEC>
 __global__ void __launch_bounds__(kLogitThreads, kLogitPerSm) logits_rows(LogitArgs a) {
   extern __shared__ __align__(16) uint32_t s_word[];  // a.share / 2 words, two tokens each
@@ -168,11 +169,17 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitPerSm) logits_rows(LogitA
   const spmv_logits& p = a.l;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, me = threadIdx.x;
   const int64_t jobs = (int64_t)p.n_requests * a.shares;
+  const auto ask_logits = [&](int64_t i, int v0) {
+    if (VEC == 1 && me == 0)
+      prefetch_bulk(static_cast<const T*>(p.logits) + i * p.stride + v0,
+                    min(a.share, p.vocab - v0) * (int64_t)sizeof(T));
+  };
   const auto bits_of = [&](int k) { return s_word[k >> 1] >> (16 * (k & 1)) & 0xffffu; };
   int64_t i = blockIdx.x / (unsigned)a.shares;
   int v0 = (int)(blockIdx.x % (unsigned)a.shares) * a.share;
   const int64_t step_i = gridDim.x / (unsigned)a.shares;
   const int step_v = (int)(gridDim.x % (unsigned)a.shares) * a.share, wrap = a.shares * a.share;
+  ask_logits(i, v0);
   Request next;
   next.load(p, i);
   const auto clear_table = [&] {
@@ -192,7 +199,8 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitPerSm) logits_rows(LogitA
     int64_t next_i = i + step_i;
     int next_v = v0 + step_v;
     if (next_v >= wrap) next_v -= wrap, ++next_i;
-    if (id + gridDim.x < jobs) next.load(p, next_i);
+    const bool more = id + gridDim.x < jobs;
+    if (more) next.load(p, next_i);
     const uint32_t* mask = q.mask_row >= 0 ? p.mask + q.mask_row * p.mask_stride + v0 / 32 : nullptr;
 
     // count the lists; who first meets a token puts it on the list of met ones
@@ -209,6 +217,7 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitPerSm) logits_rows(LogitA
     };
     for_entries(p.prompt_tokens, q.p0, q.p1, v0, n, s_queue[warp], &s_n, s_met, seen);
     for_entries(p.output_tokens, q.o0, q.o1, v0, n, s_queue[warp], &s_n, s_met, told);
+    if (more) ask_logits(next_i, next_v);
     // biases of this CTA's tokens, compacted in list order
     int listed = 0;
     for (int64_t k = q.b0; k < q.b1; k += kLogitThreads) {

@@ -615,6 +615,20 @@ def test_logits_layouts(spmv_lib, types, layouts):
                  **everything(g, 3, 1000, 90, 20))
 
 
+@pytest.mark.parametrize("types", LOGIT_TYPES, ids=lambda p: "-".join(p))
+@pytest.mark.parametrize("size", [(9, 3, 6, 2), (9, 13, 20, 3), (9, 45, 40, 9), (9, 1003, 90, 20), (5, 16387, 9000, 30)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("layouts", [((1, 0), (1, 0)), ((3, 5), (3, 5)), ((6, 2), (6, 10)), ((2, 3), (10, 11)), ((7, 1), (3, 4)), ((5, 0), (5, 1))],
+                         ids=str)
+def test_logits_row_boundaries(spmv_lib, types, size, layouts):
+    """Rows that start anywhere: vectors from the first boundary that x and
+    out share, if they share one. (layouts: elements between rows, offset)"""
+    n, v, history, biases = size
+    g = gen(57 + v)
+    check_logits(randn(g, n, v, dtype=types[0], std=3.0), types[1], *[(v + more, offset) for more, offset in layouts],
+                 **everything(g, n, v, history, biases))
+
+
 def test_logits_masks_and_special_values(spmv_lib):
     """A mask that leaves nothing; infinities, NaN and the type's lowest
     value in allowed and in masked places; a bias of -inf."""

@@ -267,6 +267,20 @@ def test_gradient(spmv_lib, shape, types):
     check_grad(dy, x, w, param if w is not None else "f32")
 
 
+@pytest.mark.parametrize("types", PAIRS, ids=lambda p: "-".join(p))
+@pytest.mark.parametrize("shape", [
+    # narrow unaligned rows; widths on both sides of each change of the columns per thread
+    (1027, 1), (1500, 31), (3000, 101), (1300, 255), (1300, 257), (1100, 511), (1030, 513), (1100, 2056), (1030, 4101),
+    (500, 6144), (400, 6160), (330, 8192), (310, 8200)], ids=lambda s: f"{s[0]}x{s[1]}")
+def test_norm_and_gradient_at_every_shape(spmv_lib, shape, types):
+    n, d = shape
+    g = gen(n * 5 + d)
+    x = randn(g, n, d, dtype=types[0], std=1.5, mean=0.25)
+    w = randn(g, d, mean=1.0, std=0.3)
+    check_norm(x, w, randn(g, d), types[1])
+    check_grad(randn(g, n, d, dtype=types[1], std=0.5), x, w)
+
+
 @pytest.mark.parametrize("want", ["x", "w", "b", "wb", "xw", "xb", ""])
 def test_gradient_parts(spmv_lib, want):
     g = gen(21)

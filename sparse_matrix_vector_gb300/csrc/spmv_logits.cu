@@ -246,6 +246,10 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitPerSm) logits_rows(LogitA
     }
     __syncthreads();
     const int met = s_n;
+    // A pair without met tokens has no further barrier, and a warp that is done
+    // with its part of the pass would raise s_n for the next pair: not before
+    // every warp has read it.
+    if (met == 0) __syncthreads();
     const bool kept = met <= kMet;  // on the list, all of them
     // a met token's result
     const auto result = [&](int k, uint32_t w, int64_t count) {

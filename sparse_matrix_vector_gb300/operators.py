@@ -7,7 +7,8 @@ Only argument marshalling lives here. Tensors are CUDA tensors of one device,
 which is the current one; matrices have contiguous columns and any row
 stride. Calls run on ``stream`` (default: the current torch stream) and do
 not synchronize. A workspace that the caller does not give comes from torch's
-caching allocator; the default stream's is kept for its next call.
+caching allocator, from the pool of the stream that the call runs on; the
+default stream's is kept for its next call.
 """
 from __future__ import annotations
 
@@ -93,13 +94,25 @@ def _same_device(first, *others) -> int:
 def _on(stream, dev: int) -> int:
     if stream is None:
         return _raw_stream(dev)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    return 0 if handle == 1 else handle  # (two names of the default stream)
 
 
-def _workspace(given, n_bytes: int, stream, handle: int, dev: int):
+def _empty_on(handle: int, n_bytes: int, dev: int):
+    """Memory of the pool of the stream that will use it. (A block of another
+    stream's pool may still be in use by work queued there before it was
+    freed, and be given away there while this stream is at work on it.)"""
+    if handle == _raw_stream(dev):
+        return torch.empty(n_bytes, dtype=torch.uint8, device=dev)
+    stream = (torch.cuda.default_stream(dev) if handle == 0
+              else torch.cuda.ExternalStream(handle, device=dev))
+    with torch.cuda.stream(stream):
+        return torch.empty(n_bytes, dtype=torch.uint8, device=dev)
+
+
+def _workspace(given, n_bytes: int, handle: int, dev: int):
     """(address, bytes, owner) of a workspace; one that the caller does not
-    give is safe to drop as soon as the call returns, on whatever stream it
-    ran."""
+    give is safe to drop as soon as the call returns."""
     if given is not None:
         if given.data_ptr() % 16 or not given.is_contiguous():
             raise ValueError("workspace must be contiguous and 16-byte aligned")
@@ -113,11 +126,9 @@ def _workspace(given, n_bytes: int, stream, handle: int, dev: int):
             kept = _kept.by_device = {}
         ws = kept.get(dev)
         if ws is None or ws.numel() < n_bytes:
-            ws = kept[dev] = torch.empty(n_bytes, dtype=torch.uint8, device=dev)
-        return ws.data_ptr(), n_bytes, ws
-    ws = torch.empty(n_bytes, dtype=torch.uint8, device=dev)
-    if stream is not None and handle != _raw_stream(dev):
-        ws.record_stream(torch.cuda.ExternalStream(handle, device=dev))
+            ws = kept[dev] = _empty_on(0, n_bytes, dev)
+    else:
+        ws = _empty_on(handle, n_bytes, dev)
     return ws.data_ptr(), n_bytes, ws
 
 
@@ -182,7 +193,7 @@ def spmv_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, works
     handle = _on(stream, dev)
     lib = _lib_handle()
     need = lib.spmv_layernorm_backward_workspace(n, d, 1 if dw or db else 0)
-    wp, wn, _owner = _workspace(workspace, need, stream, handle, dev)
+    wp, wn, _owner = _workspace(workspace, need, handle, dev)
     _check(lib.spmv_layernorm_backward(
         n, d, dy.data_ptr(), _dtype(dy, "dy"), dys, x.data_ptr(), code, xs, w, p,
         _vector(mean, n, _F32, "mean"), _vector(rstd, n, _F32, "rstd"),
@@ -227,8 +238,7 @@ def spmv_adapters_run(x, a, b, slot_ids, y, base=None, ranks=None, scales=None, 
     dev = _same_device(x, y, a, b, slot_ids, base, ranks, scales, workspace)
     handle = _on(stream, dev)
     lib = _lib_handle()
-    wp, wn, _owner = _workspace(workspace, lib.spmv_adapters_workspace(t, slots, rank), stream,
-                                handle, dev)
+    wp, wn, _owner = _workspace(workspace, lib.spmv_adapters_workspace(t, slots, rank), handle, dev)
     _check(lib.spmv_adapters_run(
         t, n_in, n_out, slots, rank, _dtype(x, "x"), x.data_ptr(), xs, a.data_ptr(),
         b.data_ptr(), _vector(slot_ids, t, _I32, "slot_ids"),

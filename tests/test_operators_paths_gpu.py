@@ -1,6 +1,8 @@
 """GPU tests of the operators around a pruned layer, beside those in
 test_operators_gpu.py (whose references and tolerances they use): paths that
 only larger calls, other streams, several threads or unusual arguments reach."""
+import threading
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -40,3 +42,87 @@ def test_logits_requests_with_and_without_lists_in_turn(spmv_lib, v, types):
         S.spmv_logits_process(xd, out, **dev)
         first = out if first is None else first
         assert torch.equal(out, first)
+
+
+# ---------------------------------------------------------------- streams
+
+class Gradient:
+    """A gradient call that needs a workspace, and what it should give."""
+
+    def __init__(self, g, n, d):
+        self.x, self.dy, self.w = (randn(g, *size).to(DEV) for size in ((n, d), (n, d), (d,)))
+        self.m, self.r = self.x.mean(1), torch.rand(n, generator=g).to(DEV) + 0.5
+        self.need = S.spmv_layernorm_backward_workspace(n, d)
+        assert self.need > 0
+        self.ref = self.run()
+
+    def outputs(self):
+        return [torch.empty_like(t) for t in (self.x, self.w, self.w)]
+
+    def run(self, out=None, stream=None):
+        out = self.outputs() if out is None else out
+        S.spmv_layernorm_backward(self.dy, self.x, self.w, self.m, self.r, *out, stream=stream)
+        return out
+
+    def check(self, out):
+        assert all(torch.equal(a, b) for a, b in zip(out, self.ref))
+
+
+def busy(times=20):
+    """Work that keeps the current stream busy for some milliseconds."""
+    a = torch.ones(8192, 8192, device=DEV)
+    for _ in range(times):
+        a = (a @ a) * 0.0 + 1.0
+    return a
+
+
+@pytest.mark.parametrize("as_int", [False, True])
+def test_a_given_stream_leaves_the_current_streams_freed_blocks_alone(spmv_lib, as_int):
+    """The current stream has work queued on a block that is free again; the
+    call's own stream is idle and starts at once."""
+    call = Gradient(gen(80), 5000, 1000)
+    out = call.outputs()
+    current, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(current):
+        victim = torch.full((call.need,), 3, dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        keep = busy()
+        copy = victim.clone()
+        del victim
+        call.run(out, stream=other.cuda_stream if as_int else other)
+        other.synchronize()
+    torch.cuda.synchronize()
+    call.check(out)
+    assert (copy == 3).all() and keep.isfinite().all()
+
+
+def test_the_default_streams_workspace_grows_under_another_current_stream(spmv_lib):
+    """A thread whose current stream is another one calls on the default
+    stream, which is busy: first a small call, then a larger one that replaces
+    the kept workspace, then other work of the current stream on new memory."""
+    small, large = Gradient(gen(81), 2000, 64), Gradient(gen(82), 5000, 1000)
+    side = torch.cuda.Stream()
+    outs = [c.outputs() for c in (small, large)]
+    failed = []
+
+    def work():
+        try:
+            keep = busy()
+            with torch.cuda.stream(side):
+                for c, out in zip((small, large), outs):
+                    c.run(out, stream=0)
+                    torch.full((c.need,), 255, dtype=torch.uint8, device=DEV)
+                torch.full((small.need,), 255, dtype=torch.uint8, device=DEV)
+            torch.cuda.synchronize()
+            del keep
+        except Exception as e:  # (shown by the test's thread)
+            failed.append(e)
+
+    torch.cuda.synchronize()
+    thread = threading.Thread(target=work)
+    thread.start()
+    thread.join()
+    assert not failed
+    small.check(outs[0])
+    large.check(outs[1])

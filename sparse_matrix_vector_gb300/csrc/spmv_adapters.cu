@@ -180,8 +180,10 @@ __device__ __forceinline__ int rank_of(const AdapterArgs& p, int slot) {
 // acc[mt][nt] += rows j0 + 16 mt .. of A times tokens 8 nt .. over the inner
 // range [k0, k1), k0 a multiple of 64. Rows past the rank repeat its last row
 // (their h is not used); x[nt] is the row of this lane's token, any row where
-// there is none. ANY: rows of any alignment.
-template <typename T, int MT, int NT, bool ANY>
+// there is none. ANY: rows of any alignment. MOST: the largest NT that the
+// caller uses for these rows. The steps' length is chosen by it and not by NT,
+// so that a token's sums are added in the same order in every tile.
+template <typename T, int MT, int NT, int MOST, bool ANY>
 __device__ __forceinline__ void shrink(const AdapterArgs& p, const T* a, int rank, int j0,
                                        const T* const (&x)[NT], int k0, int k1,
                                        float (&acc)[MT][NT][4]) {
@@ -193,7 +195,7 @@ __device__ __forceinline__ void shrink(const AdapterArgs& p, const T* a, int ran
     for (int h = 0; h < 2; ++h)
       rows[m][h] = a + (int64_t)min(j0 + 16 * m + 8 * h + g, rank - 1) * p.n_in;
   int k = k0;
-  if constexpr (!ANY && MT * NT <= 16) {  // (more would not fit the registers)
+  if constexpr (!ANY && MT * MOST <= 16) {  // (more would not fit the registers)
     const int whole = p.vec_in == 2 ? k0 + max(min(k1, p.n_in) - k0, 0) / 64 * 64 : k0;
     for (; k < whole; k += 64) {
       Vec16 v[NT], w[MT][2];
@@ -451,7 +453,7 @@ __device__ __forceinline__ void few_shrink(const AdapterArgs& p, const T* a, int
   const int2 mine_k = inner_share(k0, k1, warp, WARPS);
   float acc[MT][1][4] = {};
   const T* const xs[1] = {x};
-  shrink<T, MT, 1, ANY>(p, a, rank, j0, xs, mine_k.x, mine_k.y, acc);
+  shrink<T, MT, 1, 1, ANY>(p, a, rank, j0, xs, mine_k.x, mine_k.y, acc);
   // [warp][token][16 MT]
   float* mine = s_warp + warp * kGroup * 16 * MT;
 #pragma unroll
@@ -701,7 +703,8 @@ __global__ void __launch_bounds__(kSortThreads) adapters_sort(AdapterArgs p) {
     int base = 0;
     if (s >= 0 && lane == first) base = atomicAdd(&s_count[s], __popc(same));
     base = __shfl_sync(0xffffffffu, base, first);
-    // the order of a slot's tokens does not change any token's result
+    // in whatever order the warps come: each token's sums are added in one
+    // order, whichever tile it is in (shrink)
     if (s >= 0) p.perm[base + __popc(same & ((1u << lane) - 1))] = i;
   }
 }
@@ -720,7 +723,7 @@ __device__ __forceinline__ void tile_shrink(const AdapterArgs& p, const T* a, in
     x[n] = static_cast<const T*>(p.x) + tokens[min(8 * n + g, n_tokens - 1)] * p.xs;
   const int2 mine = inner_share(k0, k1, warp, kWarps);
   float acc[MT][NT][4] = {};
-  shrink<T, MT, NT, ANY>(p, a, rank, j0, x, mine.x, mine.y, acc);
+  shrink<T, MT, NT, kTile / 8, ANY>(p, a, rank, j0, x, mine.x, mine.y, acc);
   constexpr int kWide = 16 * MT + 1;
   float* out = s_warp + warp * 8 * NT * kWide;
 #pragma unroll

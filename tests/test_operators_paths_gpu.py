@@ -126,3 +126,31 @@ def test_the_default_streams_workspace_grows_under_another_current_stream(spmv_l
     assert not failed
     small.check(outs[0])
     large.check(outs[1])
+
+
+# --------------------------------------------------------------- adapters
+
+@pytest.mark.parametrize("types", ops.ADAPTER_TYPES, ids=lambda p: "-".join(p))
+@pytest.mark.parametrize("rank", [16, 32, 40, 64, 129, 256])
+@pytest.mark.parametrize("n_in", [1536, 1544, 1531])
+def test_adapters_bits_do_not_depend_on_the_tiles(spmv_lib, types, rank, n_in):
+    """Prompts whose slots end in tiles of few and of many tokens: a token's
+    result has the same bits wherever it stands, and every time. (Inner sums
+    long enough that every warp takes several steps.)"""
+    g = gen(91 + rank + n_in)
+    sizes = [80, 100, 1, 65, 129, 200, 9]
+    t = sum(sizes)
+    ids = torch.repeat_interleave(torch.arange(len(sizes)), torch.tensor(sizes))[torch.randperm(t, generator=g)]
+    x, a, b, ids, base, scales = (v.to(DEV) for v in ops.adapter_case(g, t, n_in, 136, rank, len(sizes), *types, ids))
+
+    def run(order):
+        y = torch.empty_like(base)
+        S.spmv_adapters_run(x[order], a, b, ids[order], y, base=base[order], scales=scales)
+        back = torch.empty_like(y)
+        back[order] = y
+        return back
+
+    first = run(torch.arange(t, device=DEV))
+    for _ in range(4):
+        assert torch.equal(run(torch.arange(t, device=DEV)), first)
+        assert torch.equal(run(torch.randperm(t, generator=g).to(DEV)), first)

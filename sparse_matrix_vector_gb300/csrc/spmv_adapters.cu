@@ -973,12 +973,6 @@ int launch_cluster(const void* fn, int grid, int block, size_t smem, int cluster
   return cudaLaunchKernelExC(&cfg, fn, args) == cudaSuccess ? 0 : -1;
 }
 
-bool allow_smem(const void* fn, size_t bytes) {
-  return bytes <= 40 * 1024 ||  // 48 KB less the static part need no opt-in
-         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
-             cudaSuccess;
-}
-
 template <typename T, typename YT>
 spmv_status run_few(AdapterArgs& p, cudaStream_t st) {
   void* args[] = {&p};

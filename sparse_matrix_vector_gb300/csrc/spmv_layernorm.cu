@@ -729,10 +729,7 @@ spmv_status by_types(spmv_dtype x, spmv_dtype y, F&& f) {
 template <typename Args>
 spmv_status launch_rows(void (*fn)(Args), const RowShape& s, size_t smem, const Args& p,
                         cudaStream_t st, int more_ctas = 0) {
-  if (smem > 48 * 1024 - kSmemStatic &&  // (48 KB with the static part need no opt-in)
-      cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return SPMV_ERR_CUDA;
+  if (!allow_smem(reinterpret_cast<const void*>(fn), smem)) return SPMV_ERR_CUDA;
   fn<<<s.grid + more_ctas, s.threads, smem, st>>>(p);
   return launched();
 }

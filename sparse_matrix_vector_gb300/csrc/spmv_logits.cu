@@ -399,10 +399,7 @@ spmv_status launch_logits(const spmv_logits& p, cudaStream_t st) {
   const void* fn = vec ? reinterpret_cast<const void*>(&logits_rows<T, OT, kVec>)
                        : reinterpret_cast<const void*>(&logits_rows<T, OT, 1>);
   const size_t smem = (size_t)a.share * 2;
-  if (smem > 16 * 1024 &&  // 48 KB less the static part need no opt-in
-      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-          cudaSuccess)
-    return SPMV_ERR_CUDA;
+  if (!allow_smem(fn, smem)) return SPMV_ERR_CUDA;
   const int64_t jobs = (int64_t)p.n_requests * a.shares;
   void* args[] = {&a};
   return cudaLaunchKernel(fn, dim3((unsigned)(jobs < kWave ? jobs : kWave)), dim3(kLogitThreads),

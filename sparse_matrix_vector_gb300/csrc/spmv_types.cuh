@@ -8,7 +8,9 @@
 
 #include <cmath>
 #include <cstdint>
+#include <map>
 #include <mutex>
+#include <utility>
 
 #include "spmv_device.cuh"
 #include "spmv_internal.h"
@@ -232,11 +234,38 @@ __device__ __forceinline__ void set_pair(Pack<__nv_bfloat16, N>& r, int k, float
 
 }  // namespace
 
+// Leave for a kernel to be launched with `bytes` of dynamic shared memory.
+// The limit belongs to the function and counts for all host threads, and a
+// launch beyond it is refused: so it is set once per kernel and device, to the
+// most that the device has beside the kernel's static part, and never lowered.
+inline bool allow_smem(const void* fn, size_t bytes) {
+  if (bytes <= 16 * 1024) return true;  // (48 KB less any static part need no leave)
+  static std::mutex mu;
+  static std::map<std::pair<const void*, int>, size_t> most;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  std::lock_guard<std::mutex> lock(mu);
+  const auto known = most.find({fn, dev});
+  if (known != most.end()) return bytes <= known->second;
+  int optin = 0;
+  cudaFuncAttributes attr;
+  if (cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) !=
+          cudaSuccess ||
+      cudaFuncGetAttributes(&attr, fn) != cudaSuccess ||
+      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           optin - (int)attr.sharedSizeBytes) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  const size_t room = (size_t)optin - attr.sharedSizeBytes;
+  most[{fn, dev}] = room;
+  return bytes <= room;
+}
+
 // Clusters of `cluster` CTAs that the current device holds at a time: what
 // fits its SMs by registers and shared memory, less what a cluster's being
 // confined to one group of SMs leaves over (36 rather than 38 clusters of 8
-// at two CTAs per SM). Asked once per kernel and launch shape, when the kernel
-// is also given leave to use `smem` bytes. 0 on error.
+// at two CTAs per SM). Asked once per kernel and launch shape. 0 on error.
 inline int resident_clusters(const void* fn, int cluster, int block, size_t smem) {
   struct Known {
     const void* fn;
@@ -265,8 +294,7 @@ inline int resident_clusters(const void* fn, int cluster, int block, size_t smem
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-          cudaSuccess ||
+  if (!allow_smem(fn, smem) ||
       cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
     cudaGetLastError();
     return 0;

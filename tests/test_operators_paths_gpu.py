@@ -154,3 +154,62 @@ def test_adapters_bits_do_not_depend_on_the_tiles(spmv_lib, types, rank, n_in):
     for _ in range(4):
         assert torch.equal(run(torch.arange(t, device=DEV)), first)
         assert torch.equal(run(torch.randperm(t, generator=g).to(DEV)), first)
+
+
+# ---------------------------------------------------------------- threads
+
+def test_threads_with_calls_of_different_sizes(spmv_lib):
+    """Threads on streams of their own, whose calls take more and less shared
+    memory of the same kernels: none is refused, each is right."""
+    g = gen(90)
+    lists = {k: tuple(t.to(DEV) for t in a) if isinstance(a, tuple) else a.to(DEV)
+             for k, a in ops.everything(g, 300, 40000, 20, 4).items()}
+
+    def norm(d):
+        x = randn(g, 4, d).to(DEV)
+        return lambda out: S.spmv_layernorm(x, None, None, out), lambda: torch.empty_like(x)
+
+    def adapters(rank):
+        args = [t.to(DEV) for t in ops.adapter_case(g, 300, 128, 72, rank, 3, "f16", "f32")]
+        return (lambda out: S.spmv_adapters_run(*args[:4], out, base=args[4], scales=args[5]),
+                lambda: torch.empty_like(args[4]))
+
+    def logits(v):
+        x = randn(g, 300, v).to(DEV)
+        kw = {k: lists[k] for k in ("output", "frequency", "presence")}
+        return lambda out: S.spmv_logits_process(x, out, **kw), lambda: torch.empty_like(x)
+
+    # (call, outputs, repeats) of each thread
+    plans = [[(*norm(d), 3000) for d in sizes] + [(*adapters(r), 300) for r in ranks] + [(*logits(v), 300) for v in vocabs]
+             for sizes, ranks, vocabs in (((12288, 10240), (256, 96), (20480 * 2, 16000)),
+                                          ((10240, 12288), (64, 160), (18000, 20480 * 2)))]
+    refs = []
+    for plan in plans:
+        refs.append([])
+        for call, make, _ in plan:
+            out = make()
+            call(out)
+            refs[-1].append(out)
+    torch.cuda.synchronize()
+    failed = []
+    start = threading.Barrier(len(plans))
+
+    def work(plan, ref):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                start.wait()
+                for (call, make, times), right in zip(plan, ref):
+                    out = make()
+                    for _ in range(times):
+                        call(out)
+                    torch.cuda.current_stream().synchronize()
+                    assert torch.equal(out, right)
+        except Exception as e:  # (shown by the test's thread)
+            failed.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(plans, refs)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed

@@ -283,13 +283,14 @@ __device__ __forceinline__ float split_terms(const float (&v)[SPMV_ADAPTER_MAX_R
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < SPMV_ADAPTER_MAX_RANK / 32; ++i)
-      if (i < nk) m = fmaxf(m, fabsf(v[i]));
+      if (i < nk && isfinite(v[i])) m = fmaxf(m, fabsf(v[i]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    // the largest element to [2^13, 2^14); 0, infinities and fp32's very
-    // smallest stay as they are
+    // the largest finite element to [2^13, 2^14) (beside an infinite one they
+    // must not become infinite themselves); 0 and fp32's very smallest stay as
+    // they are
     const int e = (int)((__float_as_uint(m) >> 23) & 255) - 127;
-    if (e >= -113 && e < 128) {
+    if (e >= -113) {
       up = __uint_as_float((uint32_t)(13 - e + 127) << 23);
       down = __uint_as_float((uint32_t)(e - 13 + 127) << 23);
     }

@@ -213,3 +213,24 @@ def test_threads_with_calls_of_different_sizes(spmv_lib):
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+@pytest.mark.parametrize("t", [1, 40, 300])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_adapters_infinite_weights_leave_infinities(spmv_lib, t, dtype):
+    """One element of A x is infinite and the others are finite, far above
+    fp16's range and of the opposite effect: y is that infinity, not NaN."""
+    g = gen(92)
+    n_in, n_out, rank = 64, 24, 8
+    x = torch.full((t, n_in), 200.0).to(ops.TYPES[dtype])
+    a = torch.full((2, rank, n_in), 200.0).to(ops.TYPES[dtype])     # A x = 2,560,000
+    a[0, 3, 5] = float("inf")
+    b = -torch.ones(2, n_out, rank).to(ops.TYPES[dtype])
+    b[:, ::2, 3] = 1.0                                              # y = inf in even columns, -inf in odd ones
+    b[:, ::2, 4:] = -3.0
+    ids = torch.arange(t).int() % 2
+    y = torch.empty(t, n_out, device=DEV)
+    S.spmv_adapters_run(x.to(DEV), a.to(DEV), b.to(DEV), ids.to(DEV), y, base=randn(g, t, n_out).to(DEV))
+    got = y.cpu()
+    assert (got[::2, ::2] == float("inf")).all() and (got[::2, 1::2] == -float("inf")).all()
+    assert got[1::2].isfinite().all()

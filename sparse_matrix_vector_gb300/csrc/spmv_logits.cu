@@ -179,7 +179,9 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitPerSm) logits_rows(LogitA
   int64_t i = blockIdx.x / (unsigned)a.shares;
   int v0 = (int)(blockIdx.x % (unsigned)a.shares) * a.share;
   const int64_t step_i = gridDim.x / (unsigned)a.shares;
-  const int step_v = (int)(gridDim.x % (unsigned)a.shares) * a.share, wrap = a.shares * a.share;
+  // (the end of a row's last share, and a step beyond it, may pass 31 bits)
+  const unsigned step_v = gridDim.x % (unsigned)a.shares * (unsigned)a.share;
+  const unsigned wrap = (unsigned)a.shares * (unsigned)a.share;
   ask_logits(i, v0);
   Request next;
   next.load(p, i);
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitPerSm) logits_rows(LogitA
     Request q = next;
     q.settle(p);
     int64_t next_i = i + step_i;
-    int next_v = v0 + step_v;
+    unsigned next_v = (unsigned)v0 + step_v;
     if (next_v >= wrap) next_v -= wrap, ++next_i;
     const bool more = id + gridDim.x < jobs;
     if (more) next.load(p, next_i);
@@ -218,7 +220,7 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitPerSm) logits_rows(LogitA
     };
     for_entries(p.prompt_tokens, q.p0, q.p1, v0, n, s_queue[warp], &s_n, s_met, seen);
     for_entries(p.output_tokens, q.o0, q.o1, v0, n, s_queue[warp], &s_n, s_met, told);
-    if (more) ask_logits(next_i, next_v);
+    if (more) ask_logits(next_i, (int)next_v);
     // biases of this CTA's tokens, compacted in list order
     int listed = 0;
     for (int64_t k = q.b0; k < q.b1; k += kLogitThreads) {
@@ -363,7 +365,7 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitPerSm) logits_rows(LogitA
       __syncthreads();
     }
     i = next_i;
-    v0 = next_v;
+    v0 = (int)next_v;
   }
 }
 
@@ -385,7 +387,7 @@ spmv_status launch_logits(const spmv_logits& p, cudaStream_t st) {
   }
   // few requests: shares for every SM's first two CTAs (37 x 50257 bf16: 12.9
   // us, for all three 14.5, for the first 14.4)
-  const int64_t spread = 2 * 152 / p.n_requests, most = (p.vocab + kLeastShare - 1) / kLeastShare;
+  const int64_t spread = 2 * 152 / p.n_requests, most = (p.vocab + kLeastShare - 1ll) / kLeastShare;
   if (a.shares < spread && a.shares < most) a.shares = (int)(spread < most ? spread : most);
   a.share = (int)(((int64_t)p.vocab + a.shares - 1) / a.shares + 31) / 32 * 32;
   a.shares = (int)(((int64_t)p.vocab + a.share - 1) / a.share);

@@ -234,3 +234,24 @@ def test_adapters_infinite_weights_leave_infinities(spmv_lib, t, dtype):
     got = y.cpu()
     assert (got[::2, ::2] == float("inf")).all() and (got[::2, 1::2] == -float("inf")).all()
     assert got[1::2].isfinite().all()
+
+
+@pytest.mark.parametrize("stride", [2 ** 31, 2 ** 31 - 1])
+def test_logits_of_the_largest_vocabulary(spmv_lib, stride):
+    """Token numbers up to the last that int32 holds, in several requests (8.6
+    GB in place): the row's end, and a step past it, are above 2^31."""
+    v = 2 ** 31 - 1
+    buf = torch.zeros(stride + v + 8, dtype=torch.bfloat16, device=DEV)
+    x = buf.as_strided((2, v), (stride, 1))
+    tokens = [torch.tensor([0, 77, 2 ** 30 + 1, v - 9_000_000, v - 20000, v - 2, v - 1]), torch.tensor([5, 2 ** 30, v - 3, v - 1])]
+    off = torch.tensor([0, len(tokens[0]), len(tokens[0]) + len(tokens[1])], device=DEV)
+    mask = torch.full((1, (v + 31) // 32), -1, dtype=torch.int32, device=DEV)
+    mask[0, -1] = 0                                # the last 31 tokens
+    S.spmv_logits_process(x, x, output=(torch.cat(tokens).int().to(DEV), off), presence=torch.ones(2, device=DEV),
+                          mask=mask, mask_rows=torch.tensor([-1, 0], dtype=torch.int32, device=DEV))
+    assert (x[0, tokens[0].to(DEV)] == -1).all()
+    assert int((x[0] != 0).sum()) == len(tokens[0])
+    assert (x[1, tokens[1][:2].to(DEV)] == -1).all()
+    assert (x[1, v - 31:] == -float("inf")).all()
+    assert int((x[1] != 0).sum()) == 2 + 31
+    assert not buf[stride + v:].any() and not buf[v:stride].any()

@@ -986,8 +986,9 @@ spmv_status run_few(AdapterArgs& p, cudaStream_t st) {
   if (groups <= 9) {
     const void* fn = p.vec_in ? reinterpret_cast<const void*>(&adapters_few<T, YT, 16, 16, false>)
                               : reinterpret_cast<const void*>(&adapters_few<T, YT, 16, 16, true>);
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-      return SPMV_ERR_CUDA;
+    const spmv_status leave =
+        status_of(cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+    if (leave != SPMV_OK) return leave;
     e = launch_cluster(fn, groups * 16, 512, 0, 16, false, st, args);
   } else {  // at most two waves of two CTAs per SM
     const void* fn = p.vec_in ? reinterpret_cast<const void*>(&adapters_few<T, YT, 8, 8, false>)
@@ -995,7 +996,7 @@ spmv_status run_few(AdapterArgs& p, cudaStream_t st) {
     const int clusters = groups < 76 ? groups : 76;
     e = launch_cluster(fn, clusters * 8, 256, 0, 8, false, st, args);
   }
-  return e == 0 ? SPMV_OK : SPMV_ERR_CUDA;
+  return status_of_launch(e);
 }
 
 template <typename T, typename YT>
@@ -1014,8 +1015,8 @@ spmv_status run_many(AdapterArgs& p, cudaStream_t st) {
   if (!allow_smem(reinterpret_cast<const void*>(&adapters_sort), sort_smem) ||
       !allow_smem(shrink_fn, shrink_smem) || !allow_smem(expand_fn, expand_smem))
     return SPMV_ERR_CUDA;
-  adapters_sort<<<1, kSortThreads, sort_smem, st>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return SPMV_ERR_CUDA;
+  const spmv_status sorted = launch(adapters_sort, dim3(1), kSortThreads, sort_smem, st, p);
+  if (sorted != SPMV_OK) return sorted;
   void* args[] = {&p};
   const int most = resident_clusters(shrink_fn, p.k_split, kThreads, shrink_smem);
   if (most == 0) return SPMV_ERR_CUDA;
@@ -1023,18 +1024,18 @@ spmv_status run_many(AdapterArgs& p, cudaStream_t st) {
   // (two CTAs per SM where the terms of a large rank leave room for them)
   const int64_t wave = expand_smem <= 112 * 1024 ? 2 * kSms : kSms;
   const int64_t steps = (int64_t)p.max_tiles * ((p.n_out + 127) / 128);
-  if (launch_cluster(shrink_fn, clusters * p.k_split, kThreads, shrink_smem, p.k_split, true, st,
-                     args) != 0 ||
-      launch_pdl(expand_fn, (int)(steps < wave ? steps : wave), kThreads, expand_smem, st, args) != 0)
-    return SPMV_ERR_CUDA;
-  return SPMV_OK;
+  int e = launch_cluster(shrink_fn, clusters * p.k_split, kThreads, shrink_smem, p.k_split, true,
+                         st, args);
+  if (e == 0)
+    e = launch_pdl(expand_fn, (int)(steps < wave ? steps : wave), kThreads, expand_smem, st, args);
+  return status_of_launch(e);
 }
 
 template <typename T, typename YT>
 spmv_status run(AdapterArgs& p, cudaStream_t st) {
   if (p.n_slots == 0) {
-    if (p.base != p.y) adapters_copy<YT><<<p.n_tokens, kThreads, 0, st>>>(p);
-    return cudaGetLastError() == cudaSuccess ? SPMV_OK : SPMV_ERR_CUDA;
+    if (p.base == p.y) return SPMV_OK;
+    return launch(adapters_copy<YT>, dim3((unsigned)p.n_tokens), kThreads, 0, st, p);
   }
   return p.n_tokens <= kFewTokens ? run_few<T, YT>(p, st) : run_many<T, YT>(p, st);
 }

@@ -713,8 +713,6 @@ int64_t backward_workspace(int64_t n_rows, int n_cols, bool want_params) {
   return parts * 2 * n_cols * 4;
 }
 
-spmv_status launched() { return cudaGetLastError() == cudaSuccess ? SPMV_OK : SPMV_ERR_CUDA; }
-
 template <typename F>
 spmv_status by_types(spmv_dtype x, spmv_dtype y, F&& f) {
   if (x == SPMV_F32 && y == SPMV_F32) return f((float*)nullptr, (float*)nullptr);
@@ -730,8 +728,7 @@ template <typename Args>
 spmv_status launch_rows(void (*fn)(Args), const RowShape& s, size_t smem, const Args& p,
                         cudaStream_t st, int more_ctas = 0) {
   if (!allow_smem(reinterpret_cast<const void*>(fn), smem)) return SPMV_ERR_CUDA;
-  fn<<<s.grid + more_ctas, s.threads, smem, st>>>(p);
-  return launched();
+  return launch(fn, dim3((unsigned)(s.grid + more_ctas)), s.threads, smem, st, p);
 }
 
 // Vectors are 16 bytes of x; rows that they do not fit take the same columns
@@ -848,19 +845,19 @@ spmv_status backward(BackwardArgs<XT, YT> p, void* dweight, void* dbias, cudaStr
     const int grid = (int)(p.n_rows < kRowGrid ? p.n_rows : kRowGrid);
     parts = kLongParts;
     if (p.part)
-      layernorm_params_part<XT, YT>
-          <<<dim3((p.n_cols + kThreads - 1) / kThreads, kLongParts), kThreads, 0, st>>>(p);
-    if (p.dx) layernorm_dx_rows<XT, YT><<<grid, kThreads, 0, st>>>(p);
-    status = launched();
+      status = launch(layernorm_params_part<XT, YT>,
+                      dim3((unsigned)((p.n_cols + kThreads - 1) / kThreads), kLongParts), kThreads,
+                      0, st, p);
+    if (p.dx && status == SPMV_OK)
+      status = launch(layernorm_dx_rows<XT, YT>, dim3((unsigned)grid), kThreads, 0, st, p);
   }
   if (status != SPMV_OK || !p.part) return status;
   int n_cols = p.n_cols, pt = p.pt;
   const float* part = p.part;
   void* args[] = {&n_cols, &parts, &part, &dweight, &dbias, &pt};
-  return launch_pdl(reinterpret_cast<const void*>(&layernorm_params_sum),
-                    (int)((2ll * n_cols + 31) / 32), kSumWarps * 32, 0, st, args) == 0
-             ? SPMV_OK
-             : SPMV_ERR_CUDA;
+  return status_of_launch(launch_pdl(reinterpret_cast<const void*>(&layernorm_params_sum),
+                                     (int)((2ll * n_cols + 31) / 32), kSumWarps * 32, 0, st,
+                                     args));
 }
 
 }  // namespace
@@ -942,10 +939,11 @@ extern "C" spmv_status spmv_layernorm_backward(
     return SPMV_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (n_rows == 0) {
-    if ((dweight && cudaMemsetAsync(dweight, 0, (size_t)(n_cols * ps), st) != cudaSuccess) ||
-        (dbias && cudaMemsetAsync(dbias, 0, (size_t)(n_cols * ps), st) != cudaSuccess))
-      return SPMV_ERR_CUDA;
-    return SPMV_OK;
+    spmv_status status = SPMV_OK;
+    for (void* sum : {dweight, dbias})
+      if (sum && status == SPMV_OK)
+        status = status_of(cudaMemsetAsync(sum, 0, (size_t)(n_cols * ps), st));
+    return status;
   }
   return by_types(x_dtype, dy_dtype, [&](auto* xt, auto* yt) {
     using XT = std::remove_pointer_t<decltype(xt)>;

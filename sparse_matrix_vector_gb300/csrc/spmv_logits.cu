@@ -404,10 +404,8 @@ spmv_status launch_logits(const spmv_logits& p, cudaStream_t st) {
   if (!allow_smem(fn, smem)) return SPMV_ERR_CUDA;
   const int64_t jobs = (int64_t)p.n_requests * a.shares;
   void* args[] = {&a};
-  return cudaLaunchKernel(fn, dim3((unsigned)(jobs < kWave ? jobs : kWave)), dim3(kLogitThreads),
-                          args, smem, st) == cudaSuccess
-             ? SPMV_OK
-             : SPMV_ERR_CUDA;
+  return status_of(cudaLaunchKernel(fn, dim3((unsigned)(jobs < kWave ? jobs : kWave)),
+                                    dim3(kLogitThreads), args, smem, st));
 }
 
 }  // namespace

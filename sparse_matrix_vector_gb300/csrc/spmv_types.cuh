@@ -234,6 +234,28 @@ __device__ __forceinline__ void set_pair(Pack<__nv_bfloat16, N>& r, int k, float
 
 }  // namespace
 
+// The status of a runtime call or a launch, from its own result: the error
+// that the runtime keeps for the thread may be an earlier call's. One of this
+// call is reported here, and not left there for a later one.
+inline spmv_status status_of(cudaError_t e) {
+  if (e == cudaSuccess) return SPMV_OK;
+  cudaGetLastError();
+  return SPMV_ERR_CUDA;
+}
+// (of launch helpers that give 0 or -1)
+inline spmv_status status_of_launch(int e) {
+  return status_of(e == 0 ? cudaSuccess : cudaErrorLaunchFailure);
+}
+
+// Launch fn(p).
+template <typename Args>
+spmv_status launch(void (*fn)(Args), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                   const Args& p) {
+  void* args[] = {const_cast<Args*>(&p)};
+  return status_of(cudaLaunchKernel(reinterpret_cast<const void*>(fn), grid, dim3((unsigned)threads),
+                                    args, smem, st));
+}
+
 // Leave for a kernel to be launched with `bytes` of dynamic shared memory.
 // The limit belongs to the function and counts for all host threads, and a
 // launch beyond it is refused: so it is set once per kernel and device, to the

@@ -255,3 +255,32 @@ def test_logits_of_the_largest_vocabulary(spmv_lib, stride):
     assert (x[1, v - 31:] == -float("inf")).all()
     assert int((x[1] != 0).sum()) == 2 + 31
     assert not buf[stride + v:].any() and not buf[v:stride].any()
+
+
+def test_an_earlier_calls_error_is_not_reported_again(spmv_lib):
+    """A call that the driver refuses (one that waits for the device, while a
+    graph is captured) says so itself; the next calls are as good as ever."""
+    import numpy as np
+    plan = S.spmv_plan_create(np.array([0, 1], np.int32), np.zeros(1, np.int32), np.ones(1, np.float32), 4)
+    g = gen(93)
+    x, out = randn(g, 3, 200).to(DEV), torch.empty(3, 200, device=DEV)
+    args = [v.to(DEV) for v in ops.adapter_case(g, 300, 64, 40, 16, 3, "f16", "f32")]
+    none = [v.to(DEV) for v in ops.adapter_case(g, 5, 64, 40, 0, 0, "f16", "f32")]
+
+    def refused():
+        graph = torch.cuda.CUDAGraph()
+        with pytest.raises((RuntimeError, S.SpmvError)):
+            with torch.cuda.graph(graph):
+                torch.zeros(1, device=DEV)
+                S.spmv_plan_check(plan)
+        torch.cuda.synchronize()
+
+    refused()
+    S.spmv_layernorm(x, None, None, out)
+    assert out.isfinite().all()
+    for a in (args, none):
+        refused()
+        y = torch.empty_like(a[4])
+        S.spmv_adapters_run(*a[:4], y, base=a[4])
+        assert y.isfinite().all()
+    S.spmv_plan_destroy(plan)

@@ -23,6 +23,7 @@ from .api import SpmvError
 
 _CODES = {torch.float32: SPMV_F32, torch.float16: SPMV_F16, torch.bfloat16: SPMV_BF16}
 _F32, _I32, _I64 = torch.float32, torch.int32, torch.int64
+_INT32_MAX = 2**31 - 1
 _current_device = torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (absent in CPU builds)
 _library = None
@@ -43,6 +44,12 @@ def _lib_handle():
 def _check(status: int, where: str) -> None:
     if status != 0:
         raise SpmvError(status, where)
+
+
+def _fits(where: str, *sizes: int) -> None:
+    """Refuse sizes that the C call's 32-bit arguments would cut short."""
+    if max(sizes) > _INT32_MAX:
+        raise SpmvError(8, where)  # SPMV_ERR_TOO_LARGE
 
 
 def _dtype(t, what: str) -> int:
@@ -151,6 +158,7 @@ def spmv_layernorm(x, weight, bias, y, eps: float = 1e-5, mean=None, rstd=None,
     n_y, d_y, ys = _rows(y, "y")
     if n_y != n or d_y != d:
         raise ValueError("x and y must have the same shape")
+    _fits("spmv_layernorm", d)
     dev = _same_device(x, y, weight, bias, mean, rstd)
     w, b, p = _params(weight, bias, d, "weight and bias")
     _check(_lib_handle().spmv_layernorm(
@@ -160,7 +168,9 @@ def spmv_layernorm(x, weight, bias, y, eps: float = 1e-5, mean=None, rstd=None,
 
 
 def spmv_layernorm_backward_workspace(n_rows: int, n_cols: int, want_params: bool = True) -> int:
-    """Bytes of workspace that spmv_layernorm_backward needs."""
+    """Bytes of workspace that spmv_layernorm_backward needs (0 for sizes it refuses)."""
+    if not 0 < n_cols <= _INT32_MAX:
+        return 0
     return int(_lib_handle().spmv_layernorm_backward_workspace(n_rows, n_cols, int(want_params)))
 
 
@@ -174,6 +184,7 @@ def spmv_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, works
     n_dy, d_dy, dys = _rows(dy, "dy")
     if n_dy != n or d_dy != d:
         raise ValueError("dy and x must have the same shape")
+    _fits("spmv_layernorm_backward", d)
     code = _dtype(x, "x")
     dxs = 0
     if dx is not None:
@@ -202,7 +213,9 @@ def spmv_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, works
 
 
 def spmv_adapters_workspace(n_tokens: int, n_slots: int, rank: int) -> int:
-    """Bytes of workspace that spmv_adapters_run needs."""
+    """Bytes of workspace that spmv_adapters_run needs (0 for sizes it refuses)."""
+    if min(n_tokens, n_slots, rank) < 0 or max(n_tokens, n_slots, rank) > _INT32_MAX:
+        return 0
     return int(_lib_handle().spmv_adapters_workspace(n_tokens, n_slots, rank))
 
 
@@ -222,6 +235,7 @@ def spmv_adapters_run(x, a, b, slot_ids, y, base=None, ranks=None, scales=None, 
     slots, rank, a_in = a.shape
     if a_in != n_in or tuple(b.shape) != (slots, n_out, rank):
         raise ValueError(f"a must be (slots, rank, {n_in}) and b (slots, {n_out}, rank)")
+    _fits("spmv_adapters_run", t, n_in, n_out, slots, rank)
     if a.dtype != x.dtype or b.dtype != x.dtype:
         raise TypeError("a and b must have x's type")
     if not a.is_contiguous() or not b.is_contiguous():
@@ -274,6 +288,7 @@ def spmv_logits_process(logits, out, prompt=None, output=None, repetition=None, 
     n_o, v_o, out_stride = _rows(out, "out")
     if n_o != n or v_o != v:
         raise ValueError("logits and out must have the same shape")
+    _fits("spmv_logits_process", n, v)
     p_tok, p_off = _list(prompt, n, "prompt")
     o_tok, o_off = _list(output, n, "output")
     b_tok = b_val = b_off = 0
@@ -287,6 +302,7 @@ def spmv_logits_process(logits, out, prompt=None, output=None, repetition=None, 
         n_masks, words, m_stride = _rows(mask, "mask")
         if words != (v + 31) // 32:
             raise ValueError(f"mask must have {(v + 31) // 32} words in a row")
+        _fits("spmv_logits_process", n_masks)
         if mask_rows is None and n_masks < n:
             raise ValueError("mask must have a row for each request (or give mask_rows)")
         m_ptr = mask.data_ptr()

@@ -7,6 +7,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+import sparse_matrix_vector_gb300 as S  # noqa: E402
 from sparse_matrix_vector_gb300 import operators as ops  # noqa: E402
 
 
@@ -61,3 +62,38 @@ def test_the_default_stream_keeps_its_workspace_in_its_own_pool(pools):
     ops._workspace(None, 2000, handle=0, dev=0)          # the smaller one is dropped
     assert pools.taken == [(0, 1000), (0, 2000)]
     assert pools.current == 64
+
+
+def _meta(*size, dtype=torch.float16):
+    return torch.empty(*size, dtype=dtype, device="meta")
+
+
+FAR = 2 ** 32 + 8  # (cut to 8 by a 32-bit argument)
+
+
+@pytest.mark.parametrize("call", [
+    lambda: S.spmv_layernorm(_meta(2, FAR), None, None, _meta(2, FAR)),
+    lambda: S.spmv_layernorm(_meta(FAR), None, None, _meta(FAR)),
+    lambda: S.spmv_layernorm_backward(_meta(2, FAR), _meta(2, FAR), None, _meta(2), _meta(2), _meta(2, FAR), None, None),
+    lambda: S.spmv_adapters_run(_meta(FAR, 4), _meta(2, 3, 4), _meta(2, 5, 3), _meta(FAR), _meta(FAR, 5)),
+    lambda: S.spmv_adapters_run(_meta(2, FAR), _meta(2, 3, FAR), _meta(2, 5, 3), _meta(2), _meta(2, 5)),
+    lambda: S.spmv_adapters_run(_meta(2, 4), _meta(2, 3, 4), _meta(2, FAR, 3), _meta(2), _meta(2, FAR)),
+    lambda: S.spmv_adapters_run(_meta(2, 4), _meta(2, FAR, 4), _meta(2, 5, FAR), _meta(2), _meta(2, 5)),
+    lambda: S.spmv_adapters_run(_meta(2, 4), _meta(FAR, 3, 4), _meta(FAR, 5, 3), _meta(2), _meta(2, 5)),
+    lambda: S.spmv_logits_process(_meta(2, FAR), _meta(2, FAR)),
+    lambda: S.spmv_logits_process(_meta(FAR, 2), _meta(FAR, 2)),
+    lambda: S.spmv_logits_process(_meta(2, 40), _meta(2, 40), mask=_meta(FAR, 2, dtype=torch.int32)),
+])
+def test_sizes_past_32_bits_are_refused(call):
+    with pytest.raises(S.SpmvError) as e:
+        call()
+    assert e.value.status == 8  # too large
+
+
+def test_workspaces_of_sizes_past_32_bits(spmv_lib):
+    assert S.spmv_layernorm_backward_workspace(5000, FAR) == 0
+    assert S.spmv_layernorm_backward_workspace(5000, 8 - 2 ** 32) == 0
+    assert S.spmv_adapters_workspace(FAR + 5000, 2, 8) == 0
+    assert S.spmv_adapters_workspace(5000, FAR, 8) == 0
+    assert S.spmv_adapters_workspace(5000, 2, FAR) == 0
+    assert S.spmv_adapters_workspace(5000 - 2 ** 32, 2, 8) == 0

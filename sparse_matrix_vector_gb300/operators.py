@@ -8,7 +8,7 @@ which is the current one; matrices have contiguous columns and any row
 stride. Calls run on ``stream`` (default: the current torch stream) and do
 not synchronize. A workspace that the caller does not give comes from torch's
 caching allocator, from the pool of the stream that the call runs on; the
-default stream's is kept for its next call.
+default stream's is kept for its next call, up to 64 MiB for each thread.
 """
 from __future__ import annotations
 
@@ -30,8 +30,11 @@ _library = None
 # Workspaces of the default stream, one per thread and device, kept for the
 # next call: its calls are in order, and it can be neither captured nor
 # destroyed. (Taking one from the allocator between launches costs 4 us and
-# makes the launches 2 us slower, of some 20 us a call.)
+# makes the launches 2 us slower, of some 20 us a call.) Larger ones, whose
+# calls take some 100 us and more, are not kept: a thread would hold its
+# largest call's for good.
 _kept = threading.local()
+_KEPT_BYTES = 64 << 20
 
 
 def _lib_handle():
@@ -126,7 +129,7 @@ def _workspace(given, n_bytes: int, handle: int, dev: int):
         return given.data_ptr(), given.numel() * given.element_size(), given
     if n_bytes == 0:
         return None, 0, None
-    if handle == 0:
+    if handle == 0 and n_bytes <= _KEPT_BYTES:
         try:
             kept = _kept.by_device
         except AttributeError:

@@ -97,3 +97,15 @@ def test_workspaces_of_sizes_past_32_bits(spmv_lib):
     assert S.spmv_adapters_workspace(5000, FAR, 8) == 0
     assert S.spmv_adapters_workspace(5000, 2, FAR) == 0
     assert S.spmv_adapters_workspace(5000 - 2 ** 32, 2, 8) == 0
+
+
+def test_a_large_workspace_is_not_kept(pools):
+    """A call with a large workspace on the default stream leaves nothing
+    behind, and the smaller one that is kept stays."""
+    first = ops._workspace(None, 1000, handle=0, dev=0)[0]
+    n = (64 << 20) + 1
+    for k in range(2):
+        owner = ops._workspace(None, n, handle=0, dev=0)[2]
+        assert owner.numel() == n and pools.taken == [(0, 1000)] + (k + 1) * [(0, n)]
+    assert [t.numel() for t in ops._kept.by_device.values()] == [1000]
+    assert ops._workspace(None, 1000, handle=0, dev=0)[0] == first

@@ -1,6 +1,7 @@
 """GPU tests of the operators around a pruned layer, beside those in
 test_operators_gpu.py (whose references and tolerances they use): paths that
 only larger calls, other streams, several threads or unusual arguments reach."""
+import ctypes
 import threading
 
 import pytest
@@ -267,12 +268,18 @@ def test_an_earlier_calls_error_is_not_reported_again(spmv_lib):
     args = [v.to(DEV) for v in ops.adapter_case(g, 300, 64, 40, 16, 3, "f16", "f32")]
     none = [v.to(DEV) for v in ops.adapter_case(g, 5, 64, 40, 0, 0, "f16", "f32")]
 
+    # (the driver's own capture: torch's would leave its random numbers in it)
+    driver, side = ctypes.CDLL("libcuda.so.1"), torch.cuda.Stream()
+
     def refused():
-        graph = torch.cuda.CUDAGraph()
-        with pytest.raises((RuntimeError, S.SpmvError)):
-            with torch.cuda.graph(graph):
-                torch.zeros(1, device=DEV)
+        graph = ctypes.c_void_p()
+        torch.cuda.synchronize()
+        assert driver.cuStreamBeginCapture_v2(ctypes.c_void_p(side.cuda_stream), 0) == 0
+        try:
+            with pytest.raises(S.SpmvError):
                 S.spmv_plan_check(plan)
+        finally:
+            driver.cuStreamEndCapture(ctypes.c_void_p(side.cuda_stream), ctypes.byref(graph))
         torch.cuda.synchronize()
 
     refused()

@@ -291,3 +291,34 @@ def test_an_earlier_calls_error_is_not_reported_again(spmv_lib):
         S.spmv_adapters_run(*a[:4], y, base=a[4])
         assert y.isfinite().all()
     S.spmv_plan_destroy(plan)
+
+
+def test_the_readmes_calls_run(spmv_lib):
+    """The operators' calls as README.md prints them."""
+    import os
+    import re
+
+    import numpy as np
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    blocks = re.findall(r"```python\n(.*?)```", open(os.path.join(root, "README.md")).read(), re.S)
+    code, = [c for c in blocks if "spmv_logits_process" in c]
+    g = gen(94)
+    n, d = 3, 64
+    plan = S.spmv_plan_create(np.arange(d + 1, dtype=np.int32), np.arange(d, dtype=np.int32), np.ones(d, np.float16), d)
+    residual, x, y = randn(g, n, d).to(DEV), torch.empty(n, d, dtype=torch.float16, device=DEV), torch.empty(n, d, device=DEV)
+    names = dict(S=S, plan=plan, residual=residual, x=x, y=y, weight=randn(g, d).to(DEV), bias=randn(g, d).to(DEV),
+                 mean=torch.empty(n, device=DEV), rstd=torch.empty(n, device=DEV), a=randn(g, 2, 4, d, dtype="f16").to(DEV),
+                 b=randn(g, 2, d, 4, dtype="f16").to(DEV), slot_ids=torch.zeros(n, dtype=torch.int32, device=DEV),
+                 ranks=torch.full((2,), 4, dtype=torch.int32, device=DEV), scales=torch.ones(2, device=DEV),
+                 logits=randn(g, n, d).to(DEV), tokens=torch.arange(n, dtype=torch.int32, device=DEV),
+                 offsets=torch.arange(n + 1, device=DEV), values=torch.ones(n, device=DEV), rep=torch.ones(n, device=DEV),
+                 freq=torch.ones(n, device=DEV), pres=torch.ones(n, device=DEV),
+                 mask=torch.full((n, d // 32), -1, dtype=torch.int32, device=DEV),
+                 mask_rows=torch.arange(n, dtype=torch.int32, device=DEV), dy=randn(g, n, d, dtype="f16").to(DEV),
+                 dx=torch.empty(n, d, device=DEV), dweight=torch.empty(d, device=DEV), dbias=torch.empty(d, device=DEV))
+    before = names["logits"].clone()
+    exec(code, names)
+    ref = before.clone()
+    ref[torch.arange(n), torch.arange(n)] += 1.0 - 1.0 - 1.0  # bias, frequency, presence
+    assert torch.allclose(names["logits"], ref, atol=1e-6)
+    S.spmv_plan_destroy(plan)

@@ -322,3 +322,144 @@ def test_the_readmes_calls_run(spmv_lib):
     ref[torch.arange(n), torch.arange(n)] += 1.0 - 1.0 - 1.0  # bias, frequency, presence
     assert torch.allclose(names["logits"], ref, atol=1e-6)
     S.spmv_plan_destroy(plan)
+
+
+# ------------------------------------- adapters: prompts and long inner sums
+#
+# The tolerance of test_operators_gpu.py with K = 256: a matrix instruction
+# adds with an error of at most 2 u of what it has summed; the longest chains
+# here are 12 of them and 16 partial sums in the first product (12288 inputs
+# over 8 blocks of 8 warps at least) and 48 in the second (256 columns of B
+# times three terms): 2 (12 + 48) + 16 + 2 < 256.
+
+def check_prompts(case, ranks=None, in_place=False, y_layout=(None, 0)):
+    """spmv_adapters_run against products per slot in 64 bits."""
+    x, a, b, ids, base, scales = (v.to(DEV) for v in case)
+    t, n_out = base.shape
+    _, y = ops.out_like(t, n_out, base.dtype, *y_layout)
+    given = base
+    if in_place:
+        y.copy_(base)
+        given = y
+    S.spmv_adapters_run(x, a, b, ids, y, base=given, scales=scales, ranks=ranks)
+    k = 256 * ops.U
+    ref, slack = base.double().clone(), k * base.double().abs()
+    for s in range(a.shape[0]):
+        at = (ids == s).nonzero()[:, 0]
+        r = a.shape[1] if ranks is None else min(max(int(ranks[s]), 0), a.shape[1])
+        A, B, xs = a[s, :r].double(), b[s, :, :r].double(), x[at].double()
+        ref[at] += float(scales[s]) * (xs @ A.T @ B.T)
+        slack[at] += k * abs(float(scales[s])) * (xs.abs() @ A.abs().T @ B.abs().T)
+    v = base.dtype
+    ops.close(y, ref.cpu(), (ops.ROUND[v] * ref.abs() + slack + ops.TINY[v]).cpu(), "y")
+
+
+@pytest.mark.parametrize("types", [("f16", "f32"), ("bf16", "bf16")], ids=lambda p: "-".join(p))
+@pytest.mark.parametrize("n_in,n_out", [(12288, 200), (12296, 136), (8195, 131)])
+@pytest.mark.parametrize("rank", [16, 32, 64, 65, 128, 256])
+@pytest.mark.parametrize("t", [1, 48, 256, 300, 600])
+def test_adapters_long_inner_sums(spmv_lib, t, rank, n_in, n_out, types):
+    """Rows of whole 32 bytes, of whole 16 bytes and of any alignment, long
+    enough for the main loops of both products, one block of ranks and more."""
+    g = gen(100 + t + rank + n_in)
+    check_prompts(ops.adapter_case(g, t, n_in, n_out, rank, 4, *types))
+
+
+@pytest.mark.parametrize("t", [300, 700])
+@pytest.mark.parametrize("ids", ["none", "outside", "one", "runs", "alternating"])
+def test_adapters_prompts_slot_ids(spmv_lib, t, ids):
+    g = gen(141)
+    slots = 6
+    i = {"none": torch.full((t,), -1), "outside": torch.tensor([-7, slots, 2 ** 31 - 1, -2 ** 31, 3])[torch.arange(t) % 5],
+         "one": torch.full((t,), 4), "runs": torch.arange(t) * slots // t, "alternating": torch.arange(t) % 2}[ids]
+    ops.check_adapters(*ops.adapter_case(g, t, 160, 96, 16, slots, "f16", "f32", i))
+
+
+@pytest.mark.parametrize("rank", [16, 72])
+@pytest.mark.parametrize("types", ops.ADAPTER_TYPES, ids=lambda p: "-".join(p))
+@pytest.mark.parametrize("layout", [dict(x_layout=(161, 0)), dict(x_layout=(None, 1)), dict(y_layout=(131, 0)),
+                                    dict(y_layout=(None, 3)), dict(base_layout=(133, 1)), dict(w_offset=1),
+                                    dict(w_offset=8, x_layout=(176, 8), y_layout=(136, 8), base_layout=(144, 8))], ids=str)
+def test_adapters_prompts_layouts(spmv_lib, types, layout, rank):
+    g = gen(142)
+    ops.check_adapters(*ops.adapter_case(g, 300, 160, 128, rank, 3, *types), **layout)
+
+
+@pytest.mark.parametrize("layout", [(None, 0), (141, 0), (140, 3)], ids=str)
+@pytest.mark.parametrize("t", [5, 300])
+def test_adapters_in_place_layouts(spmv_lib, t, layout):
+    g = gen(143)
+    check_prompts(ops.adapter_case(g, t, 264, 136, 40, 3, "f16", "f32"), in_place=True, y_layout=layout)
+
+
+def test_adapters_prompts_without_base_scales_or_sizes(spmv_lib):
+    g = gen(144)
+    t = 300
+    x, a, b, ids, base, scales = ops.adapter_case(g, t, 100, 60, 16, 3, "f16", "f32")
+    ops.check_adapters(x, a, b, ids, base, None, with_base=False)
+    ops.check_adapters(*ops.adapter_case(g, t, 128, 61, 40, 3, "bf16", "bf16"), with_base=False)
+    for n_in, rank, slots in ((100, 16, 0), (100, 0, 3), (0, 16, 3)):
+        x, a, b, _, base, _ = ops.adapter_case(g, t, n_in, 60, rank, slots, "f16", "f32", ids)
+        ops.check_adapters(x, a, b, ids, base, None)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("size", [1e-4, 1.0, 300.0])
+def test_adapters_prompts_sizes_of_the_inner_product(spmv_lib, dtype, size):
+    g = gen(145)
+    x, a, b, ids, base, scales = ops.adapter_case(g, 300, 512, 40, 16, 2, dtype, "f32", torch.zeros(300))
+    x, a = (x.float() * size).to(x.dtype), (a.float() * 22 * size).to(a.dtype)
+    ops.check_adapters(x, a, b, ids, base * 0, scales)
+
+
+def test_adapters_prompts_a_token_does_not_depend_on_its_tile(spmv_lib):
+    """NaN and infinities of one token, or of one slot's weights, stay with
+    the tokens that use them; so do those in ranks that a slot does not use."""
+    g = gen(146)
+    t = 400
+    x, a, b, ids, base, scales = ops.adapter_case(g, t, 200, 72, 40, 4, "f16", "f32", torch.arange(t) % 4)
+    x[7, 3], x[22, 0] = float("nan"), float("inf")
+    a[3, 2, 5] = float("nan")
+    ranks = torch.tensor([40, 17, 32, 40])
+    a[1, 17:], b[1, :, 17:], a[2, 32:], b[2, :, 32:] = (float("nan"),) * 4
+    y = torch.empty(t, 72, device=DEV)
+    S.spmv_adapters_run(x.to(DEV), a.to(DEV), b.to(DEV), ids.to(DEV), y, base=base.to(DEV), scales=scales.to(DEV),
+                        ranks=ranks.int().to(DEV))
+    ref, slack = ops.adapters_ref(x, a, b, ids, base, ranks, scales)
+    clean = [k for k in range(t) if k not in (7, 22) and k % 4 != 3]
+    ops.close(y[clean], ref[clean], ops.U * ref[clean].abs() + slack[clean])
+    assert y[7].isnan().all() and y[3].isnan().all() and not y[22].isfinite().any()
+
+
+def test_adapters_most_slots_and_many_tokens(spmv_lib):
+    g = gen(147)
+    # (a reference per slot met: a dense one of 16384 slots would take long)
+    x, a, b, ids, base, scales = ops.adapter_case(g, 300, 16, 8, 4, 16384, "f16", "f32")
+    ids[:2] = torch.tensor([16383, 0])
+    ops.check_adapters(x, a, b, ids, base, scales)
+    check_prompts(ops.adapter_case(g, 30000, 32, 24, 8, 3, "f16", "f16"))
+
+
+# --------------------------------------------------------- norm: long rows
+
+@pytest.mark.parametrize("types", ops.PAIRS, ids=lambda p: "-".join(p))
+@pytest.mark.parametrize("d", [13320, 16384, 16392, 20001])
+def test_norm_and_gradient_of_long_rows(spmv_lib, types, d):
+    """Both sides of where a row stops fitting one block, rows enough for
+    several per block and for partial sums; the gradient in place of dy."""
+    g = gen(150 + d)
+    n = 70
+    x = randn(g, n, d, dtype=types[0], std=1.5, mean=0.25)
+    w = randn(g, d, mean=1.0, std=0.3)
+    ops.check_norm(x, w, randn(g, d), types[1])
+    dy = randn(g, n, d, dtype=types[1], std=0.5)
+    ops.check_grad(dy, x, w)
+    if types[0] == types[1]:
+        m, r = x.float().mean(1).to(DEV), (torch.rand(n, generator=g) + 0.5).to(DEV)
+        outs = []
+        for in_place in (False, True):
+            dyd = dy.to(DEV)
+            dx, dw, db = dyd if in_place else torch.empty_like(dyd), torch.empty(d, device=DEV), torch.empty(d, device=DEV)
+            S.spmv_layernorm_backward(dyd, x.to(DEV), w.to(DEV), m, r, dx, dw, db)
+            outs.append((dx, dw, db))
+        assert all(torch.equal(p, q) for p, q in zip(*outs))

@@ -530,7 +530,8 @@ void spmv_plan_destroy(spmv_plan* plan);
  *     contiguous). An input's stride may be 0 (one row used for all); an
  *     output's is at least its number of columns. Pointers are aligned to
  *     their element size; 16-byte aligned rows are the fastest.
- *   - Inputs and outputs do not overlap unless a call says so.
+ *   - Inputs and outputs share no element unless a call says so (column
+ *     ranges of one matrix, or rows of it in turn, share none).
  *   - Sums, statistics and products are held in fp32, and each output is
  *     rounded to its type once. Runs are deterministic: the same inputs give
  *     the same bits.

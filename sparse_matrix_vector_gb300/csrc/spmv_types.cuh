@@ -349,7 +349,9 @@ inline bool rows_aligned(const void* p, int64_t rows, int64_t stride, int64_t si
   return aligned_to(p, bytes) && (rows <= 1 || (stride * size) % bytes == 0);
 }
 
-// Whether the bytes of two matrices' spans overlap.
+// Whether two matrices may share bytes. Where their spans meet, rows of one
+// distance may still be column ranges of one matrix, side by side, or rows of
+// it in turn: then they share bytes only if some do modulo that distance.
 inline bool spans_overlap(const void* p, int64_t p_rows, int64_t p_cols, int64_t p_stride,
                           int64_t p_size, const void* q, int64_t q_rows, int64_t q_cols,
                           int64_t q_stride, int64_t q_size) {
@@ -357,7 +359,15 @@ inline bool spans_overlap(const void* p, int64_t p_rows, int64_t p_cols, int64_t
   const uintptr_t p0 = (uintptr_t)p, q0 = (uintptr_t)q;
   const uintptr_t p1 = p0 + (uintptr_t)(((p_rows - 1) * p_stride + p_cols) * p_size);
   const uintptr_t q1 = q0 + (uintptr_t)(((q_rows - 1) * q_stride + q_cols) * q_size);
-  return p0 < q1 && q0 < p1;
+  if (p0 >= q1 || q0 >= p1) return false;
+  const uintptr_t p_row = (uintptr_t)(p_cols * p_size), q_row = (uintptr_t)(q_cols * q_size);
+  const uintptr_t p_step = (uintptr_t)(p_stride * p_size), q_step = (uintptr_t)(q_stride * q_size);
+  const uintptr_t step = p_rows > 1 ? p_step : q_step;
+  if ((p_rows == 1 && q_rows == 1) || (p_rows > 1 && q_rows > 1 && p_step != q_step) ||
+      p_row > step || q_row > step)
+    return true;
+  const uintptr_t d = q0 >= p0 ? (q0 - p0) % step : (step - (p0 - q0) % step) % step;
+  return d < p_row || d + q_row > step;
 }
 
 }  // namespace spmv

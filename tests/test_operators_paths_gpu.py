@@ -463,3 +463,61 @@ def test_norm_and_gradient_of_long_rows(spmv_lib, types, d):
             S.spmv_layernorm_backward(dyd, x.to(DEV), w.to(DEV), m, r, dx, dw, db)
             outs.append((dx, dw, db))
         assert all(torch.equal(p, q) for p, q in zip(*outs))
+
+
+# ----------------------------------------------- columns side by side, rows in turn
+
+def side_by_side(rows, widths, dtype):
+    """Column ranges of one matrix."""
+    buf = torch.zeros(rows, sum(widths), dtype=dtype, device=DEV)
+    at = [sum(widths[:i]) for i in range(len(widths))]
+    return [buf[:, a:a + w] for a, w in zip(at, widths)]
+
+
+def rows_in_turn(rows, n, cols, dtype):
+    buf = torch.zeros(rows * n, cols, dtype=dtype, device=DEV)
+    return [buf[i::n] for i in range(n)]
+
+
+@pytest.mark.parametrize("d", [64, 263])
+@pytest.mark.parametrize("rows", [2, 300])
+def test_inputs_and_outputs_of_one_matrix(spmv_lib, rows, d):
+    """Column ranges of one matrix, and rows of it in turn, share no element."""
+    g = gen(160 + d + rows)
+    x = randn(g, rows, d).to(DEV)
+    for xs, ys in (side_by_side(rows, (d, d), x.dtype), side_by_side(rows, (d, d), x.dtype)[::-1], rows_in_turn(rows, 2, d, x.dtype)):
+        xs.copy_(x)
+        y = torch.empty_like(x)
+        S.spmv_layernorm(x, None, None, y)
+        S.spmv_layernorm(xs, None, None, ys)
+        assert torch.equal(y, ys) and torch.equal(x, xs)
+        m, r = x.mean(1), torch.ones(rows, device=DEV)
+        dy = randn(g, rows, d, dtype="f16").to(DEV)
+        S.spmv_layernorm_backward(dy, x, None, m, r, y, None, None)
+        S.spmv_layernorm_backward(dy, xs, None, m, r, ys, None, None)
+        assert torch.equal(y, ys) and torch.equal(x, xs)
+        p = torch.ones(rows, device=DEV)
+        lists = (torch.zeros(rows, dtype=torch.int32, device=DEV), torch.arange(rows + 1, device=DEV))
+        S.spmv_logits_process(x, y, output=lists, presence=p)
+        S.spmv_logits_process(xs, ys, output=lists, presence=p)
+        assert torch.equal(y, ys) and torch.equal(x, xs)
+    case = [v.to(DEV) for v in ops.adapter_case(g, rows, d, d + 9, 16, 3, "f16", "f16")]
+    # (the same strides and boundaries, in three matrices and in one)
+    apart = [side_by_side(rows, (d, d + 9, d + 9), torch.float16)[i] for i in range(3)]
+    one = side_by_side(rows, (d, d + 9, d + 9), torch.float16)
+    for xs, bases, ys in (apart, one):
+        xs.copy_(case[0])
+        bases.copy_(case[4])
+        S.spmv_adapters_run(xs, *case[1:4], ys, base=bases, scales=case[5])
+    assert all(torch.equal(p, q) for p, q in zip(apart, one))
+    assert torch.equal(one[0], case[0]) and torch.equal(one[1], case[4])
+
+
+def test_shared_elements_are_refused(spmv_lib):
+    buf = torch.zeros(9, 40, device=DEV)
+    for x, y in ((buf[:, :16], buf[:, 15:31]), (buf[:, 8:24], buf[:, :16]), (buf[:, :30], buf[:, 10:40]), (buf[:8], buf[1:]),
+                 (buf[::2, :16], buf[::2, 8:24]), (buf[:5, :8], buf.view(-1)[4:4 + 5 * 8].view(5, 8)), (buf[0, :8], buf[0, 7:15])):
+        with pytest.raises(S.SpmvError):
+            S.spmv_layernorm(x, None, None, y)
+        with pytest.raises(S.SpmvError):
+            S.spmv_logits_process(x, y)

@@ -32,7 +32,8 @@ constexpr uint32_t kSeen = 0x8000u, kBiased = 0x4000u, kCount = 0x3fffu, kHeavy 
 constexpr int kShare = 20480;      // tokens of a CTA's share, at most (a table of 40 KB)
 constexpr int kLeastShare = 1024;  // and at least
 constexpr int kMet = 2048;         // listed tokens of a share kept as a list, with their results
-constexpr int kListed = 384;       // biases of a share kept in shared memory
+constexpr int kListed = 384;       // biases kept in shared memory at a time
+constexpr int kMany = 1 << 20;     // added to the count of met tokens of a share with more of them
 
 constexpr int kWave = kLogitPerSm * 152;  // CTAs that the device's SMs hold at a time
 
@@ -150,6 +151,97 @@ __device__ __forceinline__ void for_entries(const int32_t* list, int64_t lo, int
   flush();
 }
 
+// How often v stands in a list, by the whole CTA.
+__device__ __forceinline__ int count_of(int v, const int32_t* list, int64_t n, int* s_exact) {
+  __syncthreads();
+  if (threadIdx.x == 0) *s_exact = 0;
+  __syncthreads();
+  int count = 0;
+  for (int64_t j = threadIdx.x; j < n; j += kLogitThreads) count += list[j] == v;
+  count = __reduce_add_sync(0xffffffffu, count);
+  if ((threadIdx.x & 31) == 0) atomicAdd(s_exact, count);
+  __syncthreads();
+  return *s_exact;
+}
+
+// The places of the CTA's `mine` entries of a list's next kLogitThreads ones,
+// in list order after `listed` earlier ones; adds their number to `listed`. One
+// barrier; another one before s_warp is used again.
+__device__ __forceinline__ int list_places(bool mine, int& listed, int* s_warp) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t m = __ballot_sync(0xffffffffu, mine);
+  if (lane == 0) s_warp[warp] = __popc(m);
+  __syncthreads();
+  int before = listed;
+#pragma unroll
+  for (int w = 0; w < kLogitWarps; ++w) {
+    before += w < warp ? s_warp[w] : 0;
+    listed += s_warp[w];
+  }
+  return before + __popc(m & ((1u << lane) - 1));
+}
+
+// The met tokens of a share with more biases than are kept, which the pass has
+// left alone, straight into out (a call of its own: inlined, its registers
+// would be taken from the pass). kMet tokens at a time, first the sums of their
+// biases, each token's in list order: the list goes by in pieces of kLogitThreads entries, and in each piece
+// a token's first entry adds all of its own. (64 requests of 128000 tokens with
+// 20000 biases each: 561 us; each biased token going through the list by itself:
+// 44,000.)
+template <typename T, typename OT>
+__device__ __noinline__ void finish_many(const T* in, OT* out, int n, int v0, Penalty c,
+                                         const uint32_t* mask, const int32_t* told, int64_t n_told,
+                                         const int32_t* tokens, const float* values,
+                                         int64_t n_biases, const uint16_t* s_bits, int* s_token,
+                                         float* s_value, float* s_sum, int* s_warp, int* s_exact) {
+  static_assert(kListed >= kLogitThreads, "a piece of the list");
+  const int me = threadIdx.x;
+  for (int lo = 0; lo < n; lo += kMet) {
+    const int hi = min(lo + kMet, n);
+    for (int k = lo + me; k < hi; k += kLogitThreads) s_sum[k - lo] = 0.f;
+    int next = me < n_biases ? tokens[me] : -1;
+    for (int64_t k = me; k - me < n_biases; k += kLogitThreads) {
+      const unsigned at = (unsigned)next - (unsigned)(v0 + lo);
+      const bool mine = at < (unsigned)(hi - lo);
+      const float value = mine ? values[k] : 0.f;
+      next = k + kLogitThreads < n_biases ? tokens[k + kLogitThreads] : -1;
+      int total = 0;
+      const int place = list_places(mine, total, s_warp);
+      if (mine) s_token[place] = (int)at, s_value[place] = value;
+      __syncthreads();
+      if (me < total) {
+        const int t = s_token[me];
+        int j = 0;
+        while (s_token[j] != t) ++j;
+        if (j == me) {
+          float sum = s_sum[t];
+          for (; j < total; ++j)
+            if (s_token[j] == t) sum += s_value[j];
+          s_sum[t] = sum;
+        }
+      }
+    }
+    __syncthreads();
+    const auto finish = [&](int k, uint32_t w, int64_t count) {
+      float l = penalised(to_f32(in[k]), w & kSeen, count, c);
+      if (w & kBiased) l += s_sum[k - lo];
+      out[k] = from_f32<OT>(mask && !(mask[k / 32] >> (k % 32) & 1u) ? -INFINITY : l);
+    };
+    for (int k = lo + me; k < hi; k += kLogitThreads) {
+      const uint32_t w = s_bits[k];
+      if (w != 0 && (w & kCount) < kHeavy) finish(k, w, w & kCount);
+    }
+    if (n_told >= (int64_t)kHeavy)
+      for (int k = lo; k < hi; ++k) {
+        const uint32_t w = s_bits[k];
+        if ((w & kCount) < kHeavy) continue;
+        const int count = count_of(v0 + k, told, n_told, s_exact);
+        if (me == 0) finish(k, w, count);
+      }
+    __syncthreads();
+  }
+}
+
 // CTAs take (request, share of the vocabulary) pairs in turn; the next one's
 // parameters come into registers early and, where logits are loaded element by
 // element (VEC 1: the rows of out have other boundaries than those of the
@@ -228,24 +320,17 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitPerSm) logits_rows(LogitA
       const int v = on ? p.bias_tokens[k + me] : -1;
       const float value = on ? p.bias_values[k + me] : 0.f;
       const bool mine = v >= v0 && v < v0 + n;
-      const uint32_t m = __ballot_sync(0xffffffffu, mine);
-      if (lane == 0) s_warp[warp] = __popc(m);
       list_met(mine && mark(v - v0, kBiased), v - v0, &s_n, s_met);
-      __syncthreads();
-      int before = listed, total = 0;
-#pragma unroll
-      for (int w = 0; w < kLogitWarps; ++w) {
-        before += w < warp ? s_warp[w] : 0;
-        total += s_warp[w];
+      const int place = list_places(mine, listed, s_warp);
+      if (mine && place < kListed) {
+        s_token[place] = v;
+        s_value[place] = value;
       }
-      before += __popc(m & ((1u << lane) - 1));
-      if (mine && before < kListed) {
-        s_token[before] = v;
-        s_value[before] = value;
-      }
-      listed += total;
       if (k + kLogitThreads < q.b1) __syncthreads();
     }
+    // (told with the count: a branch on `listed` itself makes the compiler spill
+    // 260 bytes, and 256 x 128000 take 103 us for 74)
+    if (me == 0 && listed > kListed) atomicAdd(&s_n, kMany);
     __syncthreads();
     const int met = s_n;
     // A pair without met tokens has no further barrier, and a warp that is done
@@ -258,21 +343,17 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitPerSm) logits_rows(LogitA
       float l = penalised(to_f32(in[k]), w & kSeen, count, q.c);
       if (w & kBiased) {
         float sum = 0.f;
-        if (listed <= kListed) {
-          for (int j = 0; j < listed; ++j)
-            if (s_token[j] == v0 + k) sum += s_value[j];
-        } else {  // more than the compacted list holds: from the list itself
-          for (int64_t j = q.b0; j < q.b1; ++j)
-            if (p.bias_tokens[j] == v0 + k) sum += p.bias_values[j];
-        }
+        for (int j = 0; j < listed; ++j)
+          if (s_token[j] == v0 + k) sum += s_value[j];
         l += sum;
       }
       return mask && !(mask[k / 32] >> (k % 32) & 1u) ? -INFINITY : l;
     };
-    if (met > 0) {
+    if (met > 0 && met < kMany) {
       // Results of the met tokens: into the list's places or, where there are
       // more than it holds, straight into out, which the pass then leaves
-      // alone there. (out may be the logits themselves: they are read first.)
+      // alone there. (out may be the logits themselves: they are read first.
+      // Shares with more than kListed biases come after the pass.)
       for (int e = me; e < (kept ? met : n); e += kLogitThreads) {
         const int k = kept ? s_met[e] : e;
         const uint32_t w = bits_of(k);
@@ -288,17 +369,9 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitPerSm) logits_rows(LogitA
           const int k = kept ? s_met[e] : e;
           const uint32_t w = bits_of(k);
           if ((w & kCount) < kHeavy) continue;
-          __syncthreads();
-          if (me == 0) s_exact = 0;
-          __syncthreads();
-          int count = 0;
-          for (int64_t j = q.o0 + me; j < q.o1; j += kLogitThreads)
-            count += p.output_tokens[j] == v0 + k;
-          count = __reduce_add_sync(0xffffffffu, count);
-          if (lane == 0) atomicAdd(&s_exact, count);
-          __syncthreads();
+          const int count = count_of(v0 + k, p.output_tokens + q.o0, q.o1 - q.o0, &s_exact);
           if (me == 0) {
-            const float l = result(k, w, s_exact);
+            const float l = result(k, w, count);
             if (kept)
               s_result[e] = l;
             else
@@ -359,6 +432,11 @@ __global__ void __launch_bounds__(kLogitThreads, kLogitPerSm) logits_rows(LogitA
           reinterpret_cast<uint16_t*>(s_word)[s_met[e]] = 0;
         }
       } else {
+        if (met >= kMany)
+          finish_many(in, out, n, v0, q.c, mask, p.output_tokens + q.o0, q.o1 - q.o0,
+                      p.bias_tokens + q.b0, p.bias_values + q.b0, q.b1 - q.b0,
+                      reinterpret_cast<const uint16_t*>(s_word), s_token, s_value, s_result,
+                      s_warp, &s_exact);
         clear_table();
       }
       if (me == 0) s_n = 0;

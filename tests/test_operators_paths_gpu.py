@@ -521,3 +521,54 @@ def test_shared_elements_are_refused(spmv_lib):
             S.spmv_layernorm(x, None, None, y)
         with pytest.raises(S.SpmvError):
             S.spmv_logits_process(x, y)
+
+
+# --------------------------------------------------- logits: many biases
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("size", [(1, 32000, 32000), (2, 50257, 40000), (3, 20480, 3000), (5, 128000, 9000), (470, 2100, 900)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_logits_many_biases_keep_list_order(spmv_lib, size, in_place):
+    """More biases in a share than a block keeps, many of them repeated, some
+    in padding: each token's are added in list order in fp32, bit for bit."""
+    import numpy as np
+    n, v, k = size
+    g = gen(170 + v)
+    tok = torch.randint(0, v, (n, k), generator=g)
+    tok[:, ::9] = tok[:, 0:1]                       # one token in every piece of the list
+    tok[:, 1::50] = -1
+    tok[:, 2::50] = v
+    val = torch.randn(n, k, generator=g) * 10.0 ** torch.randint(-3, 4, (n, k), generator=g)
+    x = randn(g, n, v, std=3.0)
+    inside = ((tok >= 0) & (tok < v)).numpy()
+    sums = np.zeros((n, v), np.float32)
+    np.add.at(sums, (np.nonzero(inside)[0], tok.numpy()[inside]), val.numpy()[inside])
+    xd = x.to(DEV)
+    out = xd if in_place else torch.full_like(xd, float("nan"))
+    S.spmv_logits_process(xd, out, bias=(tok.reshape(-1).int().to(DEV), val.reshape(-1).to(DEV),
+                                         torch.arange(n + 1, device=DEV) * k))
+    met = torch.from_numpy(sums != 0)
+    ref = torch.where(met, x + torch.from_numpy(sums), x)
+    assert torch.equal(out.cpu(), ref)
+
+
+@pytest.mark.parametrize("types", ops.LOGIT_TYPES, ids=lambda p: "-".join(p))
+@pytest.mark.parametrize("size", [(2, 700, 600), (3, 5003, 2500)], ids=lambda s: "x".join(map(str, s)))
+def test_logits_many_biases_with_all_the_rest(spmv_lib, size, types):
+    """With penalties, masks, padding, and tokens whose counts pass the
+    table's bits, biased and not."""
+    n, v, k = size
+    g = gen(180 + v)
+    kw = ops.everything(g, n, v, 40, k, pad=True)
+    tok = torch.randint(0, v, (20000,), generator=g).int()
+    tok[:9000], tok[10000:19000] = 5, 77
+    kw["output"] = (tok, torch.tensor([0] * n + [20000]))
+    kw["frequency"] = kw["frequency"] * 0.01
+    bias = [t.clone() for t in kw["bias"]]
+    bias[2] = torch.cat([torch.zeros(1, dtype=torch.int64), torch.full((n,), k).cumsum(0)])
+    bias[0] = torch.randint(-1, v + 1, (n * k,), generator=g).int()
+    bias[0][-3] = 5
+    bias[0][bias[0] == 77] = 78
+    bias[1] = torch.randn(n * k, generator=g)
+    kw["bias"] = tuple(bias)
+    ops.check_logits(randn(g, n, v, dtype=types[0], std=3.0), types[1], **kw)

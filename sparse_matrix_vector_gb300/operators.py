@@ -49,10 +49,9 @@ def _check(status: int, where: str) -> None:
         raise SpmvError(status, where)
 
 
-def _fits(where: str, *sizes: int) -> None:
-    """Refuse sizes that the C call's 32-bit arguments would cut short."""
-    if max(sizes) > _INT32_MAX:
-        raise SpmvError(8, where)  # SPMV_ERR_TOO_LARGE
+def _too_large(where: str):
+    """Sizes that the C call's 32-bit arguments would cut short."""
+    raise SpmvError(8, where)  # SPMV_ERR_TOO_LARGE
 
 
 def _dtype(t, what: str) -> int:
@@ -161,7 +160,8 @@ def spmv_layernorm(x, weight, bias, y, eps: float = 1e-5, mean=None, rstd=None,
     n_y, d_y, ys = _rows(y, "y")
     if n_y != n or d_y != d:
         raise ValueError("x and y must have the same shape")
-    _fits("spmv_layernorm", d)
+    if d > _INT32_MAX:
+        _too_large("spmv_layernorm")
     dev = _same_device(x, y, weight, bias, mean, rstd)
     w, b, p = _params(weight, bias, d, "weight and bias")
     _check(_lib_handle().spmv_layernorm(
@@ -187,7 +187,8 @@ def spmv_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, works
     n_dy, d_dy, dys = _rows(dy, "dy")
     if n_dy != n or d_dy != d:
         raise ValueError("dy and x must have the same shape")
-    _fits("spmv_layernorm_backward", d)
+    if d > _INT32_MAX:
+        _too_large("spmv_layernorm_backward")
     code = _dtype(x, "x")
     dxs = 0
     if dx is not None:
@@ -238,7 +239,9 @@ def spmv_adapters_run(x, a, b, slot_ids, y, base=None, ranks=None, scales=None, 
     slots, rank, a_in = a.shape
     if a_in != n_in or tuple(b.shape) != (slots, n_out, rank):
         raise ValueError(f"a must be (slots, rank, {n_in}) and b (slots, {n_out}, rank)")
-    _fits("spmv_adapters_run", t, n_in, n_out, slots, rank)
+    if (t > _INT32_MAX or n_in > _INT32_MAX or n_out > _INT32_MAX or slots > _INT32_MAX
+            or rank > _INT32_MAX):
+        _too_large("spmv_adapters_run")
     if a.dtype != x.dtype or b.dtype != x.dtype:
         raise TypeError("a and b must have x's type")
     if not a.is_contiguous() or not b.is_contiguous():
@@ -291,7 +294,8 @@ def spmv_logits_process(logits, out, prompt=None, output=None, repetition=None, 
     n_o, v_o, out_stride = _rows(out, "out")
     if n_o != n or v_o != v:
         raise ValueError("logits and out must have the same shape")
-    _fits("spmv_logits_process", n, v)
+    if n > _INT32_MAX or v > _INT32_MAX:
+        _too_large("spmv_logits_process")
     p_tok, p_off = _list(prompt, n, "prompt")
     o_tok, o_off = _list(output, n, "output")
     b_tok = b_val = b_off = 0
@@ -305,7 +309,8 @@ def spmv_logits_process(logits, out, prompt=None, output=None, repetition=None, 
         n_masks, words, m_stride = _rows(mask, "mask")
         if words != (v + 31) // 32:
             raise ValueError(f"mask must have {(v + 31) // 32} words in a row")
-        _fits("spmv_logits_process", n_masks)
+        if n_masks > _INT32_MAX:
+            _too_large("spmv_logits_process")
         if mask_rows is None and n_masks < n:
             raise ValueError("mask must have a row for each request (or give mask_rows)")
         m_ptr = mask.data_ptr()

@@ -532,9 +532,9 @@ void spmv_plan_destroy(spmv_plan* plan);
  *     their element size; 16-byte aligned rows are the fastest.
  *   - Inputs and outputs share no element unless a call says so (column
  *     ranges of one matrix, or rows of it in turn, share none).
- *   - Sums, statistics and products are held in fp32, and each output is
- *     rounded to its type once. Runs are deterministic: the same inputs give
- *     the same bits.
+ *   - Sums, statistics and products are held in fp32 (one exception is
+ *     stated: spmv_adapters_run in fp16), and each output is rounded to its
+ *     type once. Runs are deterministic: the same inputs give the same bits.
  * ------------------------------------------------------------------------ */
 
 /* Layer norm of each row: with mean = sum_j x_j / n_cols and
@@ -596,7 +596,10 @@ int64_t spmv_adapters_workspace(int32_t n_tokens, int32_t n_slots, int32_t rank)
  * n_slots fp32 or NULL (1). base: n_tokens x n_out of y_dtype, the shared
  * projection's output (spmv_run's y of each token), or NULL (0); y: of
  * y_dtype, which is fp32 or `dtype`. y may be base itself (same pointer and
- * stride). A_s x_t and the product with B_s are held in fp32. workspace:
+ * stride). The sums of both products are held in fp32; between them an
+ * element of A_s x_t keeps fp32's 24 bits in bf16, and 22 in fp16 (down to
+ * 2^-38 of the token's largest finite element). A token's result does not
+ * depend on the order of the tokens. workspace:
  * 16-byte aligned device memory of at least spmv_adapters_workspace bytes
  * (NULL when that is 0); no initialisation, no meaning afterwards.
  * Errors: INVALID_ARG (sizes, null or misaligned pointers, strides,

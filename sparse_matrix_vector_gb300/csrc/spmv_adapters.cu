@@ -14,14 +14,17 @@
 //
 // Measured at 12288 x 12288, fp16 x, fp32 base and y, in us and as a share of
 // the 6.79 TB/s of a plain copy: 4096 tokens of 8 adapters at rank 32 117
-// (0.65; some 60 of them the second product, at 0.99, 35 the first), 1024
-// tokens 51 (0.40); 48 tokens of 32 adapters at rank 64 34 (0.37); one token
-// at rank 16 10. Few tokens are bound by latency: two products one after the
-// other, two trips to memory and a cluster's barrier between them.
+// (0.65; the second product 74, at 0.81; the first 32, whose eight warps per SM
+// wait for loads to registers; the sort 6), at rank 64 154 (0.51), 1024 tokens
+// at rank 16 46 (0.42); 48 tokens of 32 adapters at rank 64 34 (0.37); one
+// token at rank 16 10. Few tokens are bound by latency: two products one after
+// the other, two trips to memory and a cluster's barrier between them.
 //
 // h is kept in fp32 and enters the second product as a sum of 16-bit terms:
-// two fp16 terms after scaling each token's h by a power of two (22 bits
-// below its largest element), or three bf16 terms (24 bits).
+// three bf16 terms (24 bits of each element), or two fp16 terms (22 bits, down
+// to 2^-38 of the token's largest element) after scaling the token's h by a
+// power of two. A third fp16 term would be half as many instructions again,
+// for an error that the products' own fp32 sums exceed.
 #include <cooperative_groups.h>
 
 #include <climits>

@@ -13,8 +13,8 @@
 // biases 75 us, 0.53 of the 6.79 TB/s of a plain copy; with empty lists 50
 // (0.77). A share's lists are a chain of waits (entries, atomics on the table,
 // the listed logits) of some 6 us in each of four rounds of shares, which the
-// SM's other two CTAs hide in part. 32000 of one request: 7.9 us, of which a
-// launch is 4.
+// SM's other two CTAs hide in part. 32000 of one request: 8.0 us, of which a
+// launch is 4. Shares with more than kListed biases take longer (finish_many).
 #include <climits>
 #include <type_traits>
 
@@ -184,10 +184,10 @@ __device__ __forceinline__ int list_places(bool mine, int& listed, int* s_warp) 
 // The met tokens of a share with more biases than are kept, which the pass has
 // left alone, straight into out (a call of its own: inlined, its registers
 // would be taken from the pass). kMet tokens at a time, first the sums of their
-// biases, each token's in list order: the list goes by in pieces of kLogitThreads entries, and in each piece
-// a token's first entry adds all of its own. (64 requests of 128000 tokens with
-// 20000 biases each: 561 us; each biased token going through the list by itself:
-// 44,000.)
+// biases, each token's in list order: the list goes by in pieces of
+// kLogitThreads entries, and in each piece a token's first entry adds all of its
+// own. (64 requests of 128000 tokens with 3000 biases each 117 us, with 20000
+// 561; each biased token going through the list by itself: 230 and 44,000.)
 template <typename T, typename OT>
 __device__ __noinline__ void finish_many(const T* in, OT* out, int n, int v0, Penalty c,
                                          const uint32_t* mask, const int32_t* told, int64_t n_told,

@@ -660,6 +660,130 @@ typedef struct spmv_logits {
  * offsets, strides, overlaps), UNSUPPORTED (types), CUDA. */
 spmv_status spmv_logits_process(const spmv_logits* args, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A pruned model beside the dense one that it came from: products with 4-bit
+ * weights (the other way to make a layer small, for the layers that pruning
+ * would hurt), the verification of tokens that the pruned model drafted, and
+ * the distillation from the dense model that recovers it. The conventions
+ * are those of the section above.
+ * ------------------------------------------------------------------------ */
+
+/* Products of a few tokens with 4-bit weights:
+ *   y_t = base_t + W x_t,
+ *   W[o, i] = scale[o, i / group] * (q[o, i] - zero[o, i / group]).
+ * x: n_tokens x n_in of `dtype` (fp16 or bf16). weights: n_out rows of
+ * (n_in + 1) / 2 bytes, weights_stride bytes apart; column i of a row is the
+ * low (i even) or high (i odd) half of byte i / 2, 0 to 15 (an odd n_in
+ * leaves the last half unused). Rows at 16-byte boundaries are the fastest.
+ * scales: n_out x groups of scales_dtype (fp32 or `dtype`), groups =
+ * ceil(n_in / group), contiguous; zeros: the same of bytes, whose low four
+ * bits count, or NULL (8). group: a power of two from 32 on, or any number
+ * from n_in on (one group). base: n_tokens x n_out of y_dtype, or NULL (0); y: of
+ * y_dtype, which is fp32 or `dtype`. y may be base itself (same pointer and
+ * stride). q - zero is exact, and a group's products are summed in fp32
+ * before they are scaled. A token's result does not depend on the other
+ * tokens' values, but it may differ in the order of its sums with n_tokens.
+ * Errors: INVALID_ARG (sizes, null or misaligned
+ * pointers, strides, overlaps), UNSUPPORTED (types, group), TOO_LARGE (more
+ * than 2^18 tokens, n_in or n_out above 2^30), CUDA. */
+spmv_status spmv_int4_run(int32_t n_tokens, int32_t n_in, int32_t n_out, int32_t group,
+                          spmv_dtype dtype, const void* x, int64_t x_stride,
+                          const uint8_t* weights, int64_t weights_stride, const void* scales,
+                          spmv_dtype scales_dtype, const uint8_t* zeros, const void* base,
+                          int64_t base_stride, void* y, spmv_dtype y_dtype, int64_t y_stride,
+                          void* stream);
+
+/* Bytes of workspace that spmv_verify_drafts needs for these sizes (0 for
+ * sizes it refuses). */
+int64_t spmv_verify_workspace(int32_t n_requests, int32_t n_drafts, int32_t vocab);
+
+/* Verification of drafted tokens. Request i has the drafted tokens
+ * draft_tokens[offsets[i] .. offsets[i + 1]) (offsets: n_requests + 1
+ * non-decreasing int64 on the device, from 0 to at most n_drafts), and one row
+ * more of the target's logits than it has drafts: rows offsets[i] + i on of
+ * `target` ((n_drafts + n_requests) x vocab of `dtype`), the row at place j
+ * being what the target says once the first j drafts stand. draft: the
+ * drafter's logits of each drafted token (n_drafts x vocab of `dtype`), or
+ * NULL where drafts carry no probabilities (q is then 1 at the draft).
+ * With p = softmax(target / temperature[i]) and q = softmax(draft /
+ * temperature[i]), draft x at place j is accepted where
+ *   accept_uniforms[offsets[i] + j] * q(x) < p(x);
+ * at the first draft that is not accepted, a token is drawn from
+ * max(p - q, 0) (from p where that is 0 everywhere), and behind the last one,
+ * if all are accepted, from p: the first token in the vocabulary's order
+ * whose running sum is above sample_uniforms[i] times the whole sum. A
+ * temperature of 0 (or below, or NaN) is greedy: a draft is accepted where it
+ * is the target's largest token (the lowest of equals), which is also the
+ * token taken; the random numbers are not used. temperature: n_requests fp32, or
+ * NULL (1); others are held within [1e-30, 1e30].
+ * tokens: n_drafts + n_requests int32; request i's, from offsets[i] + i on,
+ * are its accepted drafts, the token drawn, and -1 to its end. accepted:
+ * n_requests int32, the drafts accepted. Rows behind the last request are
+ * neither read nor written.
+ * Uniforms are in [0, 1). Logits that are NaN count as minus infinity, plus
+ * infinity as the largest fp32; a probability below 2^-126 of its row's
+ * largest counts as 0. A drafted token outside [0, vocab) is not accepted. A
+ * request whose row to draw from has nothing above minus infinity gets -1.
+ * Decisions are made in 64 bits' worth where fp32's roundings could change
+ * them (relative errors of some 2^-38 remain).
+ * workspace: 16-byte aligned device memory of at least spmv_verify_workspace
+ * bytes; no initialisation, no meaning afterwards.
+ * Errors: INVALID_ARG (sizes, null or misaligned pointers, strides, overlaps,
+ * workspace), TOO_LARGE (vocab above 2^31 - 4097, too many rows), CUDA. */
+spmv_status spmv_verify_drafts(int32_t n_requests, int32_t n_drafts, int32_t vocab,
+                               spmv_dtype dtype, const void* target, int64_t target_stride,
+                               const void* draft, int64_t draft_stride,
+                               const int32_t* draft_tokens, const int64_t* offsets,
+                               const float* accept_uniforms, const float* sample_uniforms,
+                               const float* temperature, int32_t* tokens, int32_t* accepted,
+                               void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Largest number of a teacher's logits per row of spmv_distill. */
+#define SPMV_DISTILL_MAX_TOP 1024
+
+/* Distillation from a teacher's top logits. For each row, with q =
+ * softmax(logits / temperature) over the vocabulary and t the teacher's logits
+ * of the listed tokens:
+ *   p_j = exp(t_j / temperature) / sum over the listed, or, with log_sums,
+ *   p_j = exp(t_j / temperature - log_sums[row]), whose rest
+ *   r_p = max(0, 1 - sum_j p_j) stands against r_q, the sum of q over all
+ *   tokens that are not listed (r_p counts as 0 where every token is):
+ *   loss = sum_j p_j (log p_j - log q_j) + r_p (log r_p - log r_q),
+ * terms with p_j = 0 or r_p = 0 being 0. (Without log_sums r_p is 0.)
+ * logits: n_rows x vocab of `dtype` (any type). top_tokens: n_rows x top
+ * int32; entries outside [0, vocab) list nothing, so rows may be padded with
+ * -1. A token listed twice counts with both entries (and once in r_q).
+ * top_logits: n_rows x top of top_dtype (any type). log_sums: n_rows fp32 or NULL, the
+ * logarithm of the teacher's sum of exp(t / temperature) over its vocabulary.
+ * loss: n_rows fp32. stats: n_rows x 3 fp32, or NULL: what the gradient needs
+ * of each row: its largest logit m, sum of exp((logit - m) / temperature),
+ * and that over the tokens not listed (0 without log_sums). A row at which
+ * nothing is listed (or, without log_sums, nothing above minus infinity) is
+ * not read: its loss and stats are 0.
+ * Errors: INVALID_ARG (sizes, null or misaligned pointers, strides, overlaps,
+ * temperature not positive and finite), TOO_LARGE (top above the limit, more
+ * than 2^27 rows, vocab above 2^31 - 4097), CUDA. */
+spmv_status spmv_distill(int64_t n_rows, int32_t vocab, const void* logits, spmv_dtype dtype,
+                         int64_t stride, int32_t top, const int32_t* top_tokens,
+                         int64_t tokens_stride, const void* top_logits, spmv_dtype top_dtype,
+                         int64_t top_stride, const float* log_sums, float temperature,
+                         float* loss, float* stats, void* stream);
+
+/* Gradient of spmv_distill: per row, with g = dloss / temperature,
+ *   dlogits_v = g (q_v - p_v) for listed tokens (p_v the sum of a token's entries),
+ *   dlogits_v = g q_v (1 - r_p / r_q) for the others (r_p = 0 without log_sums),
+ * and 0 for a row at which nothing is listed. dloss: n_rows fp32, dloss_stride
+ * elements apart (0: one for all). stats: the forward call's. dlogits: of
+ * `dtype`, overwritten; it may be logits itself (same pointer and stride).
+ * Errors: as spmv_distill. */
+spmv_status spmv_distill_backward(int64_t n_rows, int32_t vocab, const float* dloss,
+                                  int64_t dloss_stride, const void* logits, spmv_dtype dtype,
+                                  int64_t stride, int32_t top, const int32_t* top_tokens,
+                                  int64_t tokens_stride, const void* top_logits,
+                                  spmv_dtype top_dtype, int64_t top_stride,
+                                  const float* log_sums, float temperature, const float* stats,
+                                  void* dlogits, int64_t dlogits_stride, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,6 +20,7 @@ SPMV_FORMAT_DELTA_AUTO, SPMV_FORMAT_SELL, SPMV_FORMAT_AUTO, SPMV_FORMAT_FEM = 4,
 SPMV_SELL_C = 32
 SPMV_DELTA_FEWEST_BYTES, SPMV_DELTA_SPARSITY_TABLE = 0, 1
 SPMV_ADAPTER_MAX_RANK, SPMV_ADAPTER_MAX_SLOTS = 256, 16384
+SPMV_DISTILL_MAX_TOP = 1024
 
 STATUS_NAMES = {
     0: "SPMV_OK", 1: "SPMV_ERR_INVALID_ARG", 2: "SPMV_ERR_BAD_ROW_PTR",
@@ -148,6 +149,19 @@ SIGNATURES = {
                                          c_i64, c_p, c_p, c_p, c_p, c_p, c_p, c_i64, c_p,
                                          ctypes.c_int, c_i64, c_p, c_i64, c_p]),
     "spmv_logits_process": (ctypes.c_int, [ctypes.POINTER(spmv_logits), c_p]),
+    "spmv_int4_run": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i32, ctypes.c_int, c_p, c_i64, c_p,
+                                     c_i64, c_p, ctypes.c_int, c_p, c_p, c_i64, c_p, ctypes.c_int,
+                                     c_i64, c_p]),
+    "spmv_verify_workspace": (c_i64, [c_i32, c_i32, c_i32]),
+    "spmv_verify_drafts": (ctypes.c_int, [c_i32, c_i32, c_i32, ctypes.c_int, c_p, c_i64, c_p,
+                                          c_i64, c_p, c_p, c_p, c_p, c_p, c_p, c_p, c_p, c_i64,
+                                          c_p]),
+    "spmv_distill": (ctypes.c_int, [c_i64, c_i32, c_p, ctypes.c_int, c_i64, c_i32, c_p, c_i64,
+                                    c_p, ctypes.c_int, c_i64, c_p, ctypes.c_float, c_p, c_p,
+                                    c_p]),
+    "spmv_distill_backward": (ctypes.c_int, [c_i64, c_i32, c_p, c_i64, c_p, ctypes.c_int, c_i64,
+                                             c_i32, c_p, c_i64, c_p, ctypes.c_int, c_i64, c_p,
+                                             ctypes.c_float, c_p, c_p, c_i64, c_p]),
 }
 
 _lock = threading.Lock()

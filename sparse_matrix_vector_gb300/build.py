@@ -2,7 +2,8 @@
 
 The translation units (host planner and converters, CSR tile kernel, CSR
 segment kernel, DELTA kernel, sliced-ELL kernel, matrix-free FEM kernel,
-conjugate-gradient kernels, allocation-free entry point; layer norm, adapters, logits) are
+conjugate-gradient kernels, allocation-free entry point; layer norm, adapters, logits, 4-bit products,
+verification of drafts, distillation) are
 compiled in parallel with nvcc and linked into one shared object next to this file.
 Usage: ``python -m sparse_matrix_vector_gb300.build`` or ``build_library()``.
 """
@@ -23,7 +24,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["spmv_host.cpp", "spmv_csr.cu", "spmv_csr_seg.cu", "spmv_delta.cu", "spmv_sell.cu",
            "spmv_fem.cu", "spmv_pcg.cu", "spmv_noalloc.cu", "spmv_layernorm.cu", "spmv_adapters.cu",
-           "spmv_logits.cu"]
+           "spmv_logits.cu", "spmv_int4.cu", "spmv_verify.cu", "spmv_distill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-Wall", "--expt-relaxed-constexpr"]

@@ -1,0 +1,462 @@
+// Distillation from a teacher's top logits and its gradient (spmv_distill,
+// spmv_distill_backward): per row, with a = logits / T, q = softmax(a) and p
+// the teacher's probabilities of the listed tokens,
+//   loss = sum_j p_j (log p_j - log q_j) [+ r_p (log r_p - log r_q)],
+// r the probability of all tokens that are not listed. Forward, the row is
+// read once: largest logit and sum of exponentials as it passes (a bit per
+// token marks the listed ones where r_q is wanted: as 1 - sum q_j it would
+// keep no digits once the student agrees with the teacher). Backward, each
+// logit becomes its gradient as it passes, and the listed tokens are put
+// right after it. Both are bound by those bytes.
+#include <cooperative_groups.h>
+
+#include <climits>
+
+#include "spmv_device.cuh"
+#include "spmv_softmax.cuh"
+#include "spmv_types.cuh"
+
+namespace spmv {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kDistillThreads = 256;
+constexpr int kDistillAtOnce = 4;
+constexpr int kMaxCluster = 8;
+constexpr int kChunk = 128 * 1024;       // tokens whose marks a CTA holds at a time
+constexpr int kHash = 2 * SPMV_DISTILL_MAX_TOP;
+
+struct DistillArgs {
+  int n_rows, vocab, top;
+  int dtype_top;
+  const void* logits;
+  int64_t stride;
+  const int32_t* tokens;
+  int64_t tokens_stride;
+  const void* top_logits;
+  int64_t top_stride;
+  const float* log_sums;
+  float temperature, c;  // c: log2(e) / temperature
+  float* loss;
+  float* stats;
+  // backward
+  const float* dloss;
+  int64_t dloss_stride;
+  void* dlogits;
+  int64_t out_stride;
+  int shares, share;     // CTAs of a row, and tokens of each
+};
+
+// The teacher's side of a row, in shared memory: listed tokens (-1: none) and
+// the logarithms of their probabilities.
+struct Teacher {
+  int id[SPMV_DISTILL_MAX_TOP];
+  float log_p[SPMV_DISTILL_MAX_TOP];
+  MaxSum red[kDistillThreads / 32];
+  float sums[kDistillThreads / 32];
+  int any, repeats;
+};
+
+// Sum over the CTA in a fixed order, for all threads.
+__device__ __forceinline__ float sum_cta(float v, float* s_red) {
+  v = warp_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float t = 0.f;
+#pragma unroll
+  for (int w = 0; w < kDistillThreads / 32; ++w) t += s_red[w];
+  return t;
+}
+
+// Fill `t` from row i. False if nothing is listed there (or, where the
+// probabilities are those of the listed tokens alone, nothing above minus
+// infinity). *rest: the teacher's probability of what is not listed.
+__device__ __forceinline__ bool load_teacher(const DistillArgs& a, int64_t i, Teacher& t, float* rest) {
+  const int me = threadIdx.x;
+  const int32_t* ids = a.tokens + i * a.tokens_stride;
+  if (me == 0) t.any = t.repeats = 0;
+  __syncthreads();
+  MaxSum x = MaxSum::none();
+  bool any = false;
+  for (int j = me; j < a.top; j += kDistillThreads) {
+    const int id = ids[j];
+    const bool valid = (unsigned)id < (unsigned)a.vocab;
+    t.id[j] = valid ? id : -1;
+    const float l = valid ? load_as_f32(a.top_logits, a.dtype_top, i * a.top_stride + j) : -INFINITY;
+    t.log_p[j] = l;
+    any |= valid;
+    if (valid) {
+      x.raise(l, a.c);
+      x.s += exp2_fast((l - x.m) * a.c);
+    }
+  }
+  if (any) t.any = 1;
+  x = join_cta<kDistillThreads>(x, a.c, t.red);
+  *rest = 0.f;
+  if (!t.any || (!a.log_sums && x.s == 0.f)) return false;
+  // log p_j = (l_j - largest) / T + shift
+  float shift;
+  if (a.log_sums) {
+    shift = x.s == 0.f ? 0.f : (float)((double)x.m / (double)a.temperature - (double)a.log_sums[i]);
+    const float left = 1.f - x.s * expf(shift);
+    *rest = left > 0.f || left != left ? left : 0.f;
+  } else {
+    shift = -logf(x.s);
+  }
+  for (int j = me; j < a.top; j += kDistillThreads)
+    t.log_p[j] = t.id[j] < 0 ? -INFINITY : (t.log_p[j] - x.m) / a.temperature + shift;
+  __syncthreads();
+  return true;
+}
+
+// Whether a token is listed twice, by a table of the tokens (t.repeats; all
+// threads, behind a barrier on entry and one on return). `table` has kHash
+// words.
+__device__ __forceinline__ void find_repeats(const DistillArgs& a, Teacher& t, int* table) {
+  for (int k = threadIdx.x; k < kHash; k += kDistillThreads) table[k] = -1;
+  __syncthreads();
+  for (int j = threadIdx.x; j < a.top; j += kDistillThreads) {
+    const int id = t.id[j];
+    if (id < 0) continue;
+    // (at most half of the table is ever taken)
+    for (unsigned at = (unsigned)id * 2654435761u >> 16;; ++at) {
+      const int was = atomicCAS(&table[at % kHash], -1, id);
+      if (was == -1) break;
+      if (was == id) {
+        t.repeats = 1;
+        break;
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// Whether entry j is its token's first.
+__device__ __forceinline__ bool is_first(const Teacher& t, int j) {
+  if (t.repeats)
+    for (int i = 0; i < j; ++i)
+      if (t.id[i] == t.id[j]) return false;
+  return true;
+}
+
+template <typename T, bool REST>
+__global__ void __launch_bounds__(kDistillThreads, 4) distill_rows(DistillArgs a) {
+  extern __shared__ uint32_t s_marks[];  // REST: a bit per token of a chunk
+  __shared__ Teacher t;
+  __shared__ MaxSum s_share;
+  __shared__ int s_table[REST ? kHash : 1];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int shares = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int64_t i = blockIdx.x / shares;
+  const int me = threadIdx.x;
+  float rest;
+  if (!load_teacher(a, i, t, &rest)) {  // (the same in the whole cluster)
+    if (rank == 0 && me == 0) {
+      a.loss[i] = 0.f;
+      if (a.stats) a.stats[3 * i] = a.stats[3 * i + 1] = a.stats[3 * i + 2] = 0.f;
+    }
+    return;
+  }
+  const T* row = static_cast<const T*>(a.logits) + i * a.stride;
+  const int64_t lo = (int64_t)rank * a.share, hi = min((int64_t)a.vocab, lo + a.share);
+  MaxSum x = MaxSum::none();
+  if constexpr (REST) {
+    if (rank == 0) find_repeats(a, t, s_table);
+    for (int64_t v0 = lo; v0 < hi; v0 += kChunk) {
+      const int n = (int)min((int64_t)kChunk, hi - v0);
+      const int head = units_of(row + v0, n).head;
+      // bit (v - v0 - head) + 8 of the marks: units start at whole bytes
+      for (int k = me; k < (n + 8 + 31) / 32; k += kDistillThreads) s_marks[k] = 0;
+      __syncthreads();
+      for (int j = me; j < a.top; j += kDistillThreads) {
+        const int64_t at = (int64_t)t.id[j] - v0;
+        if (at >= 0 && at < n) {
+          const int bit = (int)at - head + 8;
+          atomicOr(&s_marks[bit >> 5], 1u << (bit & 31));
+        }
+      }
+      __syncthreads();
+      const uint8_t* marks = reinterpret_cast<const uint8_t*>(s_marks);
+      for_units<kDistillThreads, kDistillAtOnce>(row + v0, n, [&](int at, float (&v)[kUnit]) {
+        // (the head's unit has its first token at bit 8 - head)
+        uint32_t m = at == 0 && head > 0 ? (uint32_t)marks[0] >> (8 - head)
+                                         : (uint32_t)marks[((at - head) >> 3) + 1];
+        if (m) {
+#pragma unroll
+          for (int k = 0; k < kUnit; ++k)
+            if (m >> k & 1) v[k] = -INFINITY;
+        }
+        x.add(v, a.c);
+      });
+      __syncthreads();
+    }
+  } else {
+    for_units<kDistillThreads, kDistillAtOnce>(row + lo, (int)(hi > lo ? hi - lo : 0),
+                                               [&](int, float (&v)[kUnit]) { x.add(v, a.c); });
+  }
+  __syncthreads();
+  x = join_cta<kDistillThreads>(x, a.c, t.red);
+  if (shares > 1) {
+    if (me == 0) s_share = x;
+    cluster.sync();
+    if (rank == 0)
+      for (int r = 1; r < shares; ++r) x.join(*cluster.map_shared_rank(&s_share, r), a.c);
+    cluster.sync();
+    if (rank != 0) return;
+  }
+  // the listed tokens: their logits, in the order of the list
+  MaxSum whole = x;
+  int distinct = 0;
+  if constexpr (REST) {
+    MaxSum y = MaxSum::none();
+    for (int j = me; j < a.top; j += kDistillThreads)
+      if (t.id[j] >= 0 && is_first(t, j)) {
+        const float z = to_f32(row[t.id[j]]);
+        y.raise(z, a.c);
+        y.s += exp2_fast((z - y.m) * a.c);
+        ++distinct;
+      }
+    __syncthreads();
+    y = join_cta<kDistillThreads>(y, a.c, t.red);
+    whole.join(y, a.c);
+    x.raise(whole.m, a.c);
+  }
+  const float log_sum = logf(whole.s);
+  float loss = 0.f;
+  for (int j = me; j < a.top; j += kDistillThreads) {
+    const float lp = t.log_p[j];
+    if (t.id[j] < 0 || lp == -INFINITY) continue;
+    const float lq = (to_f32(row[t.id[j]]) - whole.m) / a.temperature - log_sum;
+    loss += expf(lp) * (lp - lq);
+  }
+  loss = sum_cta(loss, t.sums);
+  if constexpr (REST) {
+    // (nothing is left where every token is listed)
+    const int all = (int)sum_cta((float)distinct, t.sums);
+    if (all < a.vocab && !(rest == 0.f)) loss += rest * (logf(rest) - (logf(x.s) - log_sum));
+  }
+  if (me == 0) {
+    a.loss[i] = loss;
+    if (a.stats) {
+      a.stats[3 * i] = whole.s == 0.f ? -INFINITY : whole.m;
+      a.stats[3 * i + 1] = whole.s;
+      a.stats[3 * i + 2] = REST ? x.s : 0.f;
+    }
+  }
+}
+
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(kDistillThreads, 4) distill_grad_rows(DistillArgs a) {
+  __shared__ Teacher t;
+  __shared__ int s_table[kHash];
+  __shared__ float s_z[SPMV_DISTILL_MAX_TOP];
+  const int64_t i = blockIdx.x / a.shares;
+  const int rank = (int)(blockIdx.x - i * a.shares), me = threadIdx.x;
+  const int64_t lo = (int64_t)rank * a.share;
+  const int n = (int)min((int64_t)a.vocab - lo, (int64_t)a.share);
+  const T* row = static_cast<const T*>(a.logits) + i * a.stride;
+  T* out = static_cast<T*>(a.dlogits) + i * a.out_stride;
+  float rest;
+  const bool any = load_teacher(a, i, t, &rest);
+  float m = 0.f, scale = 0.f, inv = 0.f, g = 0.f;
+  if (any) {
+    m = a.stats[3 * i];
+    const float sum = a.stats[3 * i + 1], left = a.stats[3 * i + 2];
+    g = a.dloss[i * a.dloss_stride] / a.temperature;
+    inv = 1.f / sum;
+    scale = inv * g;
+    if (a.log_sums && left != 0.f) scale *= 1.f - rest * sum / left;
+    find_repeats(a, t, s_table);
+    for (int j = me; j < a.top; j += kDistillThreads) {
+      const int64_t at = (int64_t)t.id[j] - lo;
+      s_z[j] = at >= 0 && at < n ? to_f32(row[t.id[j]]) : 0.f;
+    }
+    __syncthreads();  // (the row may be overwritten from here on)
+  }
+  const auto gradient = [&](float z) { return any ? exp2_fast((z - m) * a.c) * scale : 0.f; };
+  if constexpr (ALIGNED) {
+    const Units u = units_of(row + lo, n);
+    const T* body = row + lo + u.head;
+    T* to = out + lo + u.head;
+    for (int k = me; k < u.units; k += kDistillAtOnce * kDistillThreads) {
+      Pack<T, kUnit> r[kDistillAtOnce];
+      if (any) {
+#pragma unroll
+        for (int h = 0; h < kDistillAtOnce; ++h)
+          if (k + h * kDistillThreads < u.units)
+            r[h] = load_pack<T, kUnit>(body + (int64_t)(k + h * kDistillThreads) * kUnit, true);
+      }
+#pragma unroll
+      for (int h = 0; h < kDistillAtOnce; ++h)
+        if (k + h * kDistillThreads < u.units) {
+          Pack<T, kUnit> o;
+#pragma unroll
+          for (int e = 0; e < kUnit / 2; ++e) {
+            float2 z = make_float2(0.f, 0.f);
+            if (any) z = pair_f32(r[h], e);
+            set_pair(o, e, make_float2(gradient(z.x), gradient(z.y)));
+          }
+          store_pack<T, kUnit>(to + (int64_t)(k + h * kDistillThreads) * kUnit, o);
+        }
+    }
+    const int edge = me < u.head ? me : me >= 8 && me - 8 < u.tail ? u.head + u.units * kUnit + me - 8 : -1;
+    if (edge >= 0) out[lo + edge] = from_f32<T>(gradient(any ? to_f32(row[lo + edge]) : 0.f));
+  } else {
+    for (int k = me; k < n; k += kDistillThreads)
+      out[lo + k] = from_f32<T>(gradient(any ? to_f32(row[lo + k]) : 0.f));
+  }
+  if (!any) return;
+  __syncthreads();  // (the listed tokens are written again)
+  for (int j = me; j < a.top; j += kDistillThreads) {
+    const int64_t at = (int64_t)t.id[j] - lo;
+    if (at < 0 || at >= n || !is_first(t, j)) continue;
+    float p = expf(t.log_p[j]);
+    if (t.repeats)
+      for (int k = j + 1; k < a.top; ++k)
+        if (t.id[k] == t.id[j]) p += expf(t.log_p[k]);
+    out[t.id[j]] = from_f32<T>((exp2_fast((s_z[j] - m) * a.c) * inv - p) * g);
+  }
+}
+
+constexpr int kWave = 4 * 152;  // CTAs that the device's SMs hold at a time
+constexpr int kLeastShare = 2048;
+
+// CTAs of a row: one, or enough for half of the device's room where rows are few.
+int shares_of(int64_t rows, int vocab, int most) {
+  int64_t s = kWave / 2 / rows, room = (vocab + kLeastShare - 1ll) / kLeastShare;
+  s = s < room ? s : room;
+  s = s < most ? s : most;
+  return s < 1 ? 1 : (int)s;
+}
+
+// Shares are whole units, so that all but the first start like the row.
+int share_of(int vocab, int shares) {
+  return (int)((((int64_t)vocab + shares - 1) / shares + 63) / 64 * 64);
+}
+
+template <typename T>
+spmv_status launch_rows(DistillArgs a, cudaStream_t st) {
+  int c = shares_of(a.n_rows, a.vocab, kMaxCluster);
+  while (c & (c - 1)) c &= c - 1;  // (a power of two)
+  a.shares = c;
+  a.share = share_of(a.vocab, c);
+  const void* fn = a.log_sums ? reinterpret_cast<const void*>(&distill_rows<T, true>)
+                              : reinterpret_cast<const void*>(&distill_rows<T, false>);
+  const size_t smem = a.log_sums ? ((size_t)(a.share < kChunk ? a.share : kChunk) + 8 + 31) / 32 * 4 : 0;
+  if (!allow_smem(fn, smem)) return SPMV_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.n_rows * (unsigned)c);
+  cfg.blockDim = dim3(kDistillThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)c;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* args[] = {&a};
+  return status_of(cudaLaunchKernelExC(&cfg, fn, args));
+}
+
+template <typename T>
+spmv_status launch_grad(DistillArgs a, cudaStream_t st) {
+  a.shares = shares_of(a.n_rows, a.vocab, 1 << 16);
+  a.share = share_of(a.vocab, a.shares);
+  a.shares = (int)(((int64_t)a.vocab + a.share - 1) / a.share);
+  // rows whose 16-byte boundaries are at the same tokens in both matrices
+  const bool vec = ((reinterpret_cast<uintptr_t>(a.logits) - reinterpret_cast<uintptr_t>(a.dlogits)) & 15u) == 0 &&
+                   (a.n_rows == 1 || ((a.stride - a.out_stride) * (int64_t)sizeof(T)) % 16 == 0);
+  const void* fn = vec ? reinterpret_cast<const void*>(&distill_grad_rows<T, true>)
+                       : reinterpret_cast<const void*>(&distill_grad_rows<T, false>);
+  void* args[] = {&a};
+  return status_of(cudaLaunchKernel(fn, dim3((unsigned)(a.n_rows * a.shares)), dim3(kDistillThreads), args, 0, st));
+}
+
+// What both directions check and fill in.
+spmv_status take(DistillArgs& a, int64_t n_rows, int32_t vocab, const void* logits, spmv_dtype dtype,
+                 int64_t stride, int32_t top, const int32_t* tokens, int64_t tokens_stride,
+                 const void* top_logits, spmv_dtype top_dtype, int64_t top_stride, const float* log_sums,
+                 float temperature) {
+  if (n_rows < 0 || vocab < 1 || top < 0 || !op_dtype(dtype) || !op_dtype(top_dtype)) return SPMV_ERR_INVALID_ARG;
+  if (!(temperature > 0.f) || !std::isfinite(temperature)) return SPMV_ERR_INVALID_ARG;
+  const float c = (float)(1.4426950408889634 / (double)temperature);
+  if (!(c > 0.f) || !std::isfinite(c)) return SPMV_ERR_INVALID_ARG;
+  if (top > SPMV_DISTILL_MAX_TOP || n_rows > (1 << 27) || vocab > INT_MAX - 4096) return SPMV_ERR_TOO_LARGE;
+  if (!matrix_ok(logits, n_rows, vocab, stride, op_dtype_size(dtype), false) ||
+      !matrix_ok(tokens, n_rows, top, tokens_stride, 4, false) ||
+      !matrix_ok(top_logits, n_rows, top, top_stride, op_dtype_size(top_dtype), false) || !aligned_to(log_sums, 4))
+    return SPMV_ERR_INVALID_ARG;
+  a.n_rows = (int)n_rows, a.vocab = vocab, a.top = top, a.dtype_top = top_dtype;
+  a.logits = logits, a.stride = stride, a.tokens = tokens, a.tokens_stride = tokens_stride;
+  a.top_logits = top_logits, a.top_stride = top_stride, a.log_sums = log_sums;
+  a.temperature = temperature, a.c = c;
+  return SPMV_OK;
+}
+
+}  // namespace
+}  // namespace spmv
+
+using namespace spmv;
+
+extern "C" spmv_status spmv_distill(int64_t n_rows, int32_t vocab, const void* logits, spmv_dtype dtype,
+                                    int64_t stride, int32_t top, const int32_t* top_tokens,
+                                    int64_t tokens_stride, const void* top_logits, spmv_dtype top_dtype,
+                                    int64_t top_stride, const float* log_sums, float temperature, float* loss,
+                                    float* stats, void* stream) {
+  DistillArgs a{};
+  const spmv_status s = take(a, n_rows, vocab, logits, dtype, stride, top, top_tokens, tokens_stride, top_logits,
+                             top_dtype, top_stride, log_sums, temperature);
+  if (s != SPMV_OK) return s;
+  if ((n_rows > 0 && !loss) || !aligned_to(loss, 4) || !aligned_to(stats, 4)) return SPMV_ERR_INVALID_ARG;
+  if (n_rows == 0) return SPMV_OK;
+  const int64_t xs = op_dtype_size(dtype), ts = op_dtype_size(top_dtype);
+  const void* outs[] = {loss, stats};
+  for (int k = 0; k < 2; ++k) {
+    const int64_t cols = k == 0 ? 1 : 3;
+    if (spans_overlap(logits, n_rows, vocab, stride, xs, outs[k], n_rows, cols, cols, 4) ||
+        spans_overlap(top_tokens, n_rows, top, tokens_stride, 4, outs[k], n_rows, cols, cols, 4) ||
+        spans_overlap(top_logits, n_rows, top, top_stride, ts, outs[k], n_rows, cols, cols, 4) ||
+        spans_overlap(log_sums, 1, n_rows, n_rows, 4, outs[k], n_rows, cols, cols, 4))
+      return SPMV_ERR_INVALID_ARG;
+  }
+  if (spans_overlap(loss, 1, n_rows, n_rows, 4, stats, 1, 3 * n_rows, 3 * n_rows, 4)) return SPMV_ERR_INVALID_ARG;
+  a.loss = loss, a.stats = stats;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == SPMV_F32) return launch_rows<float>(a, st);
+  return dtype == SPMV_F16 ? launch_rows<__half>(a, st) : launch_rows<__nv_bfloat16>(a, st);
+}
+
+extern "C" spmv_status spmv_distill_backward(int64_t n_rows, int32_t vocab, const float* dloss,
+                                             int64_t dloss_stride, const void* logits, spmv_dtype dtype,
+                                             int64_t stride, int32_t top, const int32_t* top_tokens,
+                                             int64_t tokens_stride, const void* top_logits,
+                                             spmv_dtype top_dtype, int64_t top_stride,
+                                             const float* log_sums, float temperature, const float* stats,
+                                             void* dlogits, int64_t dlogits_stride, void* stream) {
+  DistillArgs a{};
+  const spmv_status s = take(a, n_rows, vocab, logits, dtype, stride, top, top_tokens, tokens_stride, top_logits,
+                             top_dtype, top_stride, log_sums, temperature);
+  if (s != SPMV_OK) return s;
+  const int64_t xs = op_dtype_size(dtype), ts = op_dtype_size(top_dtype);
+  if (!matrix_ok(dloss, n_rows, 1, dloss_stride, 4, false) || (n_rows > 0 && !stats) || !aligned_to(stats, 4) ||
+      !matrix_ok(dlogits, n_rows, vocab, dlogits_stride, xs, true))
+    return SPMV_ERR_INVALID_ARG;
+  if (n_rows == 0) return SPMV_OK;
+  const bool in_place = logits == dlogits && (stride == dlogits_stride || n_rows == 1);
+  if ((!in_place &&
+       spans_overlap(logits, n_rows, vocab, stride, xs, dlogits, n_rows, vocab, dlogits_stride, xs)) ||
+      spans_overlap(dloss, n_rows, 1, dloss_stride, 4, dlogits, n_rows, vocab, dlogits_stride, xs) ||
+      spans_overlap(top_tokens, n_rows, top, tokens_stride, 4, dlogits, n_rows, vocab, dlogits_stride, xs) ||
+      spans_overlap(top_logits, n_rows, top, top_stride, ts, dlogits, n_rows, vocab, dlogits_stride, xs) ||
+      spans_overlap(log_sums, 1, n_rows, n_rows, 4, dlogits, n_rows, vocab, dlogits_stride, xs) ||
+      spans_overlap(stats, 1, 3 * n_rows, 3 * n_rows, 4, dlogits, n_rows, vocab, dlogits_stride, xs))
+    return SPMV_ERR_INVALID_ARG;
+  a.dloss = dloss, a.dloss_stride = dloss_stride, a.stats = const_cast<float*>(stats);
+  a.dlogits = dlogits, a.out_stride = dlogits_stride;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == SPMV_F32) return launch_grad<float>(a, st);
+  return dtype == SPMV_F16 ? launch_grad<__half>(a, st) : launch_grad<__nv_bfloat16>(a, st);
+}

@@ -1,7 +1,8 @@
-"""Python binding of the operators around a pruned layer (include/spmv.h,
-last section), same names as the C calls: layer norm and its gradient,
-low-rank adapters of many requests, and the logits' penalties, biases and
-grammar masks.
+"""Python binding of the operators around a pruned layer and beside the dense
+model it came from (include/spmv.h, last two sections), same names as the C
+calls: layer norm and its gradient, low-rank adapters of many requests, the
+logits' penalties, biases and grammar masks; products with 4-bit weights, the
+verification of drafted tokens, distillation and its gradient.
 
 Only argument marshalling lives here. Tensors are CUDA tensors of one device,
 which is the current one; matrices have contiguous columns and any row
@@ -323,3 +324,164 @@ def spmv_logits_process(logits, out, prompt=None, output=None, repetition=None, 
         b_val, b_off, m_ptr, m_stride, _vector(mask_rows, n, _I32, "mask_rows"), n_masks, 0)
     _check(_lib_handle().spmv_logits_process(ctypes.byref(args), _on(stream, dev)),
            "spmv_logits_process")
+
+
+def spmv_int4_run(x, weights, scales, y, group: int, zeros=None, base=None, stream=None) -> None:
+    """y[t] = base[t] + W @ x[t], W[o, i] = scales[o, i // group] * (q[o, i] - zeros[o, i // group]).
+    x: (tokens, n_in) float16 or bfloat16 (a vector is one token); weights:
+    (n_out, ceil(n_in / 2)) uint8, column i in the low (i even) or high half of
+    byte i // 2; scales: (n_out, ceil(n_in / group)) contiguous, float32 or of
+    x's type; zeros: the same of uint8 (None: 8); group: a power of two from 32 on,
+    or at least n_in. y and base: (tokens, n_out), float32 or of x's type (base
+    may be y, or None for zero)."""
+    t, n_in, xs = _rows(x, "x")
+    t_y, n_out, ys = _rows(y, "y")
+    if t_y != t:
+        raise ValueError("x and y must have the same number of tokens")
+    if weights.dtype != torch.uint8:
+        raise TypeError(f"weights must be torch.uint8, got {weights.dtype}")
+    w_out, row_bytes, ws = _rows(weights, "weights")
+    if w_out != n_out or row_bytes != (n_in + 1) // 2:
+        raise ValueError(f"weights must be ({n_out}, {(n_in + 1) // 2})")
+    if group < 1:
+        raise ValueError("group must be at least 1")
+    if t > _INT32_MAX or n_in > _INT32_MAX or n_out > _INT32_MAX:
+        _too_large("spmv_int4_run")
+    group = min(group, _INT32_MAX)
+    groups = -(-n_in // group)
+    if tuple(scales.shape) != (n_out, groups) or not scales.is_contiguous():
+        raise ValueError(f"scales must be contiguous ({n_out}, {groups})")
+    bs = 0
+    if base is not None:
+        t_b, n_b, bs = _rows(base, "base")
+        if t_b != t or n_b != n_out:
+            raise ValueError("base and y must have the same shape")
+        if base.dtype != y.dtype:
+            raise TypeError(f"base must be {y.dtype}, got {base.dtype}")
+    dev = _same_device(x, y, weights, scales, zeros, base)
+    _check(_lib_handle().spmv_int4_run(
+        t, n_in, n_out, group, _dtype(x, "x"), x.data_ptr(), xs, weights.data_ptr(), ws,
+        scales.data_ptr(), _dtype(scales, "scales"),
+        _vector(zeros, n_out * groups, torch.uint8, "zeros"),
+        None if base is None else base.data_ptr(), bs, y.data_ptr(), _dtype(y, "y"), ys,
+        _on(stream, dev)), "spmv_int4_run")
+
+
+def spmv_verify_workspace(n_requests: int, n_drafts: int, vocab: int) -> int:
+    """Bytes of workspace that spmv_verify_drafts needs (0 for sizes it refuses)."""
+    if min(n_requests, n_drafts, vocab) < 0 or max(n_requests, n_drafts, vocab) > _INT32_MAX:
+        return 0
+    return int(_lib_handle().spmv_verify_workspace(n_requests, n_drafts, vocab))
+
+
+def spmv_verify_drafts(target, draft, draft_tokens, offsets, accept_uniforms, sample_uniforms,
+                       tokens, accepted, temperature=None, workspace=None, stream=None) -> None:
+    """Accept drafted tokens against the target's probabilities and draw one
+    token more per request, by given random numbers in [0, 1).
+    target: (drafts + requests, vocab) logits, a row more than drafts for each
+    request; draft: (drafts, vocab) logits of the same type, or None where the
+    drafts carry no probabilities; draft_tokens: int32 of all requests one
+    after the other; offsets: int64 of requests + 1. accept_uniforms: float32
+    per draft; sample_uniforms, temperature (None: 1; 0: greedy): float32 per
+    request. tokens (drafts + requests, int32) receives each request's accepted
+    drafts, the token drawn and -1 to its end, accepted (requests, int32) the
+    number of drafts accepted. include/spmv.h has the rules."""
+    rows, v, ts = _rows(target, "target")
+    d = draft_tokens.numel()
+    n = offsets.numel() - 1
+    if n < 0 or rows != d + n:
+        raise ValueError("target must have a row for each draft and one more for each request")
+    if rows > _INT32_MAX or v > _INT32_MAX:
+        _too_large("spmv_verify_drafts")
+    ds = 0
+    if draft is not None:
+        rows_d, v_d, ds = _rows(draft, "draft")
+        if rows_d != d or v_d != v:
+            raise ValueError("draft must have a row for each draft and target's vocabulary")
+        if draft.dtype != target.dtype:
+            raise TypeError(f"draft must be {target.dtype}, got {draft.dtype}")
+    if accept_uniforms is None or sample_uniforms is None or tokens is None or accepted is None:
+        raise ValueError("the random numbers and both outputs are needed")
+    dev = _same_device(target, draft, draft_tokens, offsets, accept_uniforms, sample_uniforms,
+                       tokens, accepted, temperature, workspace)
+    handle = _on(stream, dev)
+    lib = _lib_handle()
+    wp, wn, _owner = _workspace(workspace, lib.spmv_verify_workspace(n, d, v), handle, dev)
+    _check(lib.spmv_verify_drafts(
+        n, d, v, _dtype(target, "target"), target.data_ptr(), ts,
+        None if draft is None else draft.data_ptr(), ds,
+        _vector(draft_tokens, d, _I32, "draft_tokens"), _vector(offsets, n + 1, _I64, "offsets"),
+        _vector(accept_uniforms, d, _F32, "accept_uniforms"),
+        _vector(sample_uniforms, n, _F32, "sample_uniforms"),
+        _vector(temperature, n, _F32, "temperature"), _vector(tokens, rows, _I32, "tokens"),
+        _vector(accepted, n, _I32, "accepted"), wp, wn, handle), "spmv_verify_drafts")
+
+
+def _top(logits, top_tokens, top_logits, where: str):
+    """(rows, vocab, stride, top and its strides) of a distillation's inputs."""
+    n, v, stride = _rows(logits, "logits")
+    n_t, k, token_stride = _rows(top_tokens, "top_tokens")
+    n_l, k_l, top_stride = _rows(top_logits, "top_logits")
+    if n_t != n or n_l != n or k_l != k:
+        raise ValueError("top_tokens and top_logits must have one shape, with logits' rows")
+    if top_tokens.dtype != _I32:
+        raise TypeError(f"top_tokens must be {_I32}, got {top_tokens.dtype}")
+    if v > _INT32_MAX or k > _INT32_MAX:
+        _too_large(where)
+    return n, v, stride, k, token_stride, top_stride
+
+
+def _stats(stats, n: int) -> int:
+    if stats is not None and tuple(stats.shape) != (n, 3):
+        raise ValueError(f"stats must be ({n}, 3)")
+    return _vector(stats, 3 * n, _F32, "stats")
+
+
+def spmv_distill(logits, top_tokens, top_logits, loss, temperature: float = 1.0, log_sums=None,
+                 stats=None, stream=None) -> None:
+    """loss[i]: the divergence of softmax(logits[i] / temperature) from the
+    teacher's probabilities of its listed tokens. logits: (rows, vocab) (a
+    vector is one row); top_tokens: (rows, top) int32, -1 where nothing is
+    listed; top_logits: the same shape, any type. log_sums: float32 per row, the
+    teacher's log sum over its vocabulary of exp(logit / temperature): the
+    probabilities are then taken as they are and the rest counts as one more
+    class (None: normalised over the listed tokens). loss: float32 per row;
+    stats: (rows, 3) float32, what the gradient needs. include/spmv.h has the
+    formula."""
+    n, v, stride, k, token_stride, top_stride = _top(logits, top_tokens, top_logits, "spmv_distill")
+    if loss is None:
+        raise ValueError("loss is needed")
+    dev = _same_device(logits, top_tokens, top_logits, loss, log_sums, stats)
+    _check(_lib_handle().spmv_distill(
+        n, v, logits.data_ptr(), _dtype(logits, "logits"), stride, k, top_tokens.data_ptr(),
+        token_stride, top_logits.data_ptr(), _dtype(top_logits, "top_logits"), top_stride,
+        _vector(log_sums, n, _F32, "log_sums"), temperature, _vector(loss, n, _F32, "loss"),
+        _stats(stats, n), _on(stream, dev)), "spmv_distill")
+
+
+def spmv_distill_backward(dloss, logits, top_tokens, top_logits, stats, dlogits,
+                          temperature: float = 1.0, log_sums=None, stream=None) -> None:
+    """Gradient of spmv_distill: dlogits (of logits' type and shape; may be
+    logits itself) is overwritten. dloss: float32 per row, or one expanded over
+    the rows; stats: the forward call's, with the same temperature and
+    log_sums."""
+    n, v, stride, k, token_stride, top_stride = _top(logits, top_tokens, top_logits,
+                                                     "spmv_distill_backward")
+    n_o, v_o, out_stride = _rows(dlogits, "dlogits")
+    if n_o != n or v_o != v:
+        raise ValueError("dlogits and logits must have the same shape")
+    if dlogits.dtype != logits.dtype:
+        raise TypeError(f"dlogits must be {logits.dtype}, got {dlogits.dtype}")
+    if dloss.dtype != _F32:
+        raise TypeError(f"dloss must be {_F32}, got {dloss.dtype}")
+    if dloss.dim() > 1 or dloss.numel() != n:
+        raise ValueError(f"dloss must have {n} elements")
+    if stats is None:
+        raise ValueError("stats of the forward call are needed")
+    dev = _same_device(logits, top_tokens, top_logits, dloss, log_sums, stats, dlogits)
+    _check(_lib_handle().spmv_distill_backward(
+        n, v, dloss.data_ptr(), dloss.stride(0) if dloss.dim() else 0, logits.data_ptr(),
+        _dtype(logits, "logits"), stride, k, top_tokens.data_ptr(), token_stride,
+        top_logits.data_ptr(), _dtype(top_logits, "top_logits"), top_stride,
+        _vector(log_sums, n, _F32, "log_sums"), temperature, _stats(stats, n), dlogits.data_ptr(),
+        out_stride, _on(stream, dev)), "spmv_distill_backward")

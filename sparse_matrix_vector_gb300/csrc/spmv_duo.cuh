@@ -1,12 +1,14 @@
-// Numbers as unevaluated sums of two fp32 (some 2^-47 of relative error each
+// Numbers as unevaluated sums of two fp32 (some 2^-45 of relative error each
 // operation), for what lies next to a border: sums of exponentials whose
-// comparison with a given random number has to come out as in 64 bits. The
-// device's fp64 rate is a sixtieth of its fp32 rate; these cost some twenty
-// fp32 operations. The sums and products are the error-free transformations
-// of Dekker (1971) and Knuth, with fused multiply-adds for the products.
+// comparison with a given random number has to come out as in 64 bits. (The
+// device's fp64 rate is a sixtieth of its fp32 rate.) The sums and products
+// are the error-free transformations of Knuth and of Dekker (1971), with fused
+// multiply-adds for the products. Exponentials come two at a time, in the
+// packed fp32 instructions: some 30 instructions each.
 #pragma once
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cstdint>
 
 namespace spmv {
@@ -24,20 +26,31 @@ __device__ __forceinline__ Duo two_sum(float a, float b) {
   const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
   return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
-__device__ __forceinline__ Duo duo_add(const Duo& a, const Duo& b) {
+__device__ __forceinline__ Duo operator+(const Duo& a, const Duo& b) {
   const Duo s = two_sum(a.h, b.h);
   return fast_two_sum(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
 }
-__device__ __forceinline__ Duo duo_mul(const Duo& a, const Duo& b) {
+__device__ __forceinline__ Duo operator-(const Duo& a, const Duo& b) { return a + Duo{-b.h, -b.l}; }
+__device__ __forceinline__ Duo operator*(const Duo& a, const Duo& b) {
   const float p = __fmul_rn(a.h, b.h);
   const float e = __fmaf_rn(a.h, b.h, -p);
   return fast_two_sum(p, __fadd_rn(e, __fmaf_rn(a.h, b.l, __fmul_rn(a.l, b.h))));
 }
-__device__ __forceinline__ Duo duo_of(double v) {
-  const float h = (float)v;
-  return {h, (float)(v - (double)h)};
+__device__ __forceinline__ Duo operator/(const Duo& a, const Duo& b) {
+  const float q = __fdiv_rn(a.h, b.h);
+  const Duo r = a - b * Duo{q, 0.f};
+  return fast_two_sum(q, __fdiv_rn(r.h, b.h));
 }
-__device__ __forceinline__ double to_f64(const Duo& a) { return (double)a.h + (double)a.l; }
+__device__ __forceinline__ bool operator>(const Duo& a, const Duo& b) {
+  return a.h > b.h || (a.h == b.h && a.l > b.l);
+}
+
+// log2(e) / t
+__device__ __forceinline__ Duo log2e_over(float t) {
+  const Duo log2e{0x1.715476p+0f, 0x1.4ae0c0p-26f};
+  const float q = __fdiv_rn(log2e.h, t);
+  return fast_two_sum(q, __fdiv_rn(__fadd_rn(__fmaf_rn(-q, t, log2e.h), log2e.l), t));
+}
 
 // 2^(j / 64), to 2^-48.
 __device__ const float2 kRoots[64] = {
@@ -74,29 +87,113 @@ __device__ const float2 kRoots[64] = {
     {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.efa1be0000000p+0f, 0x1.cc2b440000000p-25f},
     {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f}, {0x1.fa7c180000000p+0f, 0x1.9e90d80000000p-28f},};
 
-// 2^a for a <= 0, to some 2^-40; 0 below 2^-126. With k = round(64 a),
-// 2^a = 2^(k / 64) e^y, |y| <= log(2) / 128: a table (Tang 1989) and five
-// terms of the exponential's series. `roots`: kRoots in shared memory.
-__device__ __forceinline__ Duo duo_exp2(const Duo& a, const float2* roots) {
-  if (!(a.h >= -126.f)) return {0.f, 0.f};
-  const float k = rintf(a.h * 64.f);
-  const Duo g = two_sum(__fmaf_rn(k, -1.f / 64.f, a.h), a.l);  // (the difference is exact)
-  const float ln2_h = 0x1.62e43p-1f, ln2_l = -0x1.05c61p-29f;
-  const float yh = __fmul_rn(g.h, ln2_h);
-  const float yl = __fadd_rn(__fmaf_rn(g.h, ln2_h, -yh), __fmaf_rn(g.h, ln2_l, __fmul_rn(g.l, ln2_h)));
-  // e^y - 1 - yh
-  float q = __fmaf_rn(yh, 1.f / 120.f, 1.f / 24.f);
-  q = __fmaf_rn(q, yh, 1.f / 6.f);
-  q = __fmaf_rn(q, yh, 0.5f);
-  q = __fmul_rn(q, __fmul_rn(yh, yh));
-  q = __fadd_rn(q, __fmaf_rn(yh, yl, yl));
-  const Duo e = fast_two_sum(1.f, yh);
-  const int ki = (int)k;
-  const float2 r = roots[ki & 63];
-  const Duo p = duo_mul({e.h, __fadd_rn(e.l, q)}, {r.x, r.y});
-  const float up = __int_as_float(((ki >> 6) + 127) << 23);  // 2^floor(k / 64), at least 2^-126
-  return {__fmul_rn(p.h, up), __fmul_rn(p.l, up)};
+// Two fp32 in a 64-bit register, and the packed instructions on them.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pack2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
 }
+__device__ __forceinline__ float2 unpack2(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ F2 both(float x) { return pack2(x, x); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 sub2(F2 a, F2 b) { return fma2(b, both(-1.f), a); }
+
+struct Duo2 {  // two of them; {h, l} need not be normalised: |l| <= 2^-20 |h|
+  F2 h, l;
+  // += , with the low parts' own roundings (2^-44 of the sum)
+  __device__ __forceinline__ void accumulate(const Duo2& a) {
+    const F2 s = add2(h, a.h), t = sub2(s, h);
+    const F2 e = add2(sub2(h, sub2(s, t)), sub2(a.h, t));
+    h = s;
+    l = add2(l, add2(e, a.l));
+  }
+  __device__ __forceinline__ Duo sum() const {
+    const float2 x = unpack2(h), y = unpack2(l);
+    return fast_two_sum(x.x, y.x) + fast_two_sum(x.y, y.y);
+  }
+};
+
+// 2^((x - m) c) of a row's logits x, m being the largest: relative error some
+// 2^-39. NaN and what is below 2^-126 give 0; plus infinity counts as the
+// largest number. With a = (x - m) c and k = round(64 a), 2^a = 2^(k / 64) e^y,
+// |y| <= log(2) / 128: a table of 2^(j / 64) (Tang 1989) and four terms of
+// the exponential's series. `roots`: kRoots in shared memory.
+struct RowExp2 {
+  float m, low;  // logits below `low` give 0
+  Duo c;
+  const float2* roots;
+  __device__ __forceinline__ void set(float m_, const Duo& c_, const float2* roots_) {
+    m = m_, c = c_, roots = roots_;
+    low = fmaxf(m - 126.f / c.h, -FLT_MAX);
+  }
+  __device__ __forceinline__ Duo2 operator()(float x, float y) const {
+    const bool has_x = x >= low, has_y = y >= low;
+    x = fminf(has_x ? x : m, FLT_MAX);
+    y = fminf(has_y ? y : m, FLT_MAX);
+    // d = x - m
+    const F2 v = pack2(x, y), mm = both(-m);
+    const F2 dh = add2(v, mm), dt = sub2(dh, v);
+    const F2 dl = add2(sub2(v, sub2(dh, dt)), sub2(mm, dt));
+    // a = d c, as -na + e
+    const F2 na = mul2(dh, both(-c.h));
+    F2 e = fma2(dh, both(c.h), na);
+    e = fma2(dh, both(c.l), e);
+    e = fma2(dl, both(c.h), e);
+    // k in the low bits of t (1.5 * 2^23 + k), and k / 64 - a without e
+    const F2 big = both(12582912.f);
+    const F2 t = fma2(na, both(-64.f), big);
+    const F2 nf = fma2(sub2(t, big), both(1.f / 64.f), na);
+    // y = (f + e) log(2)
+    const float ln2_h = 0x1.62e43p-1f, ln2_l = -0x1.05c61p-29f;
+    const F2 yh = mul2(nf, both(-ln2_h)), nyh = mul2(nf, both(ln2_h));
+    F2 yl = fma2(nf, both(-ln2_h), nyh);
+    yl = fma2(nf, both(-ln2_l), yl);
+    yl = fma2(e, both(ln2_h), yl);
+    // e^y - 1 - yh
+    F2 q = fma2(yh, both(1.f / 24.f), both(1.f / 6.f));
+    q = fma2(q, yh, both(0.5f));
+    const F2 p = fma2(q, mul2(yh, yh), fma2(yh, yl, yl));
+    // times the table's
+    const float2 tf = unpack2(t);
+    const uint32_t kx = __float_as_uint(tf.x), ky = __float_as_uint(tf.y);
+    const float2 r0 = roots[kx & 63], r1 = roots[ky & 63];
+    const F2 rh = pack2(r0.x, r1.x), rl = pack2(r0.y, r1.y);
+    const F2 u = mul2(rh, yh), nu = mul2(rh, nyh);
+    F2 lo = fma2(rh, yh, nu);
+    lo = fma2(rh, p, lo);
+    lo = add2(lo, fma2(rl, yh, rl));
+    const F2 h = add2(rh, u);
+    lo = add2(sub2(u, sub2(h, rh)), lo);
+    // 2^floor(k / 64)
+    float ux = __uint_as_float(((kx << 17) & 0xff800000u) + 0x3f800000u);
+    float uy = __uint_as_float(((ky << 17) & 0xff800000u) + 0x3f800000u);
+    const F2 up = pack2(has_x ? ux : 0.f, has_y ? uy : 0.f);
+    return {mul2(h, up), mul2(lo, up)};
+  }
+  __device__ __forceinline__ Duo one(float x) const {
+    const Duo2 e = (*this)(x, -INFINITY);
+    return {unpack2(e.h).x, unpack2(e.l).x};
+  }
+};
 
 }  // namespace
 }  // namespace spmv

@@ -668,6 +668,10 @@ spmv_status spmv_logits_process(const spmv_logits* args, void* stream);
  * are those of the section above.
  * ------------------------------------------------------------------------ */
 
+/* Bytes of workspace that spmv_int4_run needs for these sizes (0 for sizes it
+ * refuses). */
+int64_t spmv_int4_workspace(int32_t n_tokens, int32_t n_in);
+
 /* Products of a few tokens with 4-bit weights:
  *   y_t = base_t + W x_t,
  *   W[o, i] = scale[o, i / group] * (q[o, i] - zero[o, i / group]).
@@ -691,7 +695,7 @@ spmv_status spmv_int4_run(int32_t n_tokens, int32_t n_in, int32_t n_out, int32_t
                           const uint8_t* weights, int64_t weights_stride, const void* scales,
                           spmv_dtype scales_dtype, const uint8_t* zeros, const void* base,
                           int64_t base_stride, void* y, spmv_dtype y_dtype, int64_t y_stride,
-                          void* stream);
+                          void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Bytes of workspace that spmv_verify_drafts needs for these sizes (0 for
  * sizes it refuses). */

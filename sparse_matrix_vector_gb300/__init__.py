@@ -24,7 +24,7 @@ from ._lib import (  # noqa: F401
 )
 
 _OPERATORS = ("spmv_adapters_run", "spmv_adapters_workspace", "spmv_distill",
-              "spmv_distill_backward", "spmv_int4_run", "spmv_layernorm",
+              "spmv_distill_backward", "spmv_int4_run", "spmv_int4_workspace", "spmv_layernorm",
               "spmv_layernorm_backward", "spmv_layernorm_backward_workspace",
               "spmv_logits_process", "spmv_verify_drafts", "spmv_verify_workspace")
 

@@ -151,7 +151,8 @@ SIGNATURES = {
     "spmv_logits_process": (ctypes.c_int, [ctypes.POINTER(spmv_logits), c_p]),
     "spmv_int4_run": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i32, ctypes.c_int, c_p, c_i64, c_p,
                                      c_i64, c_p, ctypes.c_int, c_p, c_p, c_i64, c_p, ctypes.c_int,
-                                     c_i64, c_p]),
+                                     c_i64, c_p, c_i64, c_p]),
+    "spmv_int4_workspace": (c_i64, [c_i32, c_i32]),
     "spmv_verify_workspace": (c_i64, [c_i32, c_i32, c_i32]),
     "spmv_verify_drafts": (ctypes.c_int, [c_i32, c_i32, c_i32, ctypes.c_int, c_p, c_i64, c_p,
                                           c_i64, c_p, c_p, c_p, c_p, c_p, c_p, c_p, c_p, c_i64,

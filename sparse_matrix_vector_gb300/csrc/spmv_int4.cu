@@ -2,16 +2,27 @@
 //   y_t = base_t + W x_t,  W[o, i] = scale[o, i / group] * (q[o, i] - zero[o, i / group]),
 // for a few tokens t. Bound by reading the packed weights once. They become
 // exact small integers in x's 16-bit type (bits or-ed into the mantissa of
-// 1024 or 128, less 1024 or 128 plus the zero point) that go through the
-// warp-level matrix instruction (16 weights' rows x 8 tokens x 16 columns,
-// fp32 sums); a group's sum is scaled in fp32 once it is whole, so nothing is
-// rounded before the products' own sums.
+// 1024 or 128, less 1024 or 128 plus the zero point), go through the
+// fifth-generation tensor cores, and a group's sums are scaled in fp32 once
+// they are whole, so nothing is rounded before the products' own sums.
+//
+// 128 rows of W and up to 64 tokens to a CTA, up to four CTAs to an SM. The
+// rows' step of columns is the instruction's A operand and lives in tensor
+// memory: a thread unpacks its row's columns into its own lane there, so that
+// 16-bit weights never pass through shared memory. x is the B operand in
+// shared memory, and the sums of a group come back from tensor memory to be
+// scaled into registers. Four warps unpack and add up, one thread issues the
+// instructions and x's copies; there is one buffer of each, and what a CTA
+// waits for, the SM's others work meanwhile. The columns are split over a
+// cluster's CTAs, whose sums meet in distributed shared memory.
 //
 // The order of the columns within a sum is free as long as both operands agree
-// on it: a 32-bit word of 8 columns gives two instructions' worth of one
-// lane's share, in the pairs (0, 4), (1, 5), (2, 6), (3, 7) that masks take out
-// of it, and x is taken in the same pairs.
+// on it: masks take the pairs (0, 4), (1, 5), (2, 6), (3, 7) out of a word of 8
+// columns, and a first, small launch lays x out in the same order, as the very
+// image that the B operand's steps have in shared memory, so that a step of x
+// is one bulk copy.
 #include <cooperative_groups.h>
+#include <cuda.h>
 
 #include <climits>
 #include <type_traits>
@@ -24,15 +35,15 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kMaxWarps = 16;
-constexpr int kRows = 32;              // of W, to a CTA
-constexpr int kStep = 128;             // columns that a warp takes at a time
-constexpr int kStepBytes = kStep / 2;
-constexpr int kRing = 4;               // steps of weights in shared memory
-constexpr int kStage = kRows * kStepBytes;
+constexpr int kTileRows = 128;
+constexpr int kRowWarps = 4;
+constexpr int kTileThreads = (kRowWarps + 1) * 32;
+constexpr int kMaxXStages = 6, kMaxDepth = 16;
+constexpr int kMaxSplit = 8;
+constexpr int kTensorColumns = 128;  // of tensor memory: a quarter of an SM's
 
 struct Int4Args {
-  int n_tokens, n_in, n_out, group, groups;
+  int n_tokens, n_in, n_out, groups;
   const void* x;
   int64_t xs;
   const uint8_t* w;
@@ -43,28 +54,12 @@ struct Int4Args {
   int64_t bs;
   void* y;
   int64_t ys;
-  int group_shift;  // log2(group), or 31: one group
+  uint4* image;     // x as the steps' B operands
+  int group_shift;  // log2(group), or 30: one group
   int y_dtype;
   int split;        // CTAs that share a block of rows
-  bool scales_f32, vec_x;
+  bool scales_f32, vec_x, vec_y;
 };
-
-template <typename T>
-__device__ __forceinline__ void mma_int4(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  if constexpr (std::is_same<T, __half>::value)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 // (w & mask) | bits
 __device__ __forceinline__ uint32_t take_bits(uint32_t w, uint32_t mask, uint32_t bits) {
@@ -114,13 +109,6 @@ struct Unpack<__nv_bfloat16> {
   }
 };
 
-// Where piece p (16 bytes) of row r stands in a stage: rows of 64 bytes whose
-// pieces are exchanged so that reads of 4, 8 or 16 bytes by 8 rows x 4 lanes
-// meet every bank once.
-__device__ __forceinline__ int piece_at(int r, int p) {
-  return r * kStepBytes + ((p ^ (((r >> 1) & 1) << 1 | ((r >> 2) & 1))) << 4);
-}
-
 // 16 bytes at p of which `left` are inside the row (the others zero), any
 // alignment: the two 16-byte granules around them, shifted into place.
 __device__ __forceinline__ uint4 load_piece(const uint8_t* p, int left) {
@@ -159,214 +147,43 @@ __device__ __forceinline__ uint4 load_x(const T* p, int left, bool vec) {
   return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
 }
 
-// A CTA: 32 rows of W for 8 NT tokens, the columns split over its warps. SEG:
-// columns whose sums are scaled together (a group, or a step of a longer one).
-// FAST: rows of W and x start on 16-byte boundaries.
-template <typename T, int NT, int SEG, bool FAST>
-__global__ void __maxnreg__(NT == 1 ? 80 : NT == 2 ? 104 : 128) int4_rows(Int4Args a) {
-  extern __shared__ __align__(16) unsigned char s_int4[];
-  constexpr int kWords = SEG / 32, kSegs = kStep / SEG;
-  const int me = threadIdx.x, warp = me >> 5, lane = me & 31, g = lane >> 2, q = lane & 3;
-  const int warps = (int)blockDim.x >> 5;
-  const int row0 = blockIdx.x * kRows, token0 = blockIdx.y * 8 * NT;
-  const int row_bytes = (a.n_in + 1) / 2;
-  const int steps = (a.n_in + kStep - 1) / kStep, whole = a.n_in / kStep;
-  const int begin = (int)((int64_t)steps * warp / warps), end = (int)((int64_t)steps * (warp + 1) / warps);
-  unsigned char* ring = s_int4 + warp * kRing * kStage;
-  // rows g + 8 r of the CTA's, those past the end repeating the last
-  int row[4];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) row[r] = min(g + 8 * r, a.n_out - 1 - row0);
-
-  // this lane's pieces of a step: rows row[k], 16 bytes from column 32 q on
-  const uint8_t* src = a.w + (int64_t)row0 * a.ws + q * 16;
-  const uint8_t* src_row[4];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) src_row[r] = src + row[r] * a.ws;
-  const uint32_t dst0 = smem_u32(ring) + piece_at(g, q);  // (piece_at(g + 8 r, q): 8 rows of 64 bytes on)
-  const auto fetch = [&](int step) {
-    if (step < end) {
-      const int at = step * kStepBytes;
-      const uint32_t to = (step & (kRing - 1)) * kStage;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if constexpr (FAST) {
-          if (step < whole) {
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst0 + r * 8 * kStepBytes + to),
-                         "l"(src_row[r] + at)
-                         : "memory");
-          } else {
-            const int bytes = max(0, min(16, row_bytes - at - q * 16));
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst0 + r * 8 * kStepBytes + to),
-                         "l"(src_row[r] + (bytes > 0 ? at : 0)), "r"(bytes)
-                         : "memory");
-          }
-        } else {
-          const uint4 v = load_piece(src_row[r] + at, row_bytes - at - q * 16);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst0 + r * 8 * kStepBytes + to), "r"(v.x), "r"(v.y),
-                       "r"(v.z), "r"(v.w)
-                       : "memory");
-        }
-      }
-    }
-    if constexpr (FAST) copy_commit();
-  };
-
-  const T* x[NT];
-  bool has[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int t = token0 + 8 * n + g;
-    has[n] = t < a.n_tokens;
-    x[n] = static_cast<const T*>(a.x) + (has[n] ? (int64_t)t * a.xs : 0) + q * 8 * kWords;
+// Elements i to i + 3 of an array of runtime type, aligned to all four.
+__device__ __forceinline__ float4 load_four(const void* p, int dtype, int64_t i) {
+  if (dtype == SPMV_F32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+  const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const unsigned short*>(p) + i);
+  if (dtype == SPMV_F16) {
+    const float2 a = __half22float2(reinterpret_cast<const __half2&>(w.x));
+    const float2 b = __half22float2(reinterpret_cast<const __half2&>(w.y));
+    return make_float4(a.x, a.y, b.x, b.y);
   }
-  // scales and zero points of rows row[r], a segment ahead
-  const int64_t first_scale = (int64_t)row0 * a.groups;
-  int scale_row[4];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) scale_row[r] = row[r] * a.groups;
-  float scale[4];
-  uint32_t zero[4];
-  const auto load_scales = [&](int col) {
-    const int k = min(col >> a.group_shift, a.groups - 1);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      scale[r] = a.scales_f32 ? __ldg(static_cast<const float*>(a.scales) + first_scale + scale_row[r] + k)
-                              : to_f32(static_cast<const T*>(a.scales)[first_scale + scale_row[r] + k]);
-      zero[r] = a.zeros ? __ldg(a.zeros + first_scale + scale_row[r] + k) & 15u : 8u;
-    }
-  };
-
-  float acc[2][NT][4] = {};
-#pragma unroll
-  for (int k = 0; k < kRing - 1; ++k) fetch(begin + k);
-  if (begin < end) load_scales(begin * kStep);
-  for (int step = begin; step < end; ++step) {
-    if constexpr (FAST) copy_wait<kRing - 2>();
-    __syncwarp();
-    const unsigned char* stage = ring + (step & (kRing - 1)) * kStage;
-    fetch(step + kRing - 1);
-#pragma unroll
-    for (int seg = 0; seg < kSegs; ++seg) {
-      const int col0 = step * kStep + seg * SEG;
-      float s_now[4];
-      Unpack<T> un[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        s_now[r] = scale[r];
-        un[r].set(zero[r]);
-      }
-      load_scales(col0 + SEG);  // (behind the last column: the last group's again)
-      // x of this lane's words: columns col0 + q * 8 kWords + 8 w
-      uint4 v[NT][kWords];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < kWords; ++k) {
-          if (FAST && step < whole) {
-            v[n][k] = make_uint4(0, 0, 0, 0);
-            if (has[n]) v[n][k] = __ldg(reinterpret_cast<const uint4*>(x[n] + col0 + 8 * k));
-          } else {
-            v[n][k] = load_x(x[n] + col0 + 8 * k, has[n] ? a.n_in - col0 - q * 8 * kWords - 8 * k : 0, FAST);
-          }
-        }
-      // its words of the rows
-      uint32_t w[4][kWords];
-      const int byte = seg * (SEG / 2) + q * 4 * kWords;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const unsigned char* at = stage + piece_at(g, byte >> 4) + 8 * r * kStepBytes + (byte & 15);
-        if constexpr (kWords == 4) {
-          const uint4 u = *reinterpret_cast<const uint4*>(at);
-          w[r][0] = u.x, w[r][1] = u.y, w[r][2] = u.z, w[r][3] = u.w;
-        } else if constexpr (kWords == 2) {
-          const uint2 u = *reinterpret_cast<const uint2*>(at);
-          w[r][0] = u.x, w[r][1] = u.y;
-        } else {
-          w[r][0] = *reinterpret_cast<const uint32_t*>(at);
-        }
-      }
-      float part[2][NT][4] = {};
-#pragma unroll
-      for (int k = 0; k < kWords; ++k) {
-        uint32_t b[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          b[n][0] = __byte_perm(v[n][k].x, v[n][k].z, 0x5410);
-          b[n][1] = __byte_perm(v[n][k].x, v[n][k].z, 0x7632);
-          b[n][2] = __byte_perm(v[n][k].y, v[n][k].w, 0x5410);
-          b[n][3] = __byte_perm(v[n][k].y, v[n][k].w, 0x7632);
-        }
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          uint32_t lo[4], hi[4];
-          un[2 * m].run(w[2 * m][k], lo);
-          un[2 * m + 1].run(w[2 * m + 1][k], hi);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma_int4<T>(part[m][n], lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
-            mma_int4<T>(part[m][n], lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
-          }
-        }
-      }
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[m][n][k] += s_now[2 * m + (k >> 1)] * part[m][n][k];
-    }
-    __syncwarp();  // (all lanes are done with the stage before it is filled again)
-  }
-  if constexpr (FAST) copy_wait<0>();
-  __syncthreads();
-
-  // the warps' sums, joined in their order
-  constexpr int kPitch = kRows + 1;
-  float* sums = reinterpret_cast<float*>(s_int4);
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        sums[(warp * 8 * NT + 8 * n + 2 * q + (k & 1)) * kPitch + 16 * m + 8 * (k >> 1) + g] = acc[m][n][k];
-  __syncthreads();
-  for (int e = me; e < kRows * 8 * NT; e += (int)blockDim.x) {
-    const int r = e % kRows, n = e / kRows, t = token0 + n;
-    if (row0 + r >= a.n_out || t >= a.n_tokens) continue;
-    float v = 0.f;
-    for (int k = 0; k < warps; ++k) v += sums[(k * 8 * NT + n) * kPitch + r];
-    if (a.base) v += load_as_f32(a.base, a.y_dtype, (int64_t)t * a.bs + row0 + r);
-    store_from_f32(a.y, a.y_dtype, (int64_t)t * a.ys + row0 + r, v);
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store_four(void* p, int dtype, int64_t i, const float4& v) {
+  if (dtype == SPMV_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = v;
+  } else if (dtype == SPMV_F16) {
+    Pack<__half, 4> r;
+    set_pair(r, 0, make_float2(v.x, v.y));
+    set_pair(r, 1, make_float2(v.z, v.w));
+    store_pack<__half, 4>(static_cast<__half*>(p) + i, r);
+  } else {
+    Pack<__nv_bfloat16, 4> r;
+    set_pair(r, 0, make_float2(v.x, v.y));
+    set_pair(r, 1, make_float2(v.z, v.w));
+    store_pack<__nv_bfloat16, 4>(static_cast<__nv_bfloat16*>(p) + i, r);
   }
 }
 
-// ------------------------------------------------------- tensor-core tiles
-// Rows at 16-byte boundaries: 256 rows of W and up to 64 tokens to a CTA, one
-// CTA to an SM, on the fifth-generation tensor cores. A tile of 128 rows is
-// the instruction's A operand and lives in tensor memory (a thread of the
-// tile's four warps unpacks its row's columns into its own lane there), x is
-// the B operand in shared memory, and the sums of a group come back from
-// tensor memory to be scaled into fp32 registers. Three kinds of warps work
-// at the same time: eight unpack and add up (two tiles), two bring x into the
-// layout of the operand, one thread issues the instructions. The columns are
-// split over a cluster's CTAs, whose sums meet in distributed shared memory.
-
-constexpr int kTileRows = 256;
-constexpr int kRowWarps = kTileRows / 32, kXWarps = 2;
-constexpr int kTileThreads = (kRowWarps + kXWarps + 1) * 32;
-constexpr int kRingBytes = 12 * 1024;  // of a warp's weights
-constexpr int kXStages = 4;
-constexpr int kMaxSplit = 8;
-
-__device__ __forceinline__ void tmem_alloc(uint32_t* to, int columns) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(to)), "r"(columns)
+template <int COLUMNS>
+__device__ __forceinline__ void tmem_alloc(uint32_t* to) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(to)), "n"(COLUMNS)
                : "memory");
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
 }
-__device__ __forceinline__ void tmem_free(uint32_t at, int columns) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
+template <int COLUMNS>
+__device__ __forceinline__ void tmem_free(uint32_t at) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "n"(COLUMNS));
 }
 __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16]) {
   asm volatile(
@@ -397,6 +214,11 @@ __device__ __forceinline__ void tile_mma(uint32_t d, uint32_t a, uint64_t b, uin
       "r"(a), "l"(b), "r"(kind), "r"(add)
       : "memory");
 }
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
 // The barrier hears of it when all of this thread's instructions so far are done.
 __device__ __forceinline__ void tile_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
@@ -404,8 +226,8 @@ __device__ __forceinline__ void tile_commit(uint64_t* bar) {
 }
 
 struct TileBars {
-  uint64_t x_full[kXStages], x_empty[kXStages];
-  uint64_t a_full[2][2], done[2][2];  // [tile][buffer]
+  uint64_t x_full[kMaxXStages], w_full[kMaxDepth];
+  uint64_t a_full, done;
   uint64_t last;
   uint32_t tmem;
   int failed;
@@ -421,36 +243,83 @@ __device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatil
   *failed = 1;
 }
 
-template <typename T, int N, int SEG>
-__global__ void __launch_bounds__(kTileThreads, 1) int4_tiles(Int4Args a) {
-  constexpr int kPieces = SEG / 32;                // 16-byte pieces of a row's step
-  constexpr int kStageBytes = 32 * kPieces * 16;   // of a warp
-  constexpr int kDepth = kRingBytes / kStageBytes;
-  constexpr int kLine = SEG >= 64 ? 128 : 64;      // bytes of a row of the B operand: its swizzle
-  constexpr int kXBytes = N * SEG * 2;
-  constexpr int kAColumns = SEG / 2;               // tensor memory columns of a buffer of A
-  constexpr int kColumns = 4 * kAColumns + 4 * N <= 128 ? 128 : 4 * kAColumns + 4 * N <= 256 ? 256 : 512;
+// The steps of a product of N tokens at a time with groups of GROUP columns (or
+// longer ones, of which a step is a part): as many groups to a step as two
+// buffers of sums have room for in tensor memory.
+template <int N, int GROUP>
+struct Step {
+  static constexpr int kGroups = 128 / GROUP < 64 / N ? 128 / GROUP : 64 / N;
+  static constexpr int kColumns = GROUP * kGroups;
+  static constexpr int kLine = kColumns >= 64 ? 128 : 64;  // bytes of a row of the B operand: its swizzle
+  static constexpr int kXBytes = N * kColumns * 2;
+  static constexpr int kPerSm = N == 64 ? 3 : 3;           // CTAs
+  static constexpr int kXStages = N == 16 ? 6 : N == 32 ? 4 : 3;
+  static constexpr int kPre = 2;             // pieces unpacked before the last step's instructions are done
+  static constexpr int kDepth = (N == 64 ? 3 : 4) * (128 / kColumns);  // steps of weights in shared memory
+  static constexpr size_t kRings = kXStages * (size_t)kXBytes + kDepth * (size_t)kTileRows * kColumns / 2;
+  // Where 16-byte piece c of token n stands in a step's B operand: parts of
+  // N rows of kLine bytes, pieces exchanged by the row's number.
+  static __device__ __forceinline__ uint32_t place(int n, int c) {
+    uint32_t at = (uint32_t)(n * kLine + c % (kLine / 16) * 16);
+    at ^= (at >> 3) & (kLine == 128 ? 0x70u : 0x30u);
+    return at + (uint32_t)(c / (kLine / 16)) * (N * kLine);
+  }
+};
+
+// x as the B operands of all steps: [tokens / N][step], zeros behind the last
+// token and column.
+template <typename T, int N, int GROUP>
+__global__ void __launch_bounds__(256) int4_image(Int4Args a) {
+  using S = Step<N, GROUP>;
+  pdl_launch_dependents();
+  const int steps = (a.n_in + S::kColumns - 1) / S::kColumns;
+  constexpr int kPieces = S::kColumns / 8;
+  const int64_t n_pieces = (int64_t)steps * kPieces;  // of a token
+  const int64_t id = blockIdx.x * 256ll + threadIdx.x;
+  if (id >= n_pieces * N) return;
+  const int n = (int)(id / n_pieces), t = blockIdx.y * N + n;
+  const int64_t k = id - n * n_pieces;
+  const int64_t col = k * 8, step = k / kPieces;
+  const uint4 v = load_x(static_cast<const T*>(a.x) + t * a.xs + col,
+                         t < a.n_tokens && col < a.n_in ? (int)min((int64_t)8, a.n_in - col) : 0, a.vec_x);
+  char* to = reinterpret_cast<char*>(a.image) + ((int64_t)blockIdx.y * steps + step) * S::kXBytes;
+  *reinterpret_cast<uint4*>(to + S::place(n, (int)(k % kPieces))) =
+      make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                 __byte_perm(v.y, v.w, 0x7632));
+}
+
+// ALIGNED: rows of W start on 16-byte boundaries.
+template <typename T, int N, int GROUP, bool ALIGNED>
+__global__ void __launch_bounds__(kTileThreads, Step<N, GROUP>::kPerSm)
+int4_tiles(const Int4Args a, const __grid_constant__ CUtensorMap w_map) {
+  using S = Step<N, GROUP>;
+  constexpr int kColumns = S::kColumns, kGroups = S::kGroups;
+  constexpr int kPieces = kColumns / 32;           // 16-byte pieces of a row's step
+  constexpr int kStageBytes = kTileRows * kPieces * 16;
+  constexpr int kDepth = S::kDepth;
+  constexpr int kSums = kColumns / 2;              // tensor memory: A, then the sums
+  static_assert(kSums + N * kGroups <= kTensorColumns, "tensor memory");
   extern __shared__ __align__(1024) unsigned char s_raw[];
   __shared__ TileBars bars;
   // (the operand's swizzle goes by the address: rows of 1024-byte groups)
   unsigned char* s_tiles = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);
   unsigned char* x_ring = s_tiles;
-  unsigned char* w_ring = s_tiles + kXStages * kXBytes;
+  unsigned char* w_ring = s_tiles + S::kXStages * S::kXBytes;
   const int me = threadIdx.x, warp = me >> 5, lane = me & 31;
   const int rank = (int)(blockIdx.x % (unsigned)a.split), row0 = (int)(blockIdx.x / (unsigned)a.split) * kTileRows;
   const int token0 = blockIdx.y * N;
-  const int steps = (a.n_in + SEG - 1) / SEG;
+  const int steps = (a.n_in + kColumns - 1) / kColumns;
   const int begin = (int)((int64_t)steps * rank / a.split);
   const int count = (int)((int64_t)steps * (rank + 1) / a.split) - begin;
 
   if (me == 0) {
-    for (int k = 0; k < kXStages; ++k) mbar_init(&bars.x_full[k], kXWarps * 32), mbar_init(&bars.x_empty[k], 1);
-    for (int k = 0; k < 4; ++k) mbar_init(&bars.a_full[k >> 1][k & 1], 4), mbar_init(&bars.done[k >> 1][k & 1], 1);
-    mbar_init(&bars.last, 1);
+    for (int k = 0; k < S::kXStages; ++k) mbar_init(&bars.x_full[k], 1);
+    for (int k = 0; k < kDepth; ++k) mbar_init(&bars.w_full[k], 1);
+    mbar_init(&bars.a_full, kRowWarps), mbar_init(&bars.done, 1), mbar_init(&bars.last, 1);
     bars.failed = 0;
     fence_mbar_init();
   }
-  if (warp == kRowWarps + kXWarps) tmem_alloc(&bars.tmem, kColumns);
+  if (warp == kRowWarps) tmem_alloc<kTensorColumns>(&bars.tmem);
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
@@ -461,163 +330,183 @@ __global__ void __launch_bounds__(kTileThreads, 1) int4_tiles(Int4Args a) {
 #pragma unroll
   for (int n = 0; n < N; ++n) acc[n] = 0.f;
   if (warp < kRowWarps) {
-    const int tile = warp >> 2, first = row0 + 32 * warp;
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane 32 (warp % 4) of tensor memory
-    const uint32_t a_at = tmem + lanes + tile * 2 * kAColumns;
-    const uint32_t d_at = tmem + lanes + 4 * kAColumns + tile * 2 * N;
-    // copies: piece lane % kPieces of row k 32 / kPieces + lane / kPieces
-    const int row_bytes = (a.n_in + 1) / 2, whole = a.n_in / SEG;
-    const uint8_t* src[kPieces];
-    uint32_t dst[kPieces];
-    const uint32_t ring = smem_u32(w_ring) + warp * kRingBytes;
-    const auto place = [&](int r, int p) { return (uint32_t)((r * kPieces + (p ^ ((r * kPieces >> 3) & (kPieces - 1)))) * 16); };
-#pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-      const int r = k * (32 / kPieces) + lane / kPieces, p = lane % kPieces;
-      src[k] = a.w + (int64_t)min(first + r, a.n_out - 1) * a.ws + p * 16;
-      dst[k] = ring + place(r, p);
-    }
+    const int first = row0 + 32 * warp;
+    const uint32_t mine = tmem + ((uint32_t)warp << 21);  // lane 32 warp of tensor memory
+    // A stage holds rows of kPieces pieces, exchanged so that reads of a piece
+    // by 8 rows meet every bank once (as the copies' swizzle does it).
+    const auto place = [&](int r, int p) { return (r * kPieces + (p ^ ((r * kPieces >> 3) & (kPieces - 1)))) * 16; };
+    // Unaligned rows are copied by the warps themselves, loaded a step before
+    // they are stored: 16-byte piece lane % kPieces of row lane / kPieces + k 32 / kPieces.
+    uint4 held[ALIGNED ? 1 : kPieces] = {};
+    int put = 0;  // stage of the next copy
     const auto fetch = [&](int s) {
-      if (s < count) {
-        const int step = begin + s, at = step * (SEG / 2);
-        const uint32_t to = (uint32_t)(s % kDepth) * kStageBytes;
+      if constexpr (!ALIGNED) {
+        const int p = lane % kPieces, at = (begin + s) * (kColumns / 2) + p * 16, stage = put == 0 ? kDepth - 1 : put - 1;
 #pragma unroll
         for (int k = 0; k < kPieces; ++k) {
-          if (step < whole) {
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst[k] + to), "l"(src[k] + at) : "memory");
-          } else {
-            const int bytes = max(0, min(16, row_bytes - at - (lane % kPieces) * 16));
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst[k] + to),
-                         "l"(bytes > 0 ? src[k] + at : a.w), "r"(bytes)
-                         : "memory");
-          }
+          const int r = 32 * warp + lane / kPieces + k * (32 / kPieces);
+          *reinterpret_cast<uint4*>(w_ring + stage * kStageBytes + place(r, p)) = held[k];
+          if (s < count)
+            held[k] = load_piece(a.w + (int64_t)min(row0 + r, a.n_out - 1) * a.ws + at, (a.n_in + 1) / 2 - at);
         }
+        put = put + 1 == kDepth ? 0 : put + 1;
       }
-      copy_commit();
     };
-    // this thread's row
+    // this thread's row: scales and zero points, loaded some steps ahead
     const int64_t scale_row = (int64_t)min(first + lane, a.n_out - 1) * a.groups;
-    const auto scale_of = [&](int s) {
-      const int64_t k = scale_row + min((begin + s) * SEG >> a.group_shift, a.groups - 1);
-      return a.scales_f32 ? __ldg(static_cast<const float*>(a.scales) + k) : to_f32(static_cast<const T*>(a.scales)[k]);
+    const char* scales = static_cast<const char*>(a.scales) + scale_row * (a.scales_f32 ? 4 : 2);
+    const uint8_t* zeros = a.zeros + (a.zeros ? scale_row : 0);
+    constexpr int kAhead = 2;
+    uint32_t scale_bits[kAhead][kGroups], zero_bits[kAhead][kGroups];
+    const auto ask = [&](int s, uint32_t (&sc)[kGroups], uint32_t (&z)[kGroups]) {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const int k = min(((begin + s) * kColumns + g * GROUP) >> a.group_shift, a.groups - 1);
+        if (a.scales_f32)
+          sc[g] = __ldg(reinterpret_cast<const uint32_t*>(scales) + k);
+        else
+          sc[g] = __ldg(reinterpret_cast<const unsigned short*>(scales) + k);
+        z[g] = 8u;
+        if (a.zeros) z[g] = __ldg(zeros + k);
+      }
     };
-    const auto zero_of = [&](int s) {
-      const int64_t k = scale_row + min((begin + s) * SEG >> a.group_shift, a.groups - 1);
-      return a.zeros ? (uint32_t)__ldg(a.zeros + k) & 15u : 8u;
+    const auto scale_from = [&](uint32_t bits) {
+      if (a.scales_f32) return __uint_as_float(bits);
+      if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half((unsigned short)bits));
+      return __uint_as_float(bits << 16);
     };
-    const auto add_up = [&](int s, float scale) {
-      const int b = s & 1;
-      wait_for(&bars.done[tile][b], (s >> 1) & 1, failed);
+    float before[kGroups] = {};
+    const auto wait_done = [&](int s) {  // (the instructions of step s)
+      wait_for(&bars.done, s & 1, failed);
       tmem_fence_after();
       __syncwarp();
-      constexpr int kAtOnce = N < 32 ? N : 32;
+    };
+    const auto add_up = [&] {
 #pragma unroll
-      for (int n0 = 0; n0 < N; n0 += kAtOnce) {
-        float d[kAtOnce / 16][16];
-#pragma unroll
-        for (int k = 0; k < kAtOnce / 16; ++k) tmem_load16(d_at + b * N + n0 + 16 * k, d[k]);
+      for (int n = 0; n < N * kGroups; n += 16) {
+        float d[16];
+        tmem_load16(mine + kSums + n, d);
         tmem_wait_load();
 #pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) acc[n0 + k] = fmaf(scale, d[k / 16][k % 16], acc[n0 + k]);
+        for (int k = 0; k < 16; ++k) acc[n % N + k] = fmaf(before[n / N], d[k], acc[n % N + k]);
       }
     };
-#pragma unroll
     for (int k = 0; k < kDepth - 1; ++k) fetch(k);
-    float before2 = 0.f, before1 = 0.f, now = 0.f, next = count > 0 ? scale_of(0) : 0.f;
-    uint32_t next_zero = count > 0 ? zero_of(0) : 8u;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) scale_bits[k][g] = 0, zero_bits[k][g] = 8;
+      if (k < count) ask(k, scale_bits[k], zero_bits[k]);
+    }
+    int get = 0, turn = 0;  // stage of this step
     for (int s = 0; s < count; ++s) {
-      const int b = s & 1;
-      before2 = before1, before1 = now, now = next;
-      Unpack<T> un;
-      un.set(next_zero);
-      if (s + 1 < count) next = scale_of(s + 1), next_zero = zero_of(s + 1);
-      copy_wait<kDepth - 2>();
-      __syncwarp();
-      fetch(s + kDepth - 1);
-      if (s >= 2) add_up(s - 2, before2);
-      const unsigned char* stage = w_ring + warp * kRingBytes + (s % kDepth) * kStageBytes;
+      const unsigned char* stage = w_ring + get * kStageBytes;
+      if constexpr (ALIGNED) {
+        wait_for(&bars.w_full[get], turn, failed);
+      } else {
+        __syncwarp();
+        fetch(s + kDepth - 1);
+      }
+      if (++get == kDepth) get = 0, turn ^= 1;
+      Unpack<T> un[kGroups];
 #pragma unroll
-      for (int p = 0; p < kPieces; ++p) {
-        const uint4 v = *reinterpret_cast<const uint4*>(stage + place(lane, p));
+      for (int g = 0; g < kGroups; ++g) un[g].set(zero_bits[0][g] & 15u);
+      const auto unpack = [&](int p, uint32_t (&r)[16]) {
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + place(me, p));
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t r[16];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t e[4];
-          un.run(w[k], e);
+        for (int j = 0; j < 4; ++j) un[p * 32 / GROUP].run(w[j], reinterpret_cast<uint32_t(&)[4]>(r[4 * j]));
+      };
+      // the first pieces while the last step's instructions are at work
+      constexpr int kPre = S::kPre < kPieces ? S::kPre : kPieces;
+      uint32_t r[kPre][16];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) r[4 * k + j] = e[j];
-        }
-        tmem_store16(a_at + b * kAColumns + 16 * p, r);
+      for (int p = 0; p < kPre; ++p) unpack(p, r[p]);
+      if (s >= 1) wait_done(s - 1);
+#pragma unroll
+      for (int p = 0; p < kPre; ++p) tmem_store16(mine + 16 * p, r[p]);
+      if (s >= 1) add_up();
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        before[g] = scale_from(scale_bits[0][g]);
+#pragma unroll
+        for (int k = 0; k + 1 < kAhead; ++k)
+          scale_bits[k][g] = scale_bits[k + 1][g], zero_bits[k][g] = zero_bits[k + 1][g];
+      }
+      if (s + kAhead < count) ask(s + kAhead, scale_bits[kAhead - 1], zero_bits[kAhead - 1]);
+#pragma unroll
+      for (int p = kPre; p < kPieces; ++p) {
+        uint32_t e[16];
+        unpack(p, e);
+        tmem_store16(mine + 16 * p, e);
       }
       tmem_wait_store();
       tmem_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.a_full[tile][b]);
+      if (lane == 0) mbar_arrive(&bars.a_full);
     }
-    if (count >= 2) add_up(count - 2, before1);
-    if (count >= 1) add_up(count - 1, now);
-    copy_wait<0>();
-  } else if (warp < kRowWarps + kXWarps) {
-    // x into the operand's layout: rows of kLine bytes (tokens), 16-byte pieces
-    // exchanged by the row's number; within a piece the order of Unpack
-    constexpr int kChunks = SEG / 8, kMine = N * kChunks / (kXWarps * 32);
-    const int id = me - kRowWarps * 32;
-    for (int s = 0; s < count; ++s) {
-      const int stage = s % kXStages;
-      if (s >= kXStages) wait_for(&bars.x_empty[stage], ((s / kXStages) - 1) & 1, failed);
-      constexpr int kAtOnce = kMine < 8 ? kMine : 8;
-#pragma unroll
-      for (int j0 = 0; j0 < kMine; j0 += kAtOnce) {
-        uint4 v[kAtOnce];
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-          const int c = id + (j0 + j) * kXWarps * 32, n = c / kChunks, col = (begin + s) * SEG + (c % kChunks) * 8;
-          const T* from = static_cast<const T*>(a.x) + (int64_t)(token0 + n) * a.xs + col;
-          v[j] = load_x(from, token0 + n < a.n_tokens ? a.n_in - col : 0, true);
-        }
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-          const int c = id + (j0 + j) * kXWarps * 32, n = c / kChunks, kc = c % kChunks;
-          uint32_t at = (uint32_t)(n * kLine + (kc % (kLine / 16)) * 16);
-          at ^= (at >> 3) & (kLine == 128 ? 0x70u : 0x30u);
-          at += (uint32_t)(kc / (kLine / 16)) * (N * kLine);
-          *reinterpret_cast<uint4*>(x_ring + stage * kXBytes + at) =
-              make_uint4(__byte_perm(v[j].x, v[j].z, 0x5410), __byte_perm(v[j].x, v[j].z, 0x7632),
-                         __byte_perm(v[j].y, v[j].w, 0x5410), __byte_perm(v[j].y, v[j].w, 0x7632));
-        }
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(&bars.x_full[stage]);
+    if (count >= 1) {
+      wait_done(count - 1);
+      add_up();
     }
   } else {
-    if (lane == 0) {
-      // fp32 sums; both operands of T, with columns along the rows; N tokens, 128 rows
-      const uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
-      const uint32_t kind = 1u << 4 | type << 7 | type << 10 | (uint32_t)(N / 8) << 17 | 8u << 24;
-      // rows of kLine bytes in groups of eight; bits 46-47: version, 61-63: swizzle
-      const uint64_t base = (uint64_t)(8 * kLine >> 4) << 32 | 1ull << 46 | (uint64_t)(kLine == 128 ? 2 : 4) << 61 | 1ull << 16;
-      for (int s = 0; s < count; ++s) {
-        const int b = s & 1, stage = s % kXStages;
-        wait_for(&bars.x_full[stage], (s / kXStages) & 1, failed);
-        const uint32_t x_at = smem_u32(x_ring + stage * kXBytes);
+    // (all lanes go through the loop together, so that the operands' addresses
+    // are the same in all of them, and one issues)
+    const bool leads = elect_lane();
+    // x: a step's image, once the step that had its stage is done
+    const char* image = reinterpret_cast<const char*>(a.image) + ((int64_t)blockIdx.y * steps + begin) * S::kXBytes;
+    const uint32_t x_first = __shfl_sync(0xffffffffu, smem_u32(x_ring), 0);
+    const auto fetch_x = [&](int s, int stage) {
+      if (s >= count || !leads) return;
+      mbar_arrive_expect_tx(&bars.x_full[stage], S::kXBytes);
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+              x_first + stage * S::kXBytes),
+          "l"(image + (int64_t)s * S::kXBytes), "r"(S::kXBytes), "r"(smem_u32(&bars.x_full[stage]))
+          : "memory");
+    };
+    // W: a step of all rows, once the step that had its stage is unpacked
+    const uint32_t w_first = __shfl_sync(0xffffffffu, smem_u32(w_ring), 0);
+    const auto fetch_w = [&](int s, int stage) {
+      if (!ALIGNED || s >= count || !leads) return;
+      mbar_arrive_expect_tx(&bars.w_full[stage], kStageBytes);
+      asm volatile(
+          "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+          "[%4];" ::"r"(w_first + stage * kStageBytes),
+          "l"(&w_map), "r"((begin + s) * (kColumns / 2)), "r"(row0), "r"(smem_u32(&bars.w_full[stage]))
+          : "memory");
+    };
+    for (int k = 0; k < kDepth; ++k) fetch_w(k, k);
+    pdl_wait();  // (the image)
+    for (int k = 0; k < S::kXStages; ++k) fetch_x(k, k);
+    // fp32 sums; both operands of T, with columns along the rows; N tokens, 128 rows
+    constexpr uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
+    constexpr uint32_t kind = 1u << 4 | type << 7 | type << 10 | (uint32_t)(N / 8) << 17 | 8u << 24;
+    // rows of kLine bytes in groups of eight; bits 46-47: version, 61-63: swizzle
+    constexpr uint64_t base =
+        (uint64_t)(8 * S::kLine >> 4) << 32 | 1ull << 46 | (uint64_t)(S::kLine == 128 ? 2 : 4) << 61 | 1ull << 16;
+    const uint32_t at_tmem = __shfl_sync(0xffffffffu, tmem, 0);
+    int stage = 0, turn = 0, w_stage = 0;  // of the rings
+    for (int s = 0; s < count; ++s) {
+      wait_for(&bars.x_full[stage], turn, failed);
+      wait_for(&bars.a_full, s & 1, failed);  // (and step s - 1 is done)
+      __syncwarp();
+      tmem_fence_after();
+      const uint64_t x_at = base | (uint64_t)((x_first + stage * S::kXBytes) >> 4);
+      if (leads) {
 #pragma unroll
-        for (int tile = 0; tile < 2; ++tile) {
-          wait_for(&bars.a_full[tile][b], (s >> 1) & 1, failed);
-          tmem_fence_after();
-          const uint32_t d = tmem + 4 * kAColumns + (tile * 2 + b) * N, op = tmem + (tile * 2 + b) * kAColumns;
-#pragma unroll
-          for (int k = 0; k < SEG / 16; ++k) {
-            const uint32_t at = x_at + (k * 32 / kLine) * (N * kLine) + k * 32 % kLine;
-            tile_mma(d, op + 8 * k, base | (uint64_t)((at >> 4) & 0x3fff), kind, k > 0);
-          }
-          tile_commit(&bars.done[tile][b]);
-        }
-        tile_commit(&bars.x_empty[stage]);
+        for (int k = 0; k < kColumns / 16; ++k)
+          tile_mma(at_tmem + kSums + k * 16 / GROUP * N, at_tmem + 8 * k,
+                   x_at + (((k * 32 / S::kLine) * (N * S::kLine) + k * 32 % S::kLine) >> 4), kind, k * 16 % GROUP != 0);
+        tile_commit(&bars.done);
       }
-      tile_commit(&bars.last);
-      if (!mbar_wait_bounded(&bars.last, 0)) *failed = 1;  // (tensor memory is given back behind it)
+      fetch_w(s + kDepth, w_stage);
+      if (++w_stage == kDepth) w_stage = 0;
+      if (s >= 1) fetch_x(s - 1 + S::kXStages, stage == 0 ? S::kXStages - 1 : stage - 1);
+      if (++stage == S::kXStages) stage = 0, turn ^= 1;
     }
+    if (leads) tile_commit(&bars.last);
+    if (!mbar_wait_bounded(&bars.last, 0)) *failed = 1;  // (tensor memory is given back behind it)
     __syncwarp();
   }
 
@@ -626,7 +515,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) int4_tiles(Int4Args a) {
   float* sums = reinterpret_cast<float*>(s_tiles);
   if (warp < kRowWarps) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) sums[n * kTileRows + 32 * warp + lane] = acc[n];
+    for (int n = 0; n < N; ++n) sums[n * kTileRows + me] = acc[n];
   }
   tmem_fence_before();
   cg::cluster_group cluster = cg::this_cluster();
@@ -634,21 +523,59 @@ __global__ void __launch_bounds__(kTileThreads, 1) int4_tiles(Int4Args a) {
     cluster.sync();
   else
     __syncthreads();
-  if (warp == kRowWarps + kXWarps) {
+  if (warp == kRowWarps) {
     tmem_fence_after();
-    tmem_free(tmem, kColumns);
+    tmem_free<kTensorColumns>(tmem);
   }
-  const int lo = kTileRows * rank / a.split, rows = kTileRows * (rank + 1) / a.split - lo;
-  const int tokens = min(N, a.n_tokens - token0);
-  for (int e = me; e < rows * tokens; e += kTileThreads) {
-    const int n = e / rows, r = lo + e % rows;
-    if (row0 + r >= a.n_out) continue;
-    float v = 0.f;
-    for (int k = 0; k < a.split; ++k)
-      v += (a.split > 1 ? cluster.map_shared_rank(sums, k) : sums)[n * kTileRows + r];
-    if (*failed) v = NAN;
-    if (a.base) v += load_as_f32(a.base, a.y_dtype, (int64_t)(token0 + n) * a.bs + row0 + r);
-    store_from_f32(a.y, a.y_dtype, (int64_t)(token0 + n) * a.ys + row0 + r, v);
+  // four rows at a time: 32 of these for each token, in equal shares to the CTAs
+  const int lo = 32 * rank / a.split, fours = 32 * (rank + 1) / a.split - lo;
+  const int items = fours * min(N, a.n_tokens - token0);
+  constexpr int kAtOnce = 4;
+  for (int e0 = me; e0 < items; e0 += kAtOnce * kTileThreads) {
+    float4 v[kAtOnce], add[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int e = e0 + j * kTileThreads, n = e / fours, r = 4 * (lo + e % fours);
+      v[j] = add[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (a.base && e < items) {
+        const int64_t at = (int64_t)(token0 + n) * a.bs + row0 + r;
+        if (a.vec_y) {
+          if (row0 + r < a.n_out) add[j] = load_four(a.base, a.y_dtype, at);
+        } else {
+          if (row0 + r < a.n_out) add[j].x = load_as_f32(a.base, a.y_dtype, at);
+          if (row0 + r + 1 < a.n_out) add[j].y = load_as_f32(a.base, a.y_dtype, at + 1);
+          if (row0 + r + 2 < a.n_out) add[j].z = load_as_f32(a.base, a.y_dtype, at + 2);
+          if (row0 + r + 3 < a.n_out) add[j].w = load_as_f32(a.base, a.y_dtype, at + 3);
+        }
+      }
+    }
+    for (int k = 0; k < a.split; ++k) {
+      const float* from = a.split > 1 ? cluster.map_shared_rank(sums, k) : sums;
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int e = e0 + j * kTileThreads;
+        if (e < items) {
+          const float4 u = *reinterpret_cast<const float4*>(from + e / fours * kTileRows + 4 * (lo + e % fours));
+          v[j].x += u.x, v[j].y += u.y, v[j].z += u.z, v[j].w += u.w;
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int e = e0 + j * kTileThreads, n = e / fours, r = 4 * (lo + e % fours);
+      if (e >= items) continue;
+      float4 u = make_float4(v[j].x + add[j].x, v[j].y + add[j].y, v[j].z + add[j].z, v[j].w + add[j].w);
+      if (*failed) u = make_float4(NAN, NAN, NAN, NAN);
+      const int64_t at = (int64_t)(token0 + n) * a.ys + row0 + r;
+      if (a.vec_y) {
+        if (row0 + r < a.n_out) store_four(a.y, a.y_dtype, at, u);
+      } else {
+        if (row0 + r < a.n_out) store_from_f32(a.y, a.y_dtype, at, u.x);
+        if (row0 + r + 1 < a.n_out) store_from_f32(a.y, a.y_dtype, at + 1, u.y);
+        if (row0 + r + 2 < a.n_out) store_from_f32(a.y, a.y_dtype, at + 2, u.z);
+        if (row0 + r + 3 < a.n_out) store_from_f32(a.y, a.y_dtype, at + 3, u.w);
+      }
+    }
   }
   if (a.split > 1) cluster.sync();  // (the others read this CTA's sums)
 }
@@ -663,48 +590,85 @@ __global__ void int4_copy(Int4Args a) {
   }
 }
 
-template <typename T, int NT, int SEG>
-spmv_status launch_rows(const Int4Args& a, cudaStream_t st) {
-  const bool fast = aligned_to(a.w, 16) && (a.n_out <= 1 || a.ws % 16 == 0) && a.vec_x;
-  void (*fn)(Int4Args) = fast ? &int4_rows<T, NT, SEG, true> : &int4_rows<T, NT, SEG, false>;
-  const int64_t blocks = (a.n_out + kRows - 1ll) / kRows, groups = (a.n_tokens + 8ll * NT - 1) / (8 * NT);
-  // as many warps to a CTA as one wave of 24 warps per SM has for it
-  int warps = 4;
-  while (warps < kMaxWarps && blocks * groups * warps * 2 <= 24 * 152) warps *= 2;
-  const size_t ring = (size_t)warps * kRing * kStage;
-  const size_t sums = (size_t)warps * 8 * NT * (kRows + 1) * 4;
-  const size_t smem = ring > sums ? ring : sums;
-  if (!allow_smem(reinterpret_cast<const void*>(fn), smem)) return SPMV_ERR_CUDA;
-  return launch(fn, dim3((unsigned)blocks, (unsigned)groups), warps * 32, smem, st, a);
+// Clusters of k CTAs that 152 SMs hold at one CTA to an SM (as the occupancy
+// query has them).
+constexpr int kClusters[kMaxSplit + 1] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+
+// Tokens taken together, and bytes of their image.
+int tokens_at_once(int64_t n_tokens) { return n_tokens <= 16 ? 16 : n_tokens <= 32 ? 32 : 64; }
+int64_t image_bytes(int64_t n_tokens, int64_t n_in) {
+  const int64_t n = tokens_at_once(n_tokens);
+  return (n_tokens + n - 1) / n * n * ((n_in + 127) / 128 * 128) * 2;
 }
 
-template <typename T, int N, int SEG>
+// W as a matrix of bytes of which a copy takes 128 rows of `bytes` columns,
+// pieces of 16 bytes exchanged as the kernel's place() has them. False if the
+// copy engine cannot address it so.
+bool map_weights(const Int4Args& a, int bytes, CUtensorMap* map) {
+  static const auto encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
+            cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      fn = nullptr;
+    }
+    return reinterpret_cast<CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                         const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                         CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill)>(fn);
+  }();
+  if (!encode) return false;
+  const int64_t row_bytes = (a.n_in + 1ll) / 2;
+  const int64_t stride = a.n_out == 1 ? (row_bytes + 15) / 16 * 16 : a.ws;
+  const cuuint64_t size[2] = {(cuuint64_t)row_bytes, (cuuint64_t)a.n_out};
+  const cuuint64_t strides[1] = {(cuuint64_t)stride};
+  const cuuint32_t box[2] = {(cuuint32_t)bytes, kTileRows}, one[2] = {1, 1};
+  const CUtensorMapSwizzle swizzle = bytes == 64   ? CU_TENSOR_MAP_SWIZZLE_64B
+                                     : bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                                   : CU_TENSOR_MAP_SWIZZLE_NONE;
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.w), size, strides, box, one,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int N, int GROUP>
 spmv_status launch_tiles(Int4Args a, cudaStream_t st) {
-  const void* fn = reinterpret_cast<const void*>(&int4_tiles<T, N, SEG>);
-  const size_t rings = (size_t)kXStages * N * SEG * 2 + (size_t)kRowWarps * kRingBytes;
+  using S = Step<N, GROUP>;
+  CUtensorMap w_map{};
+  const bool aligned = aligned_to(a.w, 16) && (a.n_out == 1 || (a.ws % 16 == 0 && a.ws > 0)) &&
+                       map_weights(a, S::kColumns / 2, &w_map);
+  const void* fn = aligned ? reinterpret_cast<const void*>(&int4_tiles<T, N, GROUP, true>)
+                           : reinterpret_cast<const void*>(&int4_tiles<T, N, GROUP, false>);
   const size_t sums = (size_t)N * kTileRows * 4;
-  // (more than half of an SM's: two CTAs there would share its tensor memory)
-  size_t smem = (rings > sums ? rings : sums) + 1024;
-  if (smem < 120 * 1024) smem = 120 * 1024;
+  // (more than a fifth of an SM's, as no more than four may share its tensor memory)
+  size_t smem = (S::kRings > sums ? S::kRings : sums) + 1024;
+  if (smem < 47 * 1024) smem = 47 * 1024;
   if (!allow_smem(fn, smem)) return SPMV_ERR_CUDA;
   const int64_t blocks = (a.n_out + kTileRows - 1ll) / kTileRows, groups = (a.n_tokens + N - 1ll) / N;
-  // the columns over as many CTAs as the device holds together
+  // The columns over as many CTAs as the device holds together, each with four
+  // steps at least.
+  const int64_t steps = (a.n_in + S::kColumns - 1) / S::kColumns, per_sm = S::kPerSm;
   a.split = kMaxSplit;
-  while (a.split > 1 && (blocks * groups * a.split > 152 ||
-                         resident_clusters(fn, a.split, kTileThreads, smem) < blocks * groups))
-    --a.split;
+  while (a.split > 1 && (blocks * groups > kClusters[a.split] * per_sm || steps < 4 * a.split)) --a.split;
+  const int64_t pieces = steps * (S::kColumns / 8) * N;
+  const spmv_status laid_out = launch(int4_image<T, N, GROUP>, dim3((unsigned)((pieces + 255) / 256), (unsigned)groups),
+                                      256, 0, st, a);
+  if (laid_out != SPMV_OK) return laid_out;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(blocks * a.split), (unsigned)groups);
   cfg.blockDim = dim3(kTileThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)a.split;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  void* args[] = {&a};
+  cfg.numAttrs = 2;
+  void* args[] = {&a, &w_map};
   return status_of(cudaLaunchKernelExC(&cfg, fn, args));
 }
 
@@ -714,12 +678,6 @@ spmv_status tile_groups(const Int4Args& a, cudaStream_t st) {
   return a.group_shift == 6 ? launch_tiles<T, N, 64>(a, st) : launch_tiles<T, N, 32>(a, st);
 }
 
-template <typename T, int NT>
-spmv_status launch_groups(const Int4Args& a, cudaStream_t st) {
-  if (a.group_shift >= 7) return launch_rows<T, NT, 128>(a, st);
-  return a.group_shift == 6 ? launch_rows<T, NT, 64>(a, st) : launch_rows<T, NT, 32>(a, st);
-}
-
 template <typename T>
 spmv_status run_int4(const Int4Args& a, cudaStream_t st) {
   if (a.n_in == 0) {
@@ -727,13 +685,8 @@ spmv_status run_int4(const Int4Args& a, cudaStream_t st) {
     const int64_t blocks = ((int64_t)a.n_tokens * a.n_out + 255) / 256;
     return launch(int4_copy, dim3((unsigned)(blocks < 1216 ? blocks : 1216)), 256, 0, st, a);
   }
-  const bool fast = aligned_to(a.w, 16) && (a.n_out <= 1 || a.ws % 16 == 0) && a.vec_x;
-  if (fast) {
-    if (a.n_tokens <= 16) return tile_groups<T, 16>(a, st);
-    return a.n_tokens <= 32 ? tile_groups<T, 32>(a, st) : tile_groups<T, 64>(a, st);
-  }
-  if (a.n_tokens <= 8) return launch_groups<T, 1>(a, st);
-  return a.n_tokens <= 16 ? launch_groups<T, 2>(a, st) : launch_groups<T, 4>(a, st);
+  const int n = tokens_at_once(a.n_tokens);
+  return n == 16 ? tile_groups<T, 16>(a, st) : n == 32 ? tile_groups<T, 32>(a, st) : tile_groups<T, 64>(a, st);
 }
 
 }  // namespace
@@ -741,11 +694,17 @@ spmv_status run_int4(const Int4Args& a, cudaStream_t st) {
 
 using namespace spmv;
 
+extern "C" int64_t spmv_int4_workspace(int32_t n_tokens, int32_t n_in) {
+  if (n_tokens < 1 || n_in < 1 || n_tokens > (1 << 18) || n_in > (1 << 30)) return 0;
+  return image_bytes(n_tokens, n_in);
+}
+
 extern "C" spmv_status spmv_int4_run(int32_t n_tokens, int32_t n_in, int32_t n_out, int32_t group,
                                      spmv_dtype dtype, const void* x, int64_t x_stride, const uint8_t* weights,
                                      int64_t weights_stride, const void* scales, spmv_dtype scales_dtype,
                                      const uint8_t* zeros, const void* base, int64_t base_stride, void* y,
-                                     spmv_dtype y_dtype, int64_t y_stride, void* stream) {
+                                     spmv_dtype y_dtype, int64_t y_stride, void* workspace, int64_t workspace_bytes,
+                                     void* stream) {
   if (n_tokens < 0 || n_in < 0 || n_out < 0 || group < 1 || !op_dtype(dtype) || !op_dtype(scales_dtype) ||
       !op_dtype(y_dtype))
     return SPMV_ERR_INVALID_ARG;
@@ -761,9 +720,11 @@ extern "C" spmv_status spmv_int4_run(int32_t n_tokens, int32_t n_in, int32_t n_o
       !matrix_ok(weights, n_out, row_bytes, weights_stride, 1, false) ||
       (base && !matrix_ok(base, n_tokens, n_out, base_stride, ysz, false)) ||
       !matrix_ok(y, n_tokens, n_out, y_stride, ysz, true) || (n_out > 0 && groups > 0 && !scales) ||
-      !aligned_to(scales, op_dtype_size(scales_dtype)))
+      !aligned_to(scales, op_dtype_size(scales_dtype)) || !aligned_to(workspace, 16))
     return SPMV_ERR_INVALID_ARG;
   if (n_tokens == 0 || n_out == 0) return SPMV_OK;
+  const int64_t need = spmv_int4_workspace(n_tokens, n_in);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return SPMV_ERR_INVALID_ARG;
   const bool in_place = base == y && (base_stride == y_stride || n_tokens == 1);
   const auto meets_y = [&](const void* p, int64_t rows, int64_t cols, int64_t stride, int64_t size) {
     return spans_overlap(p, rows, cols, stride, size, y, n_tokens, n_out, y_stride, ysz);
@@ -771,18 +732,23 @@ extern "C" spmv_status spmv_int4_run(int32_t n_tokens, int32_t n_in, int32_t n_o
   if ((!in_place && meets_y(base, n_tokens, n_out, base_stride, ysz)) || meets_y(x, n_tokens, n_in, x_stride, 2) ||
       meets_y(weights, n_out, row_bytes, weights_stride, 1) ||
       meets_y(scales, 1, n_out * groups, n_out * groups, op_dtype_size(scales_dtype)) ||
-      meets_y(zeros, 1, n_out * groups, n_out * groups, 1))
+      meets_y(zeros, 1, n_out * groups, n_out * groups, 1) || meets_y(workspace, 1, need, need, 1) ||
+      spans_overlap(x, n_tokens, n_in, x_stride, 2, workspace, 1, need, need, 1) ||
+      spans_overlap(weights, n_out, row_bytes, weights_stride, 1, workspace, 1, need, need, 1))
     return SPMV_ERR_INVALID_ARG;
   Int4Args a{};
-  a.n_tokens = n_tokens, a.n_in = n_in, a.n_out = n_out, a.group = group, a.groups = (int)groups;
+  a.n_tokens = n_tokens, a.n_in = n_in, a.n_out = n_out, a.groups = (int)groups;
   a.x = x, a.xs = x_stride, a.w = weights, a.ws = weights_stride;
   a.scales = scales, a.zeros = zeros, a.base = base, a.bs = base_stride, a.y = y, a.ys = y_stride;
   a.y_dtype = y_dtype;
   a.scales_f32 = scales_dtype == SPMV_F32;
-  a.group_shift = 31;  // (one group)
+  a.image = static_cast<uint4*>(workspace);
+  a.group_shift = 30;  // (one group: columns behind the last one included)
   if (group < n_in)
     for (a.group_shift = 5; (1 << a.group_shift) < group;) ++a.group_shift;
   a.vec_x = rows_aligned(x, n_tokens, x_stride, 2, 8);
+  a.vec_y = n_out % 4 == 0 && rows_aligned(y, n_tokens, y_stride, ysz, 4) &&
+            (!base || rows_aligned(base, n_tokens, base_stride, ysz, 4));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return dtype == SPMV_F16 ? run_int4<__half>(a, st) : run_int4<__nv_bfloat16>(a, st);
 }

@@ -326,7 +326,15 @@ def spmv_logits_process(logits, out, prompt=None, output=None, repetition=None, 
            "spmv_logits_process")
 
 
-def spmv_int4_run(x, weights, scales, y, group: int, zeros=None, base=None, stream=None) -> None:
+def spmv_int4_workspace(n_tokens: int, n_in: int) -> int:
+    """Bytes of workspace that spmv_int4_run needs (0 for sizes it refuses)."""
+    if min(n_tokens, n_in) < 0 or max(n_tokens, n_in) > _INT32_MAX:
+        return 0
+    return int(_lib_handle().spmv_int4_workspace(n_tokens, n_in))
+
+
+def spmv_int4_run(x, weights, scales, y, group: int, zeros=None, base=None, workspace=None,
+                  stream=None) -> None:
     """y[t] = base[t] + W @ x[t], W[o, i] = scales[o, i // group] * (q[o, i] - zeros[o, i // group]).
     x: (tokens, n_in) float16 or bfloat16 (a vector is one token); weights:
     (n_out, ceil(n_in / 2)) uint8, column i in the low (i even) or high half of
@@ -358,13 +366,16 @@ def spmv_int4_run(x, weights, scales, y, group: int, zeros=None, base=None, stre
             raise ValueError("base and y must have the same shape")
         if base.dtype != y.dtype:
             raise TypeError(f"base must be {y.dtype}, got {base.dtype}")
-    dev = _same_device(x, y, weights, scales, zeros, base)
-    _check(_lib_handle().spmv_int4_run(
+    dev = _same_device(x, y, weights, scales, zeros, base, workspace)
+    handle = _on(stream, dev)
+    lib = _lib_handle()
+    wp, wn, _owner = _workspace(workspace, lib.spmv_int4_workspace(t, n_in), handle, dev)
+    _check(lib.spmv_int4_run(
         t, n_in, n_out, group, _dtype(x, "x"), x.data_ptr(), xs, weights.data_ptr(), ws,
         scales.data_ptr(), _dtype(scales, "scales"),
         _vector(zeros, n_out * groups, torch.uint8, "zeros"),
-        None if base is None else base.data_ptr(), bs, y.data_ptr(), _dtype(y, "y"), ys,
-        _on(stream, dev)), "spmv_int4_run")
+        None if base is None else base.data_ptr(), bs, y.data_ptr(), _dtype(y, "y"), ys, wp, wn,
+        handle), "spmv_int4_run")
 
 
 def spmv_verify_workspace(n_requests: int, n_drafts: int, vocab: int) -> int:

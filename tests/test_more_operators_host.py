@@ -16,13 +16,15 @@ HUGE = 2 ** 31 - 1
 
 
 def int4(lib, **kw):
-    a = dict(t=4, i=256, o=32, g=64, dt=F16, x=X, xs=256, w=W, ws=128, sc=SC, st=F32, z=Z, b=B, bs=32, y=Y, yt=F32, ys=32)
+    a = dict(t=4, i=256, o=32, g=64, dt=F16, x=X, xs=256, w=W, ws=128, sc=SC, st=F32, z=Z, b=B, bs=32, y=Y, yt=F32, ys=32, wk=WS,
+             wn=1 << 40)
     a.update(kw)
     return lib.spmv_int4_run(a["t"], a["i"], a["o"], a["g"], a["dt"], a["x"], a["xs"], a["w"], a["ws"], a["sc"], a["st"], a["z"], a["b"],
-                             a["bs"], a["y"], a["yt"], a["ys"], None)
+                             a["bs"], a["y"], a["yt"], a["ys"], a["wk"], a["wn"], None)
 
 
 @pytest.mark.parametrize("kw,status", [
+    (dict(wk=None), INVALID), (dict(wn=64), INVALID), (dict(wk=WS + 8), INVALID), (dict(wk=Y), INVALID), (dict(wk=X), INVALID), (dict(wk=W), INVALID),
     (dict(t=-1), INVALID), (dict(i=-1), INVALID), (dict(o=-1), INVALID), (dict(g=0), INVALID), (dict(g=-32), INVALID),
     (dict(dt=4), INVALID), (dict(st=-1), INVALID), (dict(yt=9), INVALID), (dict(x=None), INVALID), (dict(w=None), INVALID),
     (dict(sc=None), INVALID), (dict(y=None), INVALID), (dict(x=X + 1), INVALID), (dict(sc=SC + 2), INVALID), (dict(b=B + 2), INVALID),
@@ -36,6 +38,14 @@ def int4(lib, **kw):
 ])
 def test_int4_refuses(spmv_lib, kw, status):
     assert int4(spmv_lib, **kw) == status
+
+
+def test_int4_workspace(spmv_lib):
+    size = S.spmv_int4_workspace
+    assert size(0, 64) == 0 and size(-1, 64) == 0 and size(4, 0) == 0 and size(4, -64) == 0
+    assert size(2 ** 32 + 4, 64) == 0 and size(4, 2 ** 32 + 64) == 0 and size(2 ** 18 + 1, 64) == 0
+    n = size(4, 256)
+    assert n > 0 and int4(spmv_lib, wn=n - 1) == INVALID
 
 
 def verify(lib, **kw):

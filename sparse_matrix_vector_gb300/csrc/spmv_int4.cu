@@ -580,6 +580,240 @@ int4_tiles(const Int4Args a, const __grid_constant__ CUtensorMap w_map) {
   if (a.split > 1) cluster.sync();  // (the others read this CTA's sums)
 }
 
+// --------------------------------------------------------------- few tokens
+// Up to 16 tokens: 32 rows of W to a CTA, its warps at ranges of the columns of
+// their own, on the warp-level matrix instruction (16 rows of W x 8 tokens x 16
+// columns). A warp waits for nothing but its own copies, which is worth more
+// here than the tensor cores' rate.
+constexpr int kFewStep = 128;  // columns that a warp takes at a time
+constexpr int kFewDepth = 4;
+constexpr int kFewWarps = 16;  // of a CTA, at most
+
+// Column of the step that word w of lane q's share begins with, 8 columns each:
+// a SEG's columns are spread over the four lanes that a sum joins.
+template <int SEG>
+__host__ __device__ constexpr int column_of(int w, int q) {
+  return SEG == 128 ? 32 * q + 8 * w : SEG == 64 ? 64 * (w >> 1) + 16 * q + 8 * (w & 1) : 32 * w + 8 * q;
+}
+
+// x as the instructions' B operands: [tokens / 8][step][word][lane].
+template <typename T, int SEG>
+__global__ void __launch_bounds__(256) int4_image_few(Int4Args a) {
+  pdl_launch_dependents();
+  const int64_t steps = (a.n_in + kFewStep - 1) / kFewStep;
+  const int64_t id = blockIdx.x * 256ll + threadIdx.x;
+  if (id >= steps * 128) return;
+  const int lane = (int)(id & 31), w = (int)(id >> 5) & 3, t = blockIdx.y * 8 + (lane >> 2);
+  const int64_t col = (id >> 7) * kFewStep + column_of<SEG>(w, lane & 3);
+  const uint4 v = load_x(static_cast<const T*>(a.x) + t * a.xs + col,
+                         t < a.n_tokens && col < a.n_in ? (int)min((int64_t)8, a.n_in - col) : 0, a.vec_x);
+  a.image[blockIdx.y * steps * 128 + id] =
+      make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                 __byte_perm(v.y, v.w, 0x7632));
+}
+
+template <typename T>
+__device__ __forceinline__ void mma_few(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Registers of a thread, and so warps of an SM.
+constexpr int few_registers(int mt, int nt) { return mt == 1 ? (nt == 1 ? 72 : 96) : nt == 1 ? 104 : 128; }
+
+// NT: tokens / 8. SEG: columns whose sums are scaled together (a group, or a
+// step of a longer one).
+template <typename T, int MT, int NT, int SEG, bool ALIGNED>
+__global__ void __maxnreg__(few_registers(MT, NT))
+int4_few(const Int4Args a, const __grid_constant__ CUtensorMap w_map) {
+  constexpr int kWords = SEG / 32, kSegs = kFewStep / SEG, kRows = 16 * MT, kStage = kRows * kFewStep / 2;
+  extern __shared__ __align__(1024) unsigned char s_raw[];
+  __shared__ uint64_t w_full[kFewWarps][kFewDepth];
+  __shared__ int s_failed;
+  unsigned char* s_few = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);
+  const int me = threadIdx.x, warp = me >> 5, lane = me & 31, g = lane >> 2, q = lane & 3;
+  const int warps = (int)blockDim.x >> 5, row0 = blockIdx.x * kRows;
+  const int steps = (a.n_in + kFewStep - 1) / kFewStep;
+  const int begin = (int)((int64_t)steps * warp / warps), end = (int)((int64_t)steps * (warp + 1) / warps);
+  unsigned char* ring = s_few + warp * kFewDepth * kStage;
+  volatile int* failed = &s_failed;
+  if (lane == 0) {
+    for (int k = 0; k < kFewDepth; ++k) mbar_init(&w_full[warp][k], 1);
+    fence_mbar_init();
+    s_failed = 0;
+  }
+  __syncthreads();
+
+  // rows of 64 bytes, whose 16-byte pieces are exchanged as the copies' swizzle does it
+  const auto place = [](int r, int p) { return r * 64 + ((p ^ ((r >> 1) & 3)) << 4); };
+  uint4 held[ALIGNED ? 1 : 2 * MT] = {};  // (unaligned rows: loaded, to be stored a step later)
+  const auto fetch = [&](int i) {  // (of the warp's steps)
+    const int step = begin + i, stage = i & (kFewDepth - 1);
+    if constexpr (ALIGNED) {
+      if (lane == 0 && step < end) {
+        mbar_arrive_expect_tx(&w_full[warp][stage], kStage);
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+            "[%4];" ::"r"(smem_u32(ring) + stage * kStage),
+            "l"(&w_map), "r"(step * 64), "r"(row0), "r"(smem_u32(&w_full[warp][stage]))
+            : "memory");
+      }
+    } else {
+      const int at = step * 64 + q * 16, before = (i - 1) & (kFewDepth - 1);
+#pragma unroll
+      for (int k = 0; k < 2 * MT; ++k) {
+        *reinterpret_cast<uint4*>(ring + before * kStage + place(g + 8 * k, q)) = held[k];
+        if (step < end)
+          held[k] = load_piece(a.w + (int64_t)min(row0 + g + 8 * k, a.n_out - 1) * a.ws + at, (a.n_in + 1) / 2 - at);
+      }
+    }
+  };
+  // (aligned rows: kFewDepth steps ahead, unaligned ones two less)
+  constexpr int kAhead = ALIGNED ? kFewDepth : kFewDepth - 1;
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) fetch(k);
+
+  // scale and zero point of row `lane`, a segment ahead; every lane gets those
+  // of its own rows (g + 8 r) from the lanes that have them
+  const int64_t scale_row = (int64_t)min(row0 + lane % kRows, a.n_out - 1) * a.groups;
+  const char* scales = static_cast<const char*>(a.scales) + scale_row * (a.scales_f32 ? 4 : 2);
+  const uint8_t* zeros = a.zeros + (a.zeros ? scale_row : 0);
+  uint32_t scale_bits = 0, zero_bits = 8;
+  const auto ask = [&](int col) {
+    const int k = min(col >> a.group_shift, a.groups - 1);
+    if (a.scales_f32)
+      scale_bits = __ldg(reinterpret_cast<const uint32_t*>(scales) + k);
+    else
+      scale_bits = __ldg(reinterpret_cast<const unsigned short*>(scales) + k);
+    if (a.zeros) zero_bits = __ldg(zeros + k);
+  };
+  const auto scale_from = [&](uint32_t bits) {
+    if (a.scales_f32) return __uint_as_float(bits);
+    if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half((unsigned short)bits));
+    return __uint_as_float(bits << 16);
+  };
+  ask(begin * kFewStep);
+  // x, a step ahead
+  const uint4* image = a.image + (int64_t)begin * 128 + lane;
+  const int64_t image_pitch = (int64_t)steps * 128;
+  uint4 x[NT][4];
+  pdl_wait();  // (the image)
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[n][k] = make_uint4(0, 0, 0, 0);
+      if (begin < end) x[n][k] = __ldg(image + n * image_pitch + 32 * k);
+    }
+
+  float acc[MT][NT][4] = {};
+  for (int i = 0; i < end - begin; ++i) {
+    const int step = begin + i;
+    const unsigned char* stage = ring + (i & (kFewDepth - 1)) * kStage;
+    if constexpr (ALIGNED)
+      wait_for(&w_full[warp][i & (kFewDepth - 1)], (uint32_t)(i / kFewDepth) & 1u, failed);
+    else
+      fetch(i + kAhead);
+    __syncwarp();
+    uint32_t w[2 * MT][4];  // of rows g + 8 r: the lane's words of the step, a segment's together
+#pragma unroll
+    for (int r = 0; r < 2 * MT; ++r) {
+      const int row = g + 8 * r;
+      if constexpr (kWords == 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(stage + place(row, q));
+        w[r][0] = u.x, w[r][1] = u.y, w[r][2] = u.z, w[r][3] = u.w;
+      } else if constexpr (kWords == 2) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint2 u = *reinterpret_cast<const uint2*>(stage + place(row, 2 * h + (q >> 1)) + 8 * (q & 1));
+          w[r][2 * h] = u.x, w[r][2 * h + 1] = u.y;
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) w[r][h] = *reinterpret_cast<const uint32_t*>(stage + place(row, h) + 4 * q);
+      }
+    }
+    if constexpr (ALIGNED) {
+      __syncwarp();  // (all lanes have read the stage)
+      fetch(i + kAhead);
+    }
+    image += 128;
+#pragma unroll
+    for (int seg = 0; seg < kSegs; ++seg) {
+      const float mine = scale_from(scale_bits);
+      float scale[2 * MT];
+      Unpack<T> un[2 * MT];
+#pragma unroll
+      for (int r = 0; r < 2 * MT; ++r) {
+        scale[r] = __shfl_sync(0xffffffffu, mine, g + 8 * r);
+        un[r].set(8);
+      }
+      if (a.zeros) {
+#pragma unroll
+        for (int r = 0; r < 2 * MT; ++r) un[r].set(__shfl_sync(0xffffffffu, zero_bits, g + 8 * r) & 15u);
+      }
+      ask(step * kFewStep + (seg + 1) * SEG);  // (behind the last column: the last group's again)
+      float part[MT][NT][4] = {};
+#pragma unroll
+      for (int k = seg * kWords; k < (seg + 1) * kWords; ++k) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          uint32_t lo[4], hi[4];
+          un[2 * m].run(w[2 * m][k], lo);
+          un[2 * m + 1].run(w[2 * m + 1][k], hi);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_few<T>(part[m][n], lo[0], hi[0], lo[1], hi[1], x[n][k].x, x[n][k].y);
+            mma_few<T>(part[m][n], lo[2], hi[2], lo[3], hi[3], x[n][k].z, x[n][k].w);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          if (step + 1 < end) x[n][k] = __ldg(image + n * image_pitch + 32 * k);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[m][n][k] += scale[2 * m + (k >> 1)] * part[m][n][k];
+    }
+  }
+  __syncthreads();
+
+  // the warps' sums, joined in their order
+  constexpr int kPitch = kRows + 1;
+  float* sums = reinterpret_cast<float*>(s_few);
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        sums[(warp * 8 * NT + 8 * n + 2 * q + (k & 1)) * kPitch + 16 * m + 8 * (k >> 1) + g] = acc[m][n][k];
+  __syncthreads();
+  for (int e = me; e < kRows * min(8 * NT, a.n_tokens); e += (int)blockDim.x) {
+    const int r = e % kRows, t = e / kRows;
+    if (row0 + r >= a.n_out) continue;
+    float v = 0.f;
+    for (int k = 0; k < warps; ++k) v += sums[(k * 8 * NT + t) * kPitch + r];
+    if (*failed) v = NAN;
+    if (a.base) v += load_as_f32(a.base, a.y_dtype, (int64_t)t * a.bs + row0 + r);
+    store_from_f32(a.y, a.y_dtype, (int64_t)t * a.ys + row0 + r, v);
+  }
+}
+
 // y = base, or 0 (no columns).
 __global__ void int4_copy(Int4Args a) {
   const int64_t n = (int64_t)a.n_tokens * a.n_out;
@@ -601,10 +835,11 @@ int64_t image_bytes(int64_t n_tokens, int64_t n_in) {
   return (n_tokens + n - 1) / n * n * ((n_in + 127) / 128 * 128) * 2;
 }
 
-// W as a matrix of bytes of which a copy takes 128 rows of `bytes` columns,
+// W as a matrix of bytes of which a copy takes `rows` rows of `bytes` columns,
 // pieces of 16 bytes exchanged as the kernel's place() has them. False if the
 // copy engine cannot address it so.
-bool map_weights(const Int4Args& a, int bytes, CUtensorMap* map) {
+bool map_weights(const Int4Args& a, int rows, int bytes, CUtensorMap* map) {
+  if (!aligned_to(a.w, 16) || (a.n_out > 1 && (a.ws % 16 != 0 || a.ws == 0))) return false;
   static const auto encode = [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult found;
@@ -623,7 +858,7 @@ bool map_weights(const Int4Args& a, int bytes, CUtensorMap* map) {
   const int64_t stride = a.n_out == 1 ? (row_bytes + 15) / 16 * 16 : a.ws;
   const cuuint64_t size[2] = {(cuuint64_t)row_bytes, (cuuint64_t)a.n_out};
   const cuuint64_t strides[1] = {(cuuint64_t)stride};
-  const cuuint32_t box[2] = {(cuuint32_t)bytes, kTileRows}, one[2] = {1, 1};
+  const cuuint32_t box[2] = {(cuuint32_t)bytes, (cuuint32_t)rows}, one[2] = {1, 1};
   const CUtensorMapSwizzle swizzle = bytes == 64   ? CU_TENSOR_MAP_SWIZZLE_64B
                                      : bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
                                                    : CU_TENSOR_MAP_SWIZZLE_NONE;
@@ -632,12 +867,30 @@ bool map_weights(const Int4Args& a, int bytes, CUtensorMap* map) {
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+spmv_status launch_after_image(const void* fn, dim3 grid, int threads, size_t smem, int cluster, Int4Args a,
+                               CUtensorMap& w_map, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  void* args[] = {&a, &w_map};
+  return status_of(cudaLaunchKernelExC(&cfg, fn, args));
+}
+
 template <typename T, int N, int GROUP>
 spmv_status launch_tiles(Int4Args a, cudaStream_t st) {
   using S = Step<N, GROUP>;
   CUtensorMap w_map{};
-  const bool aligned = aligned_to(a.w, 16) && (a.n_out == 1 || (a.ws % 16 == 0 && a.ws > 0)) &&
-                       map_weights(a, S::kColumns / 2, &w_map);
+  const bool aligned = map_weights(a, kTileRows, S::kColumns / 2, &w_map);
   const void* fn = aligned ? reinterpret_cast<const void*>(&int4_tiles<T, N, GROUP, true>)
                            : reinterpret_cast<const void*>(&int4_tiles<T, N, GROUP, false>);
   const size_t sums = (size_t)N * kTileRows * 4;
@@ -655,27 +908,40 @@ spmv_status launch_tiles(Int4Args a, cudaStream_t st) {
   const spmv_status laid_out = launch(int4_image<T, N, GROUP>, dim3((unsigned)((pieces + 255) / 256), (unsigned)groups),
                                       256, 0, st, a);
   if (laid_out != SPMV_OK) return laid_out;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(blocks * a.split), (unsigned)groups);
-  cfg.blockDim = dim3(kTileThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)a.split;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  void* args[] = {&a, &w_map};
-  return status_of(cudaLaunchKernelExC(&cfg, fn, args));
+  return launch_after_image(fn, dim3((unsigned)(blocks * a.split), (unsigned)groups), kTileThreads, smem, a.split, a, w_map,
+                            st);
 }
 
 template <typename T, int N>
 spmv_status tile_groups(const Int4Args& a, cudaStream_t st) {
   if (a.group_shift >= 7) return launch_tiles<T, N, 128>(a, st);
   return a.group_shift == 6 ? launch_tiles<T, N, 64>(a, st) : launch_tiles<T, N, 32>(a, st);
+}
+
+template <typename T, int MT, int NT, int SEG>
+spmv_status launch_few(const Int4Args& a, cudaStream_t st) {
+  constexpr int kRows = 16 * MT;
+  CUtensorMap w_map{};
+  const bool aligned = map_weights(a, kRows, kFewStep / 2, &w_map);
+  const void* fn = aligned ? reinterpret_cast<const void*>(&int4_few<T, MT, NT, SEG, true>)
+                           : reinterpret_cast<const void*>(&int4_few<T, MT, NT, SEG, false>);
+  const int64_t blocks = (a.n_out + kRows - 1ll) / kRows, steps = (a.n_in + kFewStep - 1ll) / kFewStep;
+  // warps that an SM's registers hold, over the CTAs that it gets
+  const int64_t per_sm = (blocks + 151) / 152, room = 65536 / 32 / few_registers(MT, NT) / per_sm;
+  const int warps = (int)(room < 4 ? 4 : room > kFewWarps ? kFewWarps : room);
+  const size_t ring = (size_t)warps * kFewDepth * kRows * kFewStep / 2, sums = (size_t)warps * 8 * NT * (kRows + 1) * 4;
+  const size_t smem = (ring > sums ? ring : sums) + 1024;
+  if (!allow_smem(fn, smem)) return SPMV_ERR_CUDA;
+  const spmv_status laid_out = launch(int4_image_few<T, SEG>, dim3((unsigned)((steps * 128 + 255) / 256), NT), 256, 0, st, a);
+  if (laid_out != SPMV_OK) return laid_out;
+  return launch_after_image(fn, dim3((unsigned)blocks), warps * 32, smem, 0, a, w_map, st);
+}
+
+template <typename T, int NT>
+spmv_status few_groups(const Int4Args& a, cudaStream_t st) {
+  const bool wide = a.n_out >= 2 * 152 * 32 && a.n_in >= 8192;
+  if (a.group_shift >= 7) return NT == 1 && wide ? launch_few<T, 2, 1, 128>(a, st) : launch_few<T, 1, NT, 128>(a, st);
+  return a.group_shift == 6 ? launch_few<T, 1, NT, 64>(a, st) : launch_few<T, 1, NT, 32>(a, st);
 }
 
 template <typename T>
@@ -685,8 +951,9 @@ spmv_status run_int4(const Int4Args& a, cudaStream_t st) {
     const int64_t blocks = ((int64_t)a.n_tokens * a.n_out + 255) / 256;
     return launch(int4_copy, dim3((unsigned)(blocks < 1216 ? blocks : 1216)), 256, 0, st, a);
   }
-  const int n = tokens_at_once(a.n_tokens);
-  return n == 16 ? tile_groups<T, 16>(a, st) : n == 32 ? tile_groups<T, 32>(a, st) : tile_groups<T, 64>(a, st);
+  if (a.n_tokens <= 8) return few_groups<T, 1>(a, st);
+  if (a.n_tokens <= 16) return few_groups<T, 2>(a, st);
+  return a.n_tokens <= 32 ? tile_groups<T, 32>(a, st) : tile_groups<T, 64>(a, st);
 }
 
 }  // namespace

@@ -22,8 +22,9 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kDistillThreads = 256;
-constexpr int kDistillAtOnce = 4;
+constexpr int kDistillAtOnce = 4, kGradAtOnce = 4;
 constexpr int kMaxCluster = 8;
+constexpr int kAskBytes = 32 * 1024;
 constexpr int kChunk = 128 * 1024;       // tokens whose marks a CTA holds at a time
 constexpr int kHash = 2 * SPMV_DISTILL_MAX_TOP;
 
@@ -53,6 +54,7 @@ struct DistillArgs {
 struct Teacher {
   int id[SPMV_DISTILL_MAX_TOP];
   float log_p[SPMV_DISTILL_MAX_TOP];
+  float z[SPMV_DISTILL_MAX_TOP];  // the row's own logits of the listed tokens
   MaxSum red[kDistillThreads / 32];
   float sums[kDistillThreads / 32];
   int any, repeats;
@@ -70,10 +72,20 @@ __device__ __forceinline__ float sum_cta(float v, float* s_red) {
   return t;
 }
 
-// Fill `t` from row i. False if nothing is listed there (or, where the
-// probabilities are those of the listed tokens alone, nothing above minus
-// infinity). *rest: the teacher's probability of what is not listed.
-__device__ __forceinline__ bool load_teacher(const DistillArgs& a, int64_t i, Teacher& t, float* rest) {
+// Ask L2 for the beginning of a CTA's share of a row, which it comes to only
+// after the teacher's.
+template <typename T>
+__device__ __forceinline__ void ask_row(const T* row, int n) {
+  if (threadIdx.x == 0) prefetch_bulk(row, min((int64_t)n * (int)sizeof(T), (int64_t)kAskBytes));
+}
+
+// Fill `t` from row i; of the listed tokens' logits those of [lo, lo + n). False
+// if nothing is listed there (or, where the probabilities are those of the
+// listed tokens alone, nothing above minus infinity). *rest: the teacher's
+// probability of what is not listed.
+template <typename T>
+__device__ __forceinline__ bool load_teacher(const DistillArgs& a, int64_t i, const T* row, int64_t lo, int64_t n,
+                                             Teacher& t, float* rest) {
   const int me = threadIdx.x;
   const int32_t* ids = a.tokens + i * a.tokens_stride;
   if (me == 0) t.any = t.repeats = 0;
@@ -82,10 +94,12 @@ __device__ __forceinline__ bool load_teacher(const DistillArgs& a, int64_t i, Te
   bool any = false;
   for (int j = me; j < a.top; j += kDistillThreads) {
     const int id = ids[j];
+    const float given = load_as_f32(a.top_logits, a.dtype_top, i * a.top_stride + j);
     const bool valid = (unsigned)id < (unsigned)a.vocab;
+    const float l = valid ? given : -INFINITY;
     t.id[j] = valid ? id : -1;
-    const float l = valid ? load_as_f32(a.top_logits, a.dtype_top, i * a.top_stride + j) : -INFINITY;
     t.log_p[j] = l;
+    t.z[j] = valid && id >= lo && id - lo < n ? to_f32(row[id]) : 0.f;
     any |= valid;
     if (valid) {
       x.raise(l, a.c);
@@ -115,14 +129,15 @@ __device__ __forceinline__ bool load_teacher(const DistillArgs& a, int64_t i, Te
 // threads, behind a barrier on entry and one on return). `table` has kHash
 // words.
 __device__ __forceinline__ void find_repeats(const DistillArgs& a, Teacher& t, int* table) {
-  for (int k = threadIdx.x; k < kHash; k += kDistillThreads) table[k] = -1;
+  int size = 64;  // (a power of two: at most half of the table is ever taken)
+  while (size < 2 * a.top) size *= 2;
+  for (int k = threadIdx.x; k < size; k += kDistillThreads) table[k] = -1;
   __syncthreads();
   for (int j = threadIdx.x; j < a.top; j += kDistillThreads) {
     const int id = t.id[j];
     if (id < 0) continue;
-    // (at most half of the table is ever taken)
     for (unsigned at = (unsigned)id * 2654435761u >> 16;; ++at) {
-      const int was = atomicCAS(&table[at % kHash], -1, id);
+      const int was = atomicCAS(&table[at & (size - 1)], -1, id);
       if (was == -1) break;
       if (was == id) {
         t.repeats = 1;
@@ -142,7 +157,7 @@ __device__ __forceinline__ bool is_first(const Teacher& t, int j) {
 }
 
 template <typename T, bool REST>
-__global__ void __launch_bounds__(kDistillThreads, 4) distill_rows(DistillArgs a) {
+__global__ void __launch_bounds__(kDistillThreads, sizeof(T) == 4 ? 4 : 5) distill_rows(DistillArgs a) {
   extern __shared__ uint32_t s_marks[];  // REST: a bit per token of a chunk
   __shared__ Teacher t;
   __shared__ MaxSum s_share;
@@ -151,17 +166,18 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_rows(DistillArgs a
   const int shares = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int64_t i = blockIdx.x / shares;
   const int me = threadIdx.x;
+  const T* row = static_cast<const T*>(a.logits) + i * a.stride;
+  const int64_t lo = (int64_t)rank * a.share, hi = min((int64_t)a.vocab, lo + a.share);
+  if (hi > lo) ask_row(row + lo, (int)(hi - lo));
   float rest;
-  if (!load_teacher(a, i, t, &rest)) {  // (the same in the whole cluster)
+  if (!load_teacher(a, i, row, 0, rank == 0 ? a.vocab : 0, t, &rest)) {  // (the same in the whole cluster)
     if (rank == 0 && me == 0) {
       a.loss[i] = 0.f;
       if (a.stats) a.stats[3 * i] = a.stats[3 * i + 1] = a.stats[3 * i + 2] = 0.f;
     }
     return;
   }
-  const T* row = static_cast<const T*>(a.logits) + i * a.stride;
-  const int64_t lo = (int64_t)rank * a.share, hi = min((int64_t)a.vocab, lo + a.share);
-  MaxSum x = MaxSum::none();
+  UnitSum sums = UnitSum::none();
   if constexpr (REST) {
     if (rank == 0) find_repeats(a, t, s_table);
     for (int64_t v0 = lo; v0 < hi; v0 += kChunk) {
@@ -179,24 +195,21 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_rows(DistillArgs a
       }
       __syncthreads();
       const uint8_t* marks = reinterpret_cast<const uint8_t*>(s_marks);
-      for_units<kDistillThreads, kDistillAtOnce>(row + v0, n, [&](int at, float (&v)[kUnit]) {
+      for_units<kDistillThreads, kDistillAtOnce>(row + v0, n, [&](int at, Unit& v) {
         // (the head's unit has its first token at bit 8 - head)
         uint32_t m = at == 0 && head > 0 ? (uint32_t)marks[0] >> (8 - head)
                                          : (uint32_t)marks[((at - head) >> 3) + 1];
-        if (m) {
-#pragma unroll
-          for (int k = 0; k < kUnit; ++k)
-            if (m >> k & 1) v[k] = -INFINITY;
-        }
-        x.add(v, a.c);
+        if (m) v.drop(m);
+        sums.add(v, a.c);
       });
       __syncthreads();
     }
   } else {
     for_units<kDistillThreads, kDistillAtOnce>(row + lo, (int)(hi > lo ? hi - lo : 0),
-                                               [&](int, float (&v)[kUnit]) { x.add(v, a.c); });
+                                               [&](int, Unit& v) { sums.add(v, a.c); });
   }
   __syncthreads();
+  MaxSum x = sums.sum();
   x = join_cta<kDistillThreads>(x, a.c, t.red);
   if (shares > 1) {
     if (me == 0) s_share = x;
@@ -213,7 +226,7 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_rows(DistillArgs a
     MaxSum y = MaxSum::none();
     for (int j = me; j < a.top; j += kDistillThreads)
       if (t.id[j] >= 0 && is_first(t, j)) {
-        const float z = to_f32(row[t.id[j]]);
+        const float z = t.z[j];
         y.raise(z, a.c);
         y.s += exp2_fast((z - y.m) * a.c);
         ++distinct;
@@ -228,7 +241,7 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_rows(DistillArgs a
   for (int j = me; j < a.top; j += kDistillThreads) {
     const float lp = t.log_p[j];
     if (t.id[j] < 0 || lp == -INFINITY) continue;
-    const float lq = (to_f32(row[t.id[j]]) - whole.m) / a.temperature - log_sum;
+    const float lq = (t.z[j] - whole.m) / a.temperature - log_sum;
     loss += expf(lp) * (lp - lq);
   }
   loss = sum_cta(loss, t.sums);
@@ -251,15 +264,15 @@ template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(kDistillThreads, 4) distill_grad_rows(DistillArgs a) {
   __shared__ Teacher t;
   __shared__ int s_table[kHash];
-  __shared__ float s_z[SPMV_DISTILL_MAX_TOP];
   const int64_t i = blockIdx.x / a.shares;
   const int rank = (int)(blockIdx.x - i * a.shares), me = threadIdx.x;
   const int64_t lo = (int64_t)rank * a.share;
   const int n = (int)min((int64_t)a.vocab - lo, (int64_t)a.share);
   const T* row = static_cast<const T*>(a.logits) + i * a.stride;
   T* out = static_cast<T*>(a.dlogits) + i * a.out_stride;
+  ask_row(row + lo, n);
   float rest;
-  const bool any = load_teacher(a, i, t, &rest);
+  const bool any = load_teacher(a, i, row, lo, n, t, &rest);
   float m = 0.f, scale = 0.f, inv = 0.f, g = 0.f;
   if (any) {
     m = a.stats[3 * i];
@@ -269,34 +282,31 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_grad_rows(DistillA
     scale = inv * g;
     if (a.log_sums && left != 0.f) scale *= 1.f - rest * sum / left;
     find_repeats(a, t, s_table);
-    for (int j = me; j < a.top; j += kDistillThreads) {
-      const int64_t at = (int64_t)t.id[j] - lo;
-      s_z[j] = at >= 0 && at < n ? to_f32(row[t.id[j]]) : 0.f;
-    }
-    __syncthreads();  // (the row may be overwritten from here on)
   }
   const auto gradient = [&](float z) { return any ? exp2_fast((z - m) * a.c) * scale : 0.f; };
   if constexpr (ALIGNED) {
     const Units u = units_of(row + lo, n);
     const T* body = row + lo + u.head;
     T* to = out + lo + u.head;
-    for (int k = me; k < u.units; k += kDistillAtOnce * kDistillThreads) {
-      Pack<T, kUnit> r[kDistillAtOnce];
+    const F2 nm = both(-m), cc = both(a.c), ss = both(scale);
+    for (int k = me; k < u.units; k += kGradAtOnce * kDistillThreads) {
+      Pack<T, kUnit> r[kGradAtOnce];
       if (any) {
 #pragma unroll
-        for (int h = 0; h < kDistillAtOnce; ++h)
+        for (int h = 0; h < kGradAtOnce; ++h)
           if (k + h * kDistillThreads < u.units)
             r[h] = load_pack<T, kUnit>(body + (int64_t)(k + h * kDistillThreads) * kUnit, true);
       }
 #pragma unroll
-      for (int h = 0; h < kDistillAtOnce; ++h)
+      for (int h = 0; h < kGradAtOnce; ++h)
         if (k + h * kDistillThreads < u.units) {
           Pack<T, kUnit> o;
+          Unit v{};
+          if (any) v = widen(r[h]);
 #pragma unroll
           for (int e = 0; e < kUnit / 2; ++e) {
-            float2 z = make_float2(0.f, 0.f);
-            if (any) z = pair_f32(r[h], e);
-            set_pair(o, e, make_float2(gradient(z.x), gradient(z.y)));
+            const float2 d = unpack2(mul2(add2(v.p[e], nm), cc));
+            set_pair(o, e, any ? unpack2(mul2(pack2(exp2_fast(d.x), exp2_fast(d.y)), ss)) : make_float2(0.f, 0.f));
           }
           store_pack<T, kUnit>(to + (int64_t)(k + h * kDistillThreads) * kUnit, o);
         }
@@ -316,7 +326,7 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_grad_rows(DistillA
     if (t.repeats)
       for (int k = j + 1; k < a.top; ++k)
         if (t.id[k] == t.id[j]) p += expf(t.log_p[k]);
-    out[t.id[j]] = from_f32<T>((exp2_fast((s_z[j] - m) * a.c) * inv - p) * g);
+    out[t.id[j]] = from_f32<T>((exp2_fast((t.z[j] - m) * a.c) * inv - p) * g);
   }
 }
 

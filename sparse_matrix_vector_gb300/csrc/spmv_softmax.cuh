@@ -5,6 +5,7 @@
 #include <cfloat>
 
 #include "spmv_device.cuh"
+#include "spmv_pairs.cuh"
 #include "spmv_types.cuh"
 
 namespace spmv {
@@ -37,6 +38,30 @@ __device__ __forceinline__ Units units_of(const T* row, int n) {
   return u;
 }
 
+// The larger of three, as one instruction (NaN is passed over, as fmaxf does).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// The 8 logits of a unit, in pairs.
+struct Unit {
+  F2 p[kUnit / 2];
+  __device__ __forceinline__ float largest() const {
+    const float2 a = unpack2(p[0]), b = unpack2(p[1]), c = unpack2(p[2]), d = unpack2(p[3]);
+    return fmaxf(max3(max3(a.x, a.y, b.x), b.y, c.x), max3(c.y, d.x, d.y));
+  }
+  // minus infinity where `marks` has a bit
+  __device__ __forceinline__ void drop(uint32_t marks) {
+#pragma unroll
+    for (int k = 0; k < kUnit / 2; ++k) {
+      const float2 v = unpack2(p[k]);
+      p[k] = pack2(marks >> (2 * k) & 1 ? -INFINITY : v.x, marks >> (2 * k + 1) & 1 ? -INFINITY : v.y);
+    }
+  }
+};
+
 // The largest of a set of logits and sum(exp2((logit - largest) * c)) over
 // it, joined as the set grows. Starting from the lowest finite number keeps
 // the differences of minus infinities defined: they count as 0. (The
@@ -55,49 +80,71 @@ struct MaxSum {
     raise(o.m, c);
     s += o.s * exp2_fast((o.m - m) * c);
   }
-  __device__ __forceinline__ void add(const float (&v)[kUnit], float c) {
-    float top = v[0];
-#pragma unroll
-    for (int k = 1; k < kUnit; ++k) top = fmaxf(top, v[k]);
-    raise(top, c);
-    float a = 0.f, b = 0.f;
-#pragma unroll
-    for (int k = 0; k < kUnit; k += 2) {
-      a += exp2_fast((v[k] - m) * c);
-      b += exp2_fast((v[k + 1] - m) * c);
+};
+
+// The same for the units of a thread, the sum in two parts.
+struct UnitSum {
+  float m;
+  F2 s;
+  static __device__ __forceinline__ UnitSum none() { return {-FLT_MAX, 0}; }
+  __device__ __forceinline__ void add(const Unit& u, float c) {
+    const float top = u.largest();
+    if (top > m) {
+      s = mul2(s, both(exp2_fast((m - top) * c)));
+      m = top;
     }
-    s += a + b;
+    const F2 nm = both(-m), cc = both(c);
+#pragma unroll
+    for (int k = 0; k < kUnit / 2; ++k) {
+      const float2 a = unpack2(mul2(add2(u.p[k], nm), cc));
+      s = add2(s, pack2(exp2_fast(a.x), exp2_fast(a.y)));
+    }
+  }
+  __device__ __forceinline__ MaxSum sum() const {
+    const float2 t = unpack2(s);
+    return {m, t.x + t.y};
   }
 };
 
 template <typename T>
-__device__ __forceinline__ void widen(const Pack<T, kUnit>& r, float (&v)[kUnit]) {
+__device__ __forceinline__ Unit widen(const Pack<T, kUnit>& r) {
+  Unit u;
 #pragma unroll
   for (int k = 0; k < kUnit / 2; ++k) {
     const float2 p = pair_f32(r, k);
-    v[2 * k] = p.x;
-    v[2 * k + 1] = p.y;
+    u.p[k] = pack2(p.x, p.y);
   }
+  return u;
 }
 
 // f(first token of a unit, its 8 logits) over tokens [0, n) of a row by the
 // THREADS threads of a CTA; places outside the row hold minus infinity (the
-// head and the tail are units of their own). kAtOnce loads of a thread are
+// head and the tail are units of their own). AT_ONCE loads of a thread are
 // under way together.
 template <int THREADS, int AT_ONCE, typename T, typename F>
 __device__ __forceinline__ void for_units(const T* row, int n, F&& f) {
   const Units u = units_of(row, n);
   const T* body = row + u.head;
-  for (int k = threadIdx.x; k < u.units; k += AT_ONCE * THREADS) {
+  int k = threadIdx.x;
+  for (; k + (AT_ONCE - 1) * THREADS < u.units; k += AT_ONCE * THREADS) {
     Pack<T, kUnit> r[AT_ONCE];
 #pragma unroll
-    for (int h = 0; h < AT_ONCE; ++h)
+    for (int h = 0; h < AT_ONCE; ++h) r[h] = load_pack<T, kUnit>(body + (int64_t)(k + h * THREADS) * kUnit, true);
+#pragma unroll
+    for (int h = 0; h < AT_ONCE; ++h) {
+      Unit v = widen(r[h]);
+      f(u.head + (k + h * THREADS) * kUnit, v);
+    }
+  }
+  {
+    Pack<T, kUnit> r[AT_ONCE - 1];
+#pragma unroll
+    for (int h = 0; h < AT_ONCE - 1; ++h)
       if (k + h * THREADS < u.units) r[h] = load_pack<T, kUnit>(body + (int64_t)(k + h * THREADS) * kUnit, true);
 #pragma unroll
-    for (int h = 0; h < AT_ONCE; ++h)
+    for (int h = 0; h < AT_ONCE - 1; ++h)
       if (k + h * THREADS < u.units) {
-        float v[kUnit];
-        widen(r[h], v);
+        Unit v = widen(r[h]);
         f(u.head + (k + h * THREADS) * kUnit, v);
       }
   }
@@ -106,33 +153,36 @@ __device__ __forceinline__ void for_units(const T* row, int n, F&& f) {
   const bool front = me == 0 && u.head > 0, back = me == 1 && u.tail > 0;
   if (front || back) {
     const int at = front ? 0 : u.head + u.units * kUnit, m = front ? u.head : u.tail;
-    float v[kUnit];
+    Unit v;
 #pragma unroll
-    for (int k = 0; k < kUnit; ++k) v[k] = k < m ? to_f32(row[at + k]) : -INFINITY;
+    for (int j = 0; j < kUnit / 2; ++j)
+      v.p[j] = pack2(2 * j < m ? to_f32(row[at + 2 * j]) : -INFINITY, 2 * j + 1 < m ? to_f32(row[at + 2 * j + 1]) : -INFINITY);
     f(at, v);
   }
+}
+
+// Joined over LANES neighbouring lanes, the same in all of them.
+template <int LANES>
+__device__ __forceinline__ MaxSum join_lanes(MaxSum x, float c) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) {
+    const MaxSum y{__shfl_xor_sync(0xffffffffu, x.m, o), __shfl_xor_sync(0xffffffffu, x.s, o)};
+    const float m = fmaxf(x.m, y.m);
+    x.s = x.s * exp2_fast((x.m - m) * c) + y.s * exp2_fast((y.m - m) * c);
+    x.m = m;
+  }
+  return x;
 }
 
 // Join a MaxSum over the CTA; the result is the same in all threads. Ends
 // with the shared memory free for reuse after the next barrier.
 template <int THREADS>
 __device__ __forceinline__ MaxSum join_cta(MaxSum x, float c, MaxSum* s_red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    MaxSum y;
-    y.m = __shfl_xor_sync(0xffffffffu, x.m, o);
-    y.s = __shfl_xor_sync(0xffffffffu, x.s, o);
-    // (both sides compute the same: the larger first)
-    const float m = fmaxf(x.m, y.m);
-    x.s = x.s * exp2_fast((x.m - m) * c) + y.s * exp2_fast((y.m - m) * c);
-    x.m = m;
-  }
+  constexpr int kWarps = THREADS / 32;
+  x = join_lanes<32>(x, c);
   if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = x;
   __syncthreads();
-  MaxSum t = s_red[0];
-#pragma unroll
-  for (int w = 1; w < THREADS / 32; ++w) t.join(s_red[w], c);
-  return t;
+  return join_lanes<kWarps>(s_red[threadIdx.x % kWarps], c);
 }
 
 }  // namespace

@@ -113,10 +113,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) verify_rows(VerifyArgs a) {
   if (t == 0.f) {
     float m = -INFINITY;
     int at = kNone;
-    for_units<kRowThreads, kRowAtOnce>(row, n, [&](int v0, float (&v)[kUnit]) {
-      float top = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < kUnit; ++k) top = fmaxf(top, v[k]);
+    for_units<kRowThreads, kRowAtOnce>(row, n, [&](int v0, Unit& v) {
+      const float top = fmaxf(v.largest(), -INFINITY);  // (of NaN alone: minus infinity)
       if (top > m || (top == m && top > -INFINITY && v0 < at)) m = top, at = v0;
     });
 #pragma unroll
@@ -139,18 +137,21 @@ __global__ void __launch_bounds__(kRowThreads, 4) verify_rows(VerifyArgs a) {
     }
   } else {
     const float c = scale_of(t);
-    MaxSum x = MaxSum::none();
-    for_units<kRowThreads, kRowAtOnce>(row, n, [&](int, float (&v)[kUnit]) { x.add(v, c); });
-    x = join_cta<kRowThreads>(x, c, s_red);
+    UnitSum sums = UnitSum::none();
+    for_units<kRowThreads, kRowAtOnce>(row, n, [&](int, Unit& v) { sums.add(v, c); });
+    MaxSum x = join_cta<kRowThreads>(sums.sum(), c, s_red);
     if (!(x.s == x.s) || x.m > FLT_MAX) {  // NaN or plus infinity in the share: again, cleaned
       __syncthreads();
-      x = MaxSum::none();
-      for_units<kRowThreads, kRowAtOnce>(row, n, [&](int, float (&v)[kUnit]) {
+      sums = UnitSum::none();
+      for_units<kRowThreads, kRowAtOnce>(row, n, [&](int, Unit& v) {
 #pragma unroll
-        for (int k = 0; k < kUnit; ++k) v[k] = cleaned(v[k]);
-        x.add(v, c);
+        for (int k = 0; k < kUnit / 2; ++k) {
+          const float2 p = unpack2(v.p[k]);
+          v.p[k] = pack2(cleaned(p.x), cleaned(p.y));
+        }
+        sums.add(v, c);
       });
-      x = join_cta<kRowThreads>(x, c, s_red);
+      x = join_cta<kRowThreads>(sums.sum(), c, s_red);
     }
     out.m = x.m;
     out.s = x.s;
@@ -169,12 +170,9 @@ __device__ __forceinline__ Part join_row(const VerifyArgs& a, int64_t slot, floa
     x.join({p.m, p.s}, c);
     if (p.m > m || (p.m == m && p.best < at)) m = p.m, at = p.best;
   }
+  x = join_lanes<32>(x, c);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const MaxSum y{__shfl_xor_sync(0xffffffffu, x.m, o), __shfl_xor_sync(0xffffffffu, x.s, o)};
-    const float to = fmaxf(x.m, y.m);
-    x.s = x.s * exp2_fast((x.m - to) * c) + y.s * exp2_fast((y.m - to) * c);
-    x.m = to;
     const float m2 = __shfl_xor_sync(0xffffffffu, m, o);
     const int at2 = __shfl_xor_sync(0xffffffffu, at, o);
     if (m2 > m || (m2 == m && at2 < at)) m = m2, at = at2;

@@ -264,8 +264,8 @@ template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(kDistillThreads, 4) distill_grad_rows(DistillArgs a) {
   __shared__ Teacher t;
   __shared__ int s_table[kHash];
-  const int64_t i = blockIdx.x / a.shares;
-  const int rank = (int)(blockIdx.x - i * a.shares), me = threadIdx.x;
+  const int64_t i = blockIdx.x;
+  const int rank = (int)blockIdx.y, me = threadIdx.x;
   const int64_t lo = (int64_t)rank * a.share;
   const int n = (int)min((int64_t)a.vocab - lo, (int64_t)a.share);
   const T* row = static_cast<const T*>(a.logits) + i * a.stride;
@@ -285,33 +285,38 @@ __global__ void __launch_bounds__(kDistillThreads, 4) distill_grad_rows(DistillA
   }
   const auto gradient = [&](float z) { return any ? exp2_fast((z - m) * a.c) * scale : 0.f; };
   if constexpr (ALIGNED) {
-    const Units u = units_of(row + lo, n);
-    const T* body = row + lo + u.head;
-    T* to = out + lo + u.head;
+    // (whole 16-byte vectors, so that a warp writes whole lines)
+    constexpr int kVec = 16 / (int)sizeof(T);
+    const int head = units_of(row + lo, n).head, vecs = (n - head) / kVec, tail = n - head - vecs * kVec;
+    const T* body = row + lo + head;
+    T* to = out + lo + head;
     const F2 nm = both(-m), cc = both(a.c), ss = both(scale);
-    for (int k = me; k < u.units; k += kGradAtOnce * kDistillThreads) {
-      Pack<T, kUnit> r[kGradAtOnce];
+    for (int k = me; k < vecs; k += kGradAtOnce * kDistillThreads) {
+      Pack<T, kVec> r[kGradAtOnce];
       if (any) {
 #pragma unroll
         for (int h = 0; h < kGradAtOnce; ++h)
-          if (k + h * kDistillThreads < u.units)
-            r[h] = load_pack<T, kUnit>(body + (int64_t)(k + h * kDistillThreads) * kUnit, true);
+          if (k + h * kDistillThreads < vecs)
+            r[h] = load_pack<T, kVec>(body + (int64_t)(k + h * kDistillThreads) * kVec, true);
       }
 #pragma unroll
       for (int h = 0; h < kGradAtOnce; ++h)
-        if (k + h * kDistillThreads < u.units) {
-          Pack<T, kUnit> o;
-          Unit v{};
-          if (any) v = widen(r[h]);
+        if (k + h * kDistillThreads < vecs) {
+          Pack<T, kVec> o;
 #pragma unroll
-          for (int e = 0; e < kUnit / 2; ++e) {
-            const float2 d = unpack2(mul2(add2(v.p[e], nm), cc));
-            set_pair(o, e, any ? unpack2(mul2(pack2(exp2_fast(d.x), exp2_fast(d.y)), ss)) : make_float2(0.f, 0.f));
+          for (int e = 0; e < kVec / 2; ++e) {
+            float2 g2 = make_float2(0.f, 0.f);
+            if (any) {
+              const float2 z = pair_f32(r[h], e);
+              const float2 d = unpack2(mul2(add2(pack2(z.x, z.y), nm), cc));
+              g2 = unpack2(mul2(pack2(exp2_fast(d.x), exp2_fast(d.y)), ss));
+            }
+            set_pair(o, e, g2);
           }
-          store_pack<T, kUnit>(to + (int64_t)(k + h * kDistillThreads) * kUnit, o);
+          store_pack<T, kVec>(to + (int64_t)(k + h * kDistillThreads) * kVec, o);
         }
     }
-    const int edge = me < u.head ? me : me >= 8 && me - 8 < u.tail ? u.head + u.units * kUnit + me - 8 : -1;
+    const int edge = me < head ? me : me >= 8 && me - 8 < tail ? head + vecs * kVec + me - 8 : -1;
     if (edge >= 0) out[lo + edge] = from_f32<T>(gradient(any ? to_f32(row[lo + edge]) : 0.f));
   } else {
     for (int k = me; k < n; k += kDistillThreads)
@@ -373,7 +378,11 @@ spmv_status launch_rows(DistillArgs a, cudaStream_t st) {
 
 template <typename T>
 spmv_status launch_grad(DistillArgs a, cudaStream_t st) {
-  a.shares = shares_of(a.n_rows, a.vocab, 1 << 16);
+  // CTAs of some 64 KB of a row, so that the last round of them is short (2048 x
+  // 128000 bf16: 162 us, with whole rows 175; 333 x 50257 fp32: 29, 31)
+  a.shares = shares_of(a.n_rows, a.vocab, 65535);
+  const int64_t parts = (int64_t)a.vocab * (int64_t)sizeof(T) / 65536;
+  if (a.shares < parts) a.shares = (int)(parts < 65535 ? parts : 65535);
   a.share = share_of(a.vocab, a.shares);
   a.shares = (int)(((int64_t)a.vocab + a.share - 1) / a.share);
   // rows whose 16-byte boundaries are at the same tokens in both matrices
@@ -382,7 +391,8 @@ spmv_status launch_grad(DistillArgs a, cudaStream_t st) {
   const void* fn = vec ? reinterpret_cast<const void*>(&distill_grad_rows<T, true>)
                        : reinterpret_cast<const void*>(&distill_grad_rows<T, false>);
   void* args[] = {&a};
-  return status_of(cudaLaunchKernel(fn, dim3((unsigned)(a.n_rows * a.shares)), dim3(kDistillThreads), args, 0, st));
+  return status_of(
+      cudaLaunchKernel(fn, dim3((unsigned)a.n_rows, (unsigned)a.shares), dim3(kDistillThreads), args, 0, st));
 }
 
 // What both directions check and fill in.

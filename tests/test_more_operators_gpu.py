@@ -295,6 +295,33 @@ def test_verify_counts(counts):
     verify_check(*verify_case(len(counts), counts, 513, error=0.1, temperature=torch.zeros(len(counts)), masked=0.5))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("point", [False, True])
+@pytest.mark.parametrize("counts", [[5, 0, 3, 7, 1, 2, 4, 6] * 24, [200, 0, 1, 0, 70, 16, 15, 17] * 2 + [1] * 900, [0] * 700 + [400] + [0] * 300])
+def test_verify_many_rows(counts, point, dtype):
+    """Calls in which rows behind a rejected draft are left out: short lists, a
+    few long ones among many short ones, nearly all empty."""
+    case = list(verify_case(len(counts), counts, 601, dtype=dtype, error=0.2, point=point, temperature="mixed"))
+    verify_check(*case)
+
+
+def test_verify_many_rows_next_to_the_border():
+    """As above with random numbers next to p(x) / q(x), and special rows."""
+    target, draft, tokens, offsets, au, su, _ = verify_case(28, [3] * 300, 700, error=0.3)
+    rows = torch.arange(900) + torch.arange(900) // 3
+    p = torch.softmax(target[rows].double(), 1).gather(1, tokens.long()[:, None])[:, 0]
+    q = torch.softmax(draft.double(), 1).gather(1, tokens.long()[:, None])[:, 0]
+    for step in (-1, 0, 1):
+        u = (p / q).float().clamp(max=1 - 2.0 ** -24)
+        u = (u.view(torch.int32) + step).view(torch.float32).clamp(min=0, max=1 - 2.0 ** -24)
+        verify_check(target, draft, tokens, offsets, u, su, None)
+    target[5::40] = -INF
+    draft[7::30] = -INF
+    target[11::50, ::3] = float("nan")
+    tokens[::17] = 700
+    verify_check(target, draft, tokens, offsets, au, su, None)
+
+
 @pytest.mark.parametrize("t_at,d_at", [((1003, 0), (1003, 0)), ((1001, 1), (1008, 3)), ((1200, 5), (1001, 7)), ((0, 2), (0, 4))])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_verify_rows_anywhere(t_at, d_at, dtype):

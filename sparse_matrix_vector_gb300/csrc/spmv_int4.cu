@@ -38,7 +38,7 @@ namespace cg = cooperative_groups;
 constexpr int kTileRows = 128;
 constexpr int kRowWarps = 4;
 constexpr int kTileThreads = (kRowWarps + 1) * 32;
-constexpr int kMaxXStages = 6, kMaxDepth = 16;
+constexpr int kMaxXStages = 4, kMaxDepth = 12;
 constexpr int kMaxSplit = 8;
 constexpr int kTensorColumns = 128;  // of tensor memory: a quarter of an SM's
 
@@ -252,9 +252,9 @@ struct Step {
   static constexpr int kColumns = GROUP * kGroups;
   static constexpr int kLine = kColumns >= 64 ? 128 : 64;  // bytes of a row of the B operand: its swizzle
   static constexpr int kXBytes = N * kColumns * 2;
-  static constexpr int kPerSm = N == 64 ? 3 : 3;           // CTAs
-  static constexpr int kXStages = N == 16 ? 6 : N == 32 ? 4 : 3;
-  static constexpr int kPre = 2;             // pieces unpacked before the last step's instructions are done
+  static constexpr int kPerSm = 3;  // CTAs
+  static constexpr int kXStages = N == 32 ? 4 : 3;
+  static constexpr int kPre = 2;    // pieces unpacked before the last step's instructions are done
   static constexpr int kDepth = (N == 64 ? 3 : 4) * (128 / kColumns);  // steps of weights in shared memory
   static constexpr size_t kRings = kXStages * (size_t)kXBytes + kDepth * (size_t)kTileRows * kColumns / 2;
   // Where 16-byte piece c of token n stands in a step's B operand: parts of

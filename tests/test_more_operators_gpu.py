@@ -637,3 +637,150 @@ def test_distill_no_rows():
     ids, t = torch.empty(0, 3, dtype=torch.int32, device=DEV), torch.empty(0, 3, device=DEV)
     S.spmv_distill(z, ids, t, torch.empty(0, device=DEV))
     S.spmv_distill_backward(torch.empty(0, device=DEV), z, ids, t, torch.empty(0, 3, device=DEV), z)
+
+
+# --------------------------------------------------- streams, graphs, far rows
+
+def test_int4_captured_and_replayed():
+    """Calls of every kernel in one graph, replayed on new inputs in the same place."""
+    cases = [int4_case(40 + k, t, 1000, 260, g, x="bf16", scales="bf16", base="f32") + (g,)
+             for k, (t, g) in enumerate([(1, 128), (12, 64), (30, 32), (64, 128), (70, 256)])]
+    dev = [[v.to(DEV) for v in c[:5]] for c in cases]
+    outs = [torch.empty(c[0].shape[0], 260, device=DEV) for c in cases]
+
+    def run():
+        for d, o, c in zip(dev, outs, cases):
+            S.spmv_int4_run(d[0], d[1], d[2], o, c[5], zeros=d[3], base=d[4])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for seed in (0, 100):
+        for k, (d, c) in enumerate(zip(dev, cases)):
+            x = randn(gen(seed + k), *c[0].shape, dtype="bf16")
+            d[0].copy_(x)
+            outs[k].fill_(float("nan"))
+        graph.replay()
+        for k, (o, c) in enumerate(zip(outs, cases)):
+            x = randn(gen(seed + k), *c[0].shape, dtype="bf16")
+            ref, slack = int4_ref(x, *c[1:])
+            close(o, ref, U * ref.abs() + slack)
+
+
+def test_int4_on_many_streams():
+    """Calls of different kernels at work at the same time, each right."""
+    cases = [int4_case(50 + k, t, 3000, 2000, 128, zeros=False) for k, t in enumerate([1, 16, 32, 64] * 3)]
+    dev = [[None if v is None else v.to(DEV) for v in c] for c in cases]
+    outs = [torch.empty(c[0].shape[0], 2000, device=DEV) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for d, o, st in zip(dev, outs, streams):
+            S.spmv_int4_run(d[0], d[1], d[2], o, 128, stream=st)
+    torch.cuda.synchronize()
+    for o, c in zip(outs, cases):
+        ref, slack = int4_ref(*c, 128)
+        close(o, ref, U * ref.abs() + slack)
+
+
+def test_verify_and_distill_on_a_given_stream():
+    """A stream that is not the current one, while the current one is busy."""
+    case = verify_case(61, [3, 1, 0, 4], 20000, temperature="mixed")
+    st = torch.cuda.Stream()
+    busy = torch.randn(4096, 4096, device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        busy = busy @ busy * 1e-3
+    verify_check(*case, stream=st)
+    z, ids, t, sums = distill_case(62, 6, 5000, 9, rest=True)
+    dev = [v.to(DEV) for v in (z, ids, t, sums)]
+    loss, stats, out = torch.empty(6, device=DEV), torch.empty(6, 3, device=DEV), torch.empty_like(dev[0])
+    torch.cuda.synchronize()
+    for _ in range(20):
+        busy = busy @ busy * 1e-3
+    S.spmv_distill(dev[0], dev[1], dev[2], loss, log_sums=dev[3], stats=stats, stream=st)
+    S.spmv_distill_backward(torch.ones(6, device=DEV), dev[0], dev[1], dev[2], stats, out, log_sums=dev[3], stream=st)
+    st.synchronize()
+    loss_ref, dl, _, _, grad, dg = distill_ref(z, ids, t, sums, 1.0)
+    close(loss, loss_ref, dl + 1e-37)
+
+
+def test_distill_captured_and_replayed():
+    """Both directions in one graph; new logits in the same place at each replay."""
+    z, ids, t, sums = distill_case(63, 5, 3001, 20, rest=True)
+    dev = [v.to(DEV) for v in (z, ids, t, sums)]
+    loss, stats, out = torch.empty(5, device=DEV), torch.empty(5, 3, device=DEV), torch.empty_like(dev[0])
+    ones = torch.ones(1, device=DEV).expand(5)
+
+    def run():
+        S.spmv_distill(dev[0], dev[1], dev[2], loss, log_sums=dev[3], stats=stats)
+        S.spmv_distill_backward(ones, dev[0], dev[1], dev[2], stats, out, log_sums=dev[3])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for seed in (64, 65):
+        new = randn(gen(seed), 5, 3001, std=2.0)
+        dev[0].copy_(new)
+        graph.replay()
+        loss_ref, dl, _, _, grad, dg = distill_ref(new, ids, t, sums, 1.0)
+        close(loss, loss_ref, dl + 1e-37)
+        close(out, grad, U * grad.abs() + dg + 1e-37)
+
+
+def far_rows(t, fill):
+    """The rows of t on the GPU, 2^31 + 16 elements apart."""
+    stride = 2 ** 31 + 16
+    buf = torch.empty((t.shape[0] - 1) * stride + t.shape[1], dtype=t.dtype, device=DEV)
+    view = buf.as_strided(t.shape, (stride, 1))
+    view.copy_(t) if fill else None
+    return view
+
+
+def test_rows_far_apart():
+    """Offsets past 32 bits in every matrix."""
+    z, ids, t, sums = distill_case(66, 3, 2000, 9, "bf16", rest=True)
+    zd = far_rows(z, True)
+    loss, stats = torch.empty(3, device=DEV), torch.empty(3, 3, device=DEV)
+    dev = [v.to(DEV) for v in (ids, t, sums)]
+    S.spmv_distill(zd, dev[0], dev[1], loss, log_sums=dev[2], stats=stats)
+    S.spmv_distill_backward(torch.ones(3, device=DEV), zd, dev[0], dev[1], stats, zd, log_sums=dev[2])
+    loss_ref, dl, _, _, grad, dg = distill_ref(z, ids, t, sums, 1.0)
+    close(loss, loss_ref, dl + 1e-37)
+    close(zd, grad, 2.0 ** -8 * grad.abs() + 1.01 * dg + TINY[torch.bfloat16])
+    del zd
+    case = verify_case(67, [1], 3000, dtype="bf16")
+    got, acc = torch.empty(2, dtype=torch.int32, device=DEV), torch.empty(1, dtype=torch.int32, device=DEV)
+    S.spmv_verify_drafts(far_rows(case[0], True), case[1].to(DEV), case[2].to(DEV), torch.tensor(case[3]).to(DEV), case[4].to(DEV), case[5].to(DEV),
+                         got, acc)
+    out, accepted = verify_ref(*case)
+    assert acc.tolist() == accepted and got.tolist() == [out[0], out[1]]
+    for n in (3, 20, 40):
+        x, w, sc, zp, base = int4_case(68, n, 200, 3, 64, base="f32")
+        y = torch.empty(n, 3, device=DEV)
+        S.spmv_int4_run(to_dev(x), far_rows(w, True), sc.to(DEV), y, 64, zeros=zp.to(DEV), base=base.to(DEV))
+        ref, slack = int4_ref(x, w, sc, zp, base, 64)
+        close(y, ref, U * ref.abs() + slack)
+    x, w, sc, zp, _ = int4_case(69, 2, 200, 130, 64)
+    y = far_rows(torch.empty(2, 130), False)
+    S.spmv_int4_run(far_rows(x, True), w.to(DEV), sc.to(DEV), y, 64, zeros=zp.to(DEV))
+    ref, slack = int4_ref(x, w, sc, zp, None, 64)
+    close(y, ref, U * ref.abs() + slack)
+
+
+def test_int4_one_row_and_one_matrix_for_all():
+    """Expanded inputs: one token for all, one row of base for all, one row of weights for all."""
+    for t in (5, 40):
+        x, w, sc, zp, base = int4_case(70, t, 700, 150, 128, base="f32")
+        y = torch.empty(t, 150, device=DEV)
+        S.spmv_int4_run(x[:1].to(DEV).expand(t, -1), w[:1].to(DEV).expand(150, -1), sc.to(DEV), y, 128, zeros=zp.to(DEV), base=base[:1].to(DEV).expand(t, -1))
+        ref, slack = int4_ref(x[:1].expand(t, -1), w[:1].expand(150, -1), sc, zp, base[:1].expand(t, -1), 128)
+        close(y, ref, U * ref.abs() + slack)

@@ -687,9 +687,12 @@ int64_t spmv_int4_workspace(int32_t n_tokens, int32_t n_in);
  * stride). q - zero is exact, and a group's products are summed in fp32
  * before they are scaled. A token's result does not depend on the other
  * tokens' values, but it may differ in the order of its sums with n_tokens.
- * Errors: INVALID_ARG (sizes, null or misaligned
- * pointers, strides, overlaps), UNSUPPORTED (types, group), TOO_LARGE (more
- * than 2^18 tokens, n_in or n_out above 2^30), CUDA. */
+ * workspace: 16-byte aligned device memory of at least spmv_int4_workspace
+ * bytes; no initialisation, no meaning afterwards; calls that may run at the
+ * same time have one each.
+ * Errors: INVALID_ARG (sizes, null or misaligned pointers, strides, overlaps,
+ * workspace), UNSUPPORTED (types, group), TOO_LARGE (more than 2^18 tokens,
+ * n_in or n_out above 2^30), CUDA. */
 spmv_status spmv_int4_run(int32_t n_tokens, int32_t n_in, int32_t n_out, int32_t group,
                           spmv_dtype dtype, const void* x, int64_t x_stride,
                           const uint8_t* weights, int64_t weights_stride, const void* scales,
@@ -729,9 +732,10 @@ int64_t spmv_verify_workspace(int32_t n_requests, int32_t n_drafts, int32_t voca
  * largest counts as 0. A drafted token outside [0, vocab) is not accepted. A
  * request whose row to draw from has nothing above minus infinity gets -1.
  * Decisions are made in 64 bits' worth where fp32's roundings could change
- * them (relative errors of some 2^-38 remain).
+ * them (relative errors of some 2^-34 remain).
  * workspace: 16-byte aligned device memory of at least spmv_verify_workspace
- * bytes; no initialisation, no meaning afterwards.
+ * bytes; no initialisation, no meaning afterwards; calls that may run at the
+ * same time have one each.
  * Errors: INVALID_ARG (sizes, null or misaligned pointers, strides, overlaps,
  * workspace), TOO_LARGE (vocab above 2^31 - 4097, too many rows), CUDA. */
 spmv_status spmv_verify_drafts(int32_t n_requests, int32_t n_drafts, int32_t vocab,

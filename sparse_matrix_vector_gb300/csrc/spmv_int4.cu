@@ -6,15 +6,25 @@
 // fifth-generation tensor cores, and a group's sums are scaled in fp32 once
 // they are whole, so nothing is rounded before the products' own sums.
 //
-// 128 rows of W and up to 64 tokens to a CTA, up to four CTAs to an SM. The
-// rows' step of columns is the instruction's A operand and lives in tensor
-// memory: a thread unpacks its row's columns into its own lane there, so that
-// 16-bit weights never pass through shared memory. x is the B operand in
-// shared memory, and the sums of a group come back from tensor memory to be
-// scaled into registers. Four warps unpack and add up, one thread issues the
-// instructions and x's copies; there is one buffer of each, and what a CTA
-// waits for, the SM's others work meanwhile. The columns are split over a
-// cluster's CTAs, whose sums meet in distributed shared memory.
+// Up to 16 tokens (int4_few): warps at ranges of the columns of their own, 16
+// or 32 rows at a time, on the warp-level instruction, whose A operand a thread
+// unpacks straight into its registers. What a warp waits for is only its own
+// copies. 12288 x 12288, groups of 128, fp16, one token: 23 us, 0.49 of the
+// copy rate; the launch of x's image and the first loads take 6 of them, the
+// rest is instructions (unpacking is 1.3 of them to a weight's half byte).
+//
+// More tokens (int4_tiles): 128 rows of W and 32 or 64 tokens to a CTA, three
+// CTAs to an SM. The rows' step of columns is the instruction's A operand and
+// lives in tensor memory: a thread unpacks its row's columns into its own lane
+// there, so that 16-bit weights never pass through shared memory. x is the B
+// operand in shared memory, and the sums of a group come back from tensor
+// memory to be scaled into registers. Four warps unpack and add up, one issues
+// the instructions and the copies; there is one buffer of the operand and what
+// a CTA waits for, the SM's others work meanwhile. The columns are split over a
+// cluster's CTAs, whose sums meet in distributed shared memory. 64 tokens of
+// 12288 x 12288: 39 us, 500 TFLOP/s; bound by the four warps' unpacking and
+// adding up between the instructions (two warps to a row's columns 47 us, with
+// a second buffer and two CTAs to an SM 44).
 //
 // The order of the columns within a sum is free as long as both operands agree
 // on it: masks take the pairs (0, 4), (1, 5), (2, 6), (3, 7) out of a word of 8
@@ -361,12 +371,13 @@ int4_tiles(const Int4Args a, const __grid_constant__ CUtensorMap w_map) {
     const auto ask = [&](int s, uint32_t (&sc)[kGroups], uint32_t (&z)[kGroups]) {
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        const int k = min(((begin + s) * kColumns + g * GROUP) >> a.group_shift, a.groups - 1);
+        const int col = (begin + s) * kColumns + g * GROUP, k = col >> a.group_shift;
+        sc[g] = 0, z[g] = 8;
+        if (col >= a.n_in) continue;  // (an infinite scale would make a NaN of no products)
         if (a.scales_f32)
           sc[g] = __ldg(reinterpret_cast<const uint32_t*>(scales) + k);
         else
           sc[g] = __ldg(reinterpret_cast<const unsigned short*>(scales) + k);
-        z[g] = 8u;
         if (a.zeros) z[g] = __ldg(zeros + k);
       }
     };
@@ -586,7 +597,7 @@ int4_tiles(const Int4Args a, const __grid_constant__ CUtensorMap w_map) {
 // columns). A warp waits for nothing but its own copies, which is worth more
 // here than the tensor cores' rate.
 constexpr int kFewStep = 128;  // columns that a warp takes at a time
-constexpr int kFewDepth = 4;
+constexpr int kFewDepth = 2;
 constexpr int kFewWarps = 16;  // of a CTA, at most
 
 // Column of the step that word w of lane q's share begins with, 8 columns each:
@@ -612,21 +623,21 @@ __global__ void __launch_bounds__(256) int4_image_few(Int4Args a) {
                  __byte_perm(v.y, v.w, 0x7632));
 }
 
-template <typename T>
-__device__ __forceinline__ void mma_few(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+// d = or += (16 rows of W) x (8 tokens) over 16 columns
+template <typename T, bool ADD>
+__device__ __forceinline__ void mma_few(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
+  const float c0 = ADD ? d[0] : 0.f, c1 = ADD ? d[1] : 0.f, c2 = ADD ? d[2] : 0.f, c3 = ADD ? d[3] : 0.f;
   if constexpr (std::is_same<T, __half>::value)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
   else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 // Registers of a thread, and so warps of an SM.
@@ -679,7 +690,7 @@ int4_few(const Int4Args a, const __grid_constant__ CUtensorMap w_map) {
       }
     }
   };
-  // (aligned rows: kFewDepth steps ahead, unaligned ones two less)
+  // (unaligned rows one step less: they are loaded a step before they are stored)
   constexpr int kAhead = ALIGNED ? kFewDepth : kFewDepth - 1;
 #pragma unroll
   for (int k = 0; k < kAhead; ++k) fetch(k);
@@ -691,6 +702,11 @@ int4_few(const Int4Args a, const __grid_constant__ CUtensorMap w_map) {
   const uint8_t* zeros = a.zeros + (a.zeros ? scale_row : 0);
   uint32_t scale_bits = 0, zero_bits = 8;
   const auto ask = [&](int col) {
+    // (segments behind the last column: 0, as an infinite scale would make a NaN of no products)
+    if (SEG < kFewStep && col >= a.n_in) {
+      scale_bits = 0;
+      return;
+    }
     const int k = min(col >> a.group_shift, a.groups - 1);
     if (a.scales_f32)
       scale_bits = __ldg(reinterpret_cast<const uint32_t*>(scales) + k);
@@ -704,9 +720,14 @@ int4_few(const Int4Args a, const __grid_constant__ CUtensorMap w_map) {
     return __uint_as_float(bits << 16);
   };
   ask(begin * kFewStep);
-  // x, a step ahead
-  const uint4* image = a.image + (int64_t)begin * 128 + lane;
+  // x, a step ahead; in the place of tokens that there are not, the first of
+  // the eight, whose loads cost nothing more. (Plain loads: the kernel before
+  // this one writes the image while this one has begun.)
   const int64_t image_pitch = (int64_t)steps * 128;
+  const uint4* image[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    image[n] = a.image + n * image_pitch + (int64_t)begin * 128 + (8 * n + g < a.n_tokens ? lane : q);
   uint4 x[NT][4];
   pdl_wait();  // (the image)
 #pragma unroll
@@ -714,9 +735,12 @@ int4_few(const Int4Args a, const __grid_constant__ CUtensorMap w_map) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       x[n][k] = make_uint4(0, 0, 0, 0);
-      if (begin < end) x[n][k] = __ldg(image + n * image_pitch + 32 * k);
+      if (begin < end) x[n][k] = image[n][32 * k];
     }
 
+  Unpack<T> un[2 * MT];
+#pragma unroll
+  for (int r = 0; r < 2 * MT; ++r) un[r].set(8);
   float acc[MT][NT][4] = {};
   for (int i = 0; i < end - begin; ++i) {
     const int step = begin + i;
@@ -745,26 +769,25 @@ int4_few(const Int4Args a, const __grid_constant__ CUtensorMap w_map) {
       }
     }
     if constexpr (ALIGNED) {
-      __syncwarp();  // (all lanes have read the stage)
+      // (all lanes have read the stage, before the copy engine writes there)
+      fence_proxy_async_smem();
+      __syncwarp();
       fetch(i + kAhead);
     }
-    image += 128;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) image[n] += 128;
 #pragma unroll
     for (int seg = 0; seg < kSegs; ++seg) {
       const float mine = scale_from(scale_bits);
       float scale[2 * MT];
-      Unpack<T> un[2 * MT];
 #pragma unroll
-      for (int r = 0; r < 2 * MT; ++r) {
-        scale[r] = __shfl_sync(0xffffffffu, mine, g + 8 * r);
-        un[r].set(8);
-      }
+      for (int r = 0; r < 2 * MT; ++r) scale[r] = __shfl_sync(0xffffffffu, mine, g + 8 * r);
       if (a.zeros) {
 #pragma unroll
         for (int r = 0; r < 2 * MT; ++r) un[r].set(__shfl_sync(0xffffffffu, zero_bits, g + 8 * r) & 15u);
       }
-      ask(step * kFewStep + (seg + 1) * SEG);  // (behind the last column: the last group's again)
-      float part[MT][NT][4] = {};
+      ask(step * kFewStep + (seg + 1) * SEG);
+      float part[MT][NT][4];
 #pragma unroll
       for (int k = seg * kWords; k < (seg + 1) * kWords; ++k) {
 #pragma unroll
@@ -774,13 +797,16 @@ int4_few(const Int4Args a, const __grid_constant__ CUtensorMap w_map) {
           un[2 * m + 1].run(w[2 * m + 1][k], hi);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma_few<T>(part[m][n], lo[0], hi[0], lo[1], hi[1], x[n][k].x, x[n][k].y);
-            mma_few<T>(part[m][n], lo[2], hi[2], lo[3], hi[3], x[n][k].z, x[n][k].w);
+            if (k == seg * kWords)
+              mma_few<T, false>(part[m][n], lo[0], hi[0], lo[1], hi[1], x[n][k].x, x[n][k].y);
+            else
+              mma_few<T, true>(part[m][n], lo[0], hi[0], lo[1], hi[1], x[n][k].x, x[n][k].y);
+            mma_few<T, true>(part[m][n], lo[2], hi[2], lo[3], hi[3], x[n][k].z, x[n][k].w);
           }
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          if (step + 1 < end) x[n][k] = __ldg(image + n * image_pitch + 32 * k);
+          if (step + 1 < end) x[n][k] = image[n][32 * k];
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m)
@@ -835,11 +861,14 @@ int64_t image_bytes(int64_t n_tokens, int64_t n_in) {
   return (n_tokens + n - 1) / n * n * ((n_in + 127) / 128 * 128) * 2;
 }
 
+// W's rows at 16-byte boundaries, which the copy engine asks for.
+bool rows_at_16(const Int4Args& a) { return aligned_to(a.w, 16) && (a.n_out == 1 || (a.ws != 0 && a.ws % 16 == 0)); }
+
 // W as a matrix of bytes of which a copy takes `rows` rows of `bytes` columns,
 // pieces of 16 bytes exchanged as the kernel's place() has them. False if the
 // copy engine cannot address it so.
 bool map_weights(const Int4Args& a, int rows, int bytes, CUtensorMap* map) {
-  if (!aligned_to(a.w, 16) || (a.n_out > 1 && (a.ws % 16 != 0 || a.ws == 0))) return false;
+  if (!rows_at_16(a)) return false;
   static const auto encode = [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult found;
@@ -918,15 +947,18 @@ spmv_status tile_groups(const Int4Args& a, cudaStream_t st) {
   return a.group_shift == 6 ? launch_tiles<T, N, 64>(a, st) : launch_tiles<T, N, 32>(a, st);
 }
 
-template <typename T, int MT, int NT, int SEG>
+template <typename T, int MT, int NT, int SEG, bool ALIGNED>
 spmv_status launch_few(const Int4Args& a, cudaStream_t st) {
   constexpr int kRows = 16 * MT;
   CUtensorMap w_map{};
-  const bool aligned = map_weights(a, kRows, kFewStep / 2, &w_map);
-  const void* fn = aligned ? reinterpret_cast<const void*>(&int4_few<T, MT, NT, SEG, true>)
-                           : reinterpret_cast<const void*>(&int4_few<T, MT, NT, SEG, false>);
+  if constexpr (ALIGNED) {
+    if (!map_weights(a, kRows, kFewStep / 2, &w_map)) return launch_few<T, 1, NT, SEG, false>(a, st);
+  }
+  const void* fn = reinterpret_cast<const void*>(&int4_few<T, MT, NT, SEG, ALIGNED>);
   const int64_t blocks = (a.n_out + kRows - 1ll) / kRows, steps = (a.n_in + kFewStep - 1ll) / kFewStep;
-  // warps that an SM's registers hold, over the CTAs that it gets
+  // Warps that an SM's registers hold, over the CTAs that it gets. (Eight to a
+  // CTA instead: 12288 x 12288, one token, 24.0 for 22.9 us, 4096 -> 12288, 6
+  // tokens, 16.5 for 14.5.)
   const int64_t per_sm = (blocks + 151) / 152, room = 65536 / 32 / few_registers(MT, NT) / per_sm;
   const int warps = (int)(room < 4 ? 4 : room > kFewWarps ? kFewWarps : room);
   const size_t ring = (size_t)warps * kFewDepth * kRows * kFewStep / 2, sums = (size_t)warps * 8 * NT * (kRows + 1) * 4;
@@ -937,11 +969,25 @@ spmv_status launch_few(const Int4Args& a, cudaStream_t st) {
   return launch_after_image(fn, dim3((unsigned)blocks), warps * 32, smem, 0, a, w_map, st);
 }
 
+// Rows of a CTA. 32 give x's loads twice the work (us of 12288 x 12288 with
+// groups of 128: one token 22.6 where 16 rows take 25.1, 12 tokens 27.9 and
+// 34.1; 4096 x 4096 5.8 and 6.6). Shorter groups of up to 8 tokens have more
+// to do for each row and want the warps that 16 rows' registers leave (12288 x
+// 12288 with groups of 64 29.5, with 32 rows 35.7), but where the SMs get one
+// CTA each (4096 x 4096 7.3 and 6.4). Unaligned rows pass through registers,
+// with 16 rows (8193 -> 28672, one token 53 and 81, 16 tokens 74 and 98; 5003 ->
+// 12289, one token 20 and 39; only 16 tokens there 33 and 31).
 template <typename T, int NT>
 spmv_status few_groups(const Int4Args& a, cudaStream_t st) {
-  const bool wide = a.n_out >= 2 * 152 * 32 && a.n_in >= 8192;
-  if (a.group_shift >= 7) return NT == 1 && wide ? launch_few<T, 2, 1, 128>(a, st) : launch_few<T, 1, NT, 128>(a, st);
-  return a.group_shift == 6 ? launch_few<T, 1, NT, 64>(a, st) : launch_few<T, 1, NT, 32>(a, st);
+  const int seg = a.group_shift >= 7 ? 128 : 1 << a.group_shift;
+  if (!rows_at_16(a))
+    return seg == 128  ? launch_few<T, 1, NT, 128, false>(a, st)
+           : seg == 64 ? launch_few<T, 1, NT, 64, false>(a, st)
+                       : launch_few<T, 1, NT, 32, false>(a, st);
+  if (seg == 128) return launch_few<T, 2, NT, 128, true>(a, st);
+  if (NT == 2 || a.n_out <= 152 * 32)
+    return seg == 64 ? launch_few<T, 2, NT, 64, true>(a, st) : launch_few<T, 2, NT, 32, true>(a, st);
+  return seg == 64 ? launch_few<T, 1, 1, 64, true>(a, st) : launch_few<T, 1, 1, 32, true>(a, st);
 }
 
 template <typename T>
@@ -951,6 +997,8 @@ spmv_status run_int4(const Int4Args& a, cudaStream_t st) {
     const int64_t blocks = ((int64_t)a.n_tokens * a.n_out + 255) / 256;
     return launch(int4_copy, dim3((unsigned)(blocks < 1216 ? blocks : 1216)), 256, 0, st, a);
   }
+  // (12288 x 12288 with groups of 128, us: 8 tokens 23, in tiles 28; 16 tokens
+  // 28 both, but 4096 x 4096 8 and 12; 32 tokens 30, in tiles of 64 tokens 32.)
   if (a.n_tokens <= 8) return few_groups<T, 1>(a, st);
   if (a.n_tokens <= 16) return few_groups<T, 2>(a, st);
   return a.n_tokens <= 32 ? tile_groups<T, 32>(a, st) : tile_groups<T, 64>(a, st);
@@ -999,9 +1047,15 @@ extern "C" spmv_status spmv_int4_run(int32_t n_tokens, int32_t n_in, int32_t n_o
   if ((!in_place && meets_y(base, n_tokens, n_out, base_stride, ysz)) || meets_y(x, n_tokens, n_in, x_stride, 2) ||
       meets_y(weights, n_out, row_bytes, weights_stride, 1) ||
       meets_y(scales, 1, n_out * groups, n_out * groups, op_dtype_size(scales_dtype)) ||
-      meets_y(zeros, 1, n_out * groups, n_out * groups, 1) || meets_y(workspace, 1, need, need, 1) ||
-      spans_overlap(x, n_tokens, n_in, x_stride, 2, workspace, 1, need, need, 1) ||
-      spans_overlap(weights, n_out, row_bytes, weights_stride, 1, workspace, 1, need, need, 1))
+      meets_y(zeros, 1, n_out * groups, n_out * groups, 1) || meets_y(workspace, 1, need, need, 1))
+    return SPMV_ERR_INVALID_ARG;
+  const auto meets_workspace = [&](const void* p, int64_t rows, int64_t cols, int64_t stride, int64_t size) {
+    return spans_overlap(p, rows, cols, stride, size, workspace, 1, need, need, 1);
+  };
+  if (meets_workspace(x, n_tokens, n_in, x_stride, 2) || meets_workspace(weights, n_out, row_bytes, weights_stride, 1) ||
+      meets_workspace(scales, 1, n_out * groups, n_out * groups, op_dtype_size(scales_dtype)) ||
+      meets_workspace(zeros, 1, n_out * groups, n_out * groups, 1) ||
+      meets_workspace(base, n_tokens, n_out, base_stride, ysz))
     return SPMV_ERR_INVALID_ARG;
   Int4Args a{};
   a.n_tokens = n_tokens, a.n_in = n_in, a.n_out = n_out, a.groups = (int)groups;

@@ -296,7 +296,7 @@ inline int resident_clusters(const void* fn, int cluster, int block, size_t smem
     int n;
   };
   static std::mutex mu;
-  static Known known[512];
+  static Known known[128];
   static int count = 0;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
@@ -321,7 +321,7 @@ inline int resident_clusters(const void* fn, int cluster, int block, size_t smem
     cudaGetLastError();
     return 0;
   }
-  if (count < 512) known[count++] = Known{fn, dev, cluster, smem, n};
+  if (count < 128) known[count++] = Known{fn, dev, cluster, smem, n};
   return n;
 }
 

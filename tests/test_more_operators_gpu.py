@@ -164,6 +164,37 @@ def test_int4_special_values(t):
     close(out, ref, U * ref.abs() + slack)
 
 
+@pytest.mark.parametrize("t", [1, 12, 24, 40])
+@pytest.mark.parametrize("n_in,group", [(300, 32), (300, 64), (300, 128), (300, 300), (130, 64), (257, 32)])
+def test_int4_infinite_scale(t, n_in, group):
+    # the last group's scale is infinite: infinity of products of one sign, whatever is behind the last column
+    w = torch.randint(9, 16, (40, n_in), dtype=torch.uint8)
+    w = torch.cat([w, w.new_zeros(40, 1)], 1)[:, :(n_in + 1) // 2 * 2]
+    w = (w[:, ::2] | w[:, 1::2] << 4).contiguous()
+    x = torch.rand(t, n_in).add(0.5).half()
+    scales = torch.ones(40, -(-n_in // group))
+    scales[::2, -1] = math.inf
+    y = torch.zeros(t, 40, device=DEV)
+    S.spmv_int4_run(to_dev(x), to_dev(w), to_dev(scales), y, group)
+    y = y.cpu()
+    assert bool((y[:, ::2] == math.inf).all()) and bool(y[:, 1::2].isfinite().all())
+
+
+@pytest.mark.parametrize("t", [1, 8, 16, 32, 64])
+@pytest.mark.parametrize("n_in,n_out,group", [(12288, 33, 32), (12288, 5000, 32), (4096, 12288, 64), (8192, 9000, 128)])
+def test_int4_many_times(t, n_in, n_out, group):
+    """The same bits in every one of many calls, one right after the other."""
+    xs, w, sc, z, _ = int4_case(7, t, n_in, n_out, group, x="bf16", scales="bf16")
+    args = [to_dev(v) for v in (xs, w, sc)]
+    z, outs = to_dev(z), torch.empty(60, t, n_out, dtype=torch.bfloat16, device=DEV)
+    for k in range(60):
+        S.spmv_int4_run(*args, outs[k], group, zeros=z)
+    assert bool((outs == outs[0]).all())
+    at = torch.randperm(n_out, generator=gen(8))[:40]
+    ref, slack = int4_ref(xs, w[at], sc[at], z.cpu()[at], None, group)
+    close(outs[0][:, at.to(DEV)], ref, ROUND[torch.bfloat16] * ref.abs() + slack)
+
+
 @pytest.mark.parametrize("t", [1, 6, 16, 64, 200])
 def test_int4_repeats_and_tokens_apart(t):
     """The same bits again, and a token's bits whatever the others hold."""

@@ -30,7 +30,7 @@ def int4(lib, **kw):
     (dict(sc=None), INVALID), (dict(y=None), INVALID), (dict(x=X + 1), INVALID), (dict(sc=SC + 2), INVALID), (dict(b=B + 2), INVALID),
     (dict(y=Y + 2), INVALID), (dict(xs=-1), INVALID), (dict(ws=-1), INVALID), (dict(ys=31), INVALID), (dict(ys=0), INVALID),
     (dict(bs=-1), INVALID), (dict(b=Y + 64), INVALID), (dict(b=Y, bs=64), INVALID), (dict(x=Y), INVALID), (dict(w=Y + 16), INVALID),
-    (dict(sc=Y), INVALID), (dict(z=Y + 3), INVALID),
+    (dict(sc=Y), INVALID), (dict(z=Y + 3), INVALID), (dict(wk=SC), INVALID), (dict(wk=Z), INVALID), (dict(wk=B), INVALID),
     (dict(dt=F32), UNSUPPORTED), (dict(yt=BF16), UNSUPPORTED), (dict(st=BF16), UNSUPPORTED), (dict(dt=BF16, yt=F16), UNSUPPORTED),
     (dict(g=16), UNSUPPORTED), (dict(g=48), UNSUPPORTED), (dict(g=255), UNSUPPORTED), (dict(g=96), UNSUPPORTED),
     (dict(t=2 ** 18 + 1), TOO_LARGE), (dict(i=2 ** 30 + 1, g=HUGE), TOO_LARGE), (dict(o=2 ** 30 + 1), TOO_LARGE),

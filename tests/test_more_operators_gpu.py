@@ -815,3 +815,28 @@ def test_int4_one_row_and_one_matrix_for_all():
         S.spmv_int4_run(x[:1].to(DEV).expand(t, -1), w[:1].to(DEV).expand(150, -1), sc.to(DEV), y, 128, zeros=zp.to(DEV), base=base[:1].to(DEV).expand(t, -1))
         ref, slack = int4_ref(x[:1].expand(t, -1), w[:1].expand(150, -1), sc, zp, base[:1].expand(t, -1), 128)
         close(y, ref, U * ref.abs() + slack)
+
+
+def test_the_readmes_calls_run():
+    """The calls of these operators as README.md prints them."""
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code, = [c for c in re.findall(r"```python\n(.*?)```", open(os.path.join(root, "README.md")).read(), re.S) if "spmv_distill" in c]
+    w, sc, zp = int4_case(80, 3, 256, 40, 128)[1:4]
+    x = randn(gen(81), 3, 256, dtype="f16")
+    logits, teacher = randn(gen(82), 5, 90), randn(gen(83), 5, 8)
+    names = dict(S=S, x=x.to(DEV), weights=w.to(DEV), scales=sc.to(DEV), zeros=zp.to(DEV), y=torch.empty(3, 40, device=DEV),
+                 target_logits=randn(gen(84), 5, 90).to(DEV), draft_logits=randn(gen(85), 3, 90).to(DEV),
+                 draft_tokens=torch.tensor([3, 5, 7], dtype=torch.int32, device=DEV), offsets=torch.tensor([0, 2, 3], device=DEV),
+                 accept_uniforms=torch.rand(3, generator=gen(86)).to(DEV), sample_uniforms=torch.rand(2, generator=gen(87)).to(DEV),
+                 tokens=torch.empty(5, dtype=torch.int32, device=DEV), accepted=torch.empty(2, dtype=torch.int32, device=DEV),
+                 temperature=torch.tensor([1.0, 0.7], device=DEV), logits=logits.to(DEV), top_logits=teacher.to(DEV),
+                 top_tokens=torch.arange(0, 80, 10, dtype=torch.int32).expand(5, -1).contiguous().to(DEV),
+                 loss=torch.empty(5, device=DEV), stats=torch.empty(5, 3, device=DEV), dloss=torch.ones(5, device=DEV))
+    exec(code, names)
+    ref, slack = int4_ref(x, w, sc, zp, None, 128)
+    close(names["y"], ref, U * ref.abs() + slack)
+    assert bool((names["accepted"] >= 0).all()) and bool((names["loss"] > 0).all())
+    # q - p of a row sums to nothing (dloss / temperature = 1/2, 90 terms of at most 1 rounded a few times)
+    assert bool((names["logits"].double().sum(1).abs() <= 90 * 16 * U).all())

@@ -9,9 +9,10 @@
 // Up to 16 tokens (int4_few): warps at ranges of the columns of their own, 16
 // or 32 rows at a time, on the warp-level instruction, whose A operand a thread
 // unpacks straight into its registers. What a warp waits for is only its own
-// copies. 12288 x 12288, groups of 128, fp16, one token: 23 us, 0.49 of the
+// copies. 12288 x 12288, groups of 128, fp16, one token: 24 us, 0.48 of the
 // copy rate; the launch of x's image and the first loads take 6 of them, the
-// rest is instructions (unpacking is 1.3 of them to a weight's half byte).
+// rest is instructions (2.2 to a weight, half of them unpacking, at half of the
+// issue slots).
 //
 // More tokens (int4_tiles): 128 rows of W and 32 or 64 tokens to a CTA, three
 // CTAs to an SM. The rows' step of columns is the instruction's A operand and
@@ -597,7 +598,7 @@ int4_tiles(const Int4Args a, const __grid_constant__ CUtensorMap w_map) {
 // columns). A warp waits for nothing but its own copies, which is worth more
 // here than the tensor cores' rate.
 constexpr int kFewStep = 128;  // columns that a warp takes at a time
-constexpr int kFewDepth = 2;
+constexpr int kFewDepth = 2;  // of a warp's stages: shared memory taken from L1 costs more than it gives (4: 25.3 us, 8: 31)
 constexpr int kFewWarps = 16;  // of a CTA, at most
 
 // Column of the step that word w of lane q's share begins with, 8 columns each:

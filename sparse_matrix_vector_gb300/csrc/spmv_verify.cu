@@ -17,12 +17,12 @@
 // is too near to call in fp32 (within kNear).
 //
 // 64 requests of up to 7 drafts, 128000 fp32 logits: 88 us, of which 38 are
-// verify_rows (512 rows, those of greedy requests' drafts not read), 8 the tests, some 32 the sums (bound by
-// instructions: a pair's exponential is some 20 packed ones) and 10 the last
-// CTA's search. One request of 5 drafts, 32000: 18 us, a chain of short steps.
-// (Sums in FP64 187 us; a cluster in place of the CTA that is done last 96;
-// rows behind a rejected draft left out make a chain of verify_rows, 47 to 56
-// for its 38.)
+// verify_rows (512 rows, those of greedy requests' drafts not read), 8 the
+// tests, some 32 the sums (bound by instructions: a pair's exponential is some
+// 20 packed ones) and 10 the last CTA's search. One request of 5 drafts, 32000:
+// 18 us, a chain of short steps. (Sums in FP64 187 us; a cluster in place of
+// the CTA that is done last 96; rows behind a rejected draft left out make a
+// chain of verify_rows, 47 to 56 for its 38.)
 #include <climits>
 
 #include "spmv_device.cuh"

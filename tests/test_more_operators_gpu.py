@@ -181,7 +181,7 @@ def test_int4_infinite_scale(t, n_in, group):
 
 
 @pytest.mark.parametrize("t", [1, 8, 16, 32, 64])
-@pytest.mark.parametrize("n_in,n_out,group", [(12288, 33, 32), (12288, 5000, 32), (4096, 12288, 64), (8192, 9000, 128)])
+@pytest.mark.parametrize("n_in,n_out,group", [(12288, 33, 32), (12288, 5000, 32), (4096, 12288, 64), (8192, 9000, 128), (5003, 4100, 32), (4097, 6000, 128)])
 def test_int4_many_times(t, n_in, n_out, group):
     """The same bits in every one of many calls, one right after the other."""
     xs, w, sc, z, _ = int4_case(7, t, n_in, n_out, group, x="bf16", scales="bf16")
